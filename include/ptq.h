@@ -404,6 +404,144 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_embed_ptq1(
     const int8_t* signs, void* out, int64_t M, int64_t V, int64_t H,
     ptq_dtype out_dtype, ptq_stream_t stream);
 
+/* ---- attention over a paged key-value cache.  What a decoder layer runs
+ * between its QKV projection and its output projection, so that the layers
+ * around ptq_rotate_matmul and ptq_ffn stay on the device.  The source pages
+ * name the cache formats and an attention kernel but define neither; the
+ * definitions are the ones written here.
+ *
+ * Query head h (of q_heads) reads kv head h / (q_heads / kv_heads).  For a
+ * query q over keys k_j and values v_j, j in the visible set J:
+ *     s_j = softmax_scale * sum_d q_d k_jd
+ *     lse = ln sum_j e^(s_j)
+ *     out = sum_j e^(s_j - lse) v_j
+ * With J empty out is 0 and lse is -infinity.  Scores, the softmax's maximum
+ * and sum, and the output's sums are fp32; a bf16 output is rounded once. */
+
+/* PTQ_KV_BF16: rows are rounded to nearest-even bf16.
+ * PTQ_KV_I8: a row x (one token, one head) is stored as
+ *     s = max_d |x_d| / 127   (fp32, rounded to nearest)
+ *     c_d = x_d / s rounded to the nearest integer, ties to even
+ * and stands for c_d s.  A row of zeros has s = 0; a row that holds a
+ * non-finite value has s = NaN and c = 0, and reads back as NaN. */
+typedef enum ptq_kv_type { PTQ_KV_BF16 = 0, PTQ_KV_I8 = 1 } ptq_kv_type;
+
+/* A paged cache; all memory is the caller's, on the device.
+ *   k, v     pages x kv_heads x page_tokens x head_dim, bf16 or int8,
+ *            16-byte aligned
+ *   k_scale, v_scale  pages x kv_heads x page_tokens fp32 (PTQ_KV_I8; NULL
+ *            for PTQ_KV_BF16), 4-byte aligned
+ * The token in place p of page g has slot g * page_tokens + p.  head_dim is
+ * 64, 128 or 256 (others: PTQ_ERR_UNSUPPORTED); page_tokens is any size >= 1;
+ * pages * page_tokens < 2^31.  Contents of slots that hold no token are never
+ * used and may be anything. */
+typedef struct ptq_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int64_t page_tokens;
+  int64_t kv_heads;
+  int64_t head_dim;
+  ptq_kv_type type;
+} ptq_kv_cache;
+
+/* ptq_kv_write -- stores T tokens' keys and values into the cache.
+ *   k, v   T x kv_heads x head_dim of dtype (PTQ_F32 or PTQ_BF16); the heads
+ *          of a token are contiguous, tokens are k_stride / v_stride elements
+ *          apart (so they may be columns of a fused projection's output);
+ *          16-byte aligned, strides a multiple of 16 bytes
+ *   slots  T int32 slots (device); a slot outside the cache skips its token.
+ *          Two tokens with one slot leave either token's values there.
+ * cache: a HOST struct, read during the call only.  T = 0 is a no-op.
+ * Errors: PTQ_ERR_NULL, PTQ_ERR_SHAPE, PTQ_ERR_ALIGN, PTQ_ERR_VALUE (dtype or
+ * type), PTQ_ERR_UNSUPPORTED (head_dim), PTQ_ERR_CUDA. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_kv_write(const ptq_kv_cache* cache, const void* k,
+                                              const void* v, int64_t k_stride,
+                                              int64_t v_stride, const int32_t* slots, int64_t T,
+                                              ptq_dtype dtype, ptq_stream_t stream);
+
+/* ptq_kv_read -- the inverse gather: the values that T slots of the cache
+ * stand for, into k and v (layout as for ptq_kv_write).  A slot outside the
+ * cache gives rows of quiet NaN (nothing is read for it).  A prefix read this
+ * way is what ptq_attn_prefill takes as the keys before a prompt's next
+ * chunk.  An int8 row's value c s is rounded to fp32 and, for PTQ_BF16, to
+ * bf16.  Errors as ptq_kv_write. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_kv_read(const ptq_kv_cache* cache, const int32_t* slots,
+                                             int64_t T, void* k, void* v, int64_t k_stride,
+                                             int64_t v_stride, ptq_dtype dtype,
+                                             ptq_stream_t stream);
+
+/* ptq_attn_decode_workspace_bytes -- scratch of ptq_attn_decode; 0 when the
+ * arguments are invalid. */
+PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t kv_heads,
+                                               int64_t head_dim, ptq_dtype dtype);
+
+/* ptq_attn_decode -- attention of one new token of each of B sequences over
+ * its cached tokens (the new one among them, once ptq_kv_write has stored
+ * it).
+ *   q      B x q_heads x head_dim of dtype, sequences q_stride elements
+ *          apart; 16-byte aligned, stride a multiple of 16 bytes
+ *   table  B x table_width int32 page numbers: token j of sequence b is in
+ *          place j % page_tokens of page table[b, j / page_tokens].  Entries
+ *          past a sequence's length are not used.  An entry in use that is
+ *          outside the cache makes that sequence's outputs NaN (nothing is
+ *          read for it).
+ *   lens   B int32 token counts; below 0 counts as 0, above table_width *
+ *          page_tokens as that
+ *   out    B x q_heads x head_dim of dtype, contiguous
+ *   lse    B x q_heads fp32, or NULL
+ * softmax_scale is finite and positive.  With PTQ_F32 the arithmetic keeps
+ * fp32 accuracy over both cache types.  The work is split over the lengths by
+ * a rule on the lengths alone, and the parts are joined in a fixed order:
+ * results are bitwise reproducible.  B = 0 is a no-op.
+ * workspace: device scratch of ptq_attn_decode_workspace_bytes(...) bytes,
+ * 16-byte aligned, caller-owned, any initial contents.  Calls whose kernels
+ * overlap on the GPU need separate workspaces.
+ * Errors: PTQ_ERR_NULL, PTQ_ERR_SHAPE (q_heads not a multiple of kv_heads
+ * among them), PTQ_ERR_ALIGN, PTQ_ERR_VALUE (dtype, type or softmax_scale),
+ * PTQ_ERR_UNSUPPORTED (head_dim), PTQ_ERR_WORKSPACE, PTQ_ERR_CUDA. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_attn_decode(
+    const void* q, int64_t q_stride, const ptq_kv_cache* cache, const int32_t* table,
+    int64_t table_width, const int32_t* lens, void* out, float* lse, int64_t B, int64_t q_heads,
+    float softmax_scale, ptq_dtype dtype, void* workspace, size_t workspace_bytes,
+    ptq_stream_t stream);
+
+/* ptq_attn_prefill_workspace_bytes -- scratch of ptq_attn_prefill; 0 when it
+ * needs none or the arguments are invalid. */
+PTQ_API size_t ptq_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk,
+                                                int64_t q_heads, int64_t kv_heads,
+                                                int64_t head_dim, ptq_dtype dtype);
+
+/* ptq_attn_prefill -- attention of B sequences' queries, packed one after the
+ * other, over their packed keys and values.
+ *   q      Tq x q_heads x head_dim, k and v Tk x kv_heads x head_dim, bf16,
+ *          tokens q_stride / k_stride / v_stride elements apart; 16-byte
+ *          aligned, strides a multiple of 16 bytes
+ *   cu_q, cu_k  B + 1 int32 offsets (device), not decreasing: sequence b has
+ *          the queries cu_q[b] .. cu_q[b+1] - 1 and the keys cu_k[b] ..
+ *          cu_k[b+1] - 1.  Offsets outside [0, Tq] and [0, Tk] count as the
+ *          nearer bound.
+ *   out    Tq x q_heads x head_dim bf16, contiguous; lse: Tq x q_heads fp32,
+ *          or NULL.  Rows of no sequence are not written.
+ * flags: 0, every query sees all keys of its sequence; PTQ_ATTN_CAUSAL, query
+ * i of nq sees the keys j <= i + nk - nq (the last query sees all, and with
+ * nk < nq the first ones see none).  A key or value a query does not see has
+ * no effect on it, NaN and infinities included.
+ * dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED (the fp32
+ * route serves decode).  Probabilities enter the second product as bf16.
+ * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op.  workspace
+ * as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
+ * Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for unknown flags. */
+#define PTQ_ATTN_CAUSAL 1u
+PTQ_API PTQ_NODISCARD ptq_status ptq_attn_prefill(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse, int64_t B,
+    int64_t Tq, int64_t Tk, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+    float softmax_scale, unsigned flags, ptq_dtype dtype, void* workspace,
+    size_t workspace_bytes, ptq_stream_t stream);
+
 /* ptq_route -- the kernel ptq_matmul would run for (M, dtype) when K/128 is
  * even: writes its name to *kernel_name (static storage) and returns PTQ_OK,
  * or returns PTQ_ERR_UNSUPPORTED / PTQ_ERR_VALUE.  Host only. */

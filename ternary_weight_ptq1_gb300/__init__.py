@@ -33,6 +33,8 @@ EXPORTS = ("ptq1_pack", "ptq1_unpack", "ptq_fwht", "ptq_matmul_workspace_bytes",
            "ptq_ffn", "ptq_ffn_noalloc", "ptq_ffn_stack_workspace_bytes", "ptq_ffn_stack",
            "ptq_ffn_stack_ex", "ptq_ffn_stack_route", "ptq2_pack", "ptq2_unpack",
            "ptq_matmul_pq2_workspace_bytes", "ptq_matmul_pq2", "ptq_embed", "ptq_embed_ptq1",
+           "ptq_kv_write", "ptq_kv_read", "ptq_attn_decode_workspace_bytes", "ptq_attn_decode",
+           "ptq_attn_prefill_workspace_bytes", "ptq_attn_prefill",
            "ptq_route", "ptq_gemv_plan", "ptq_matmul_bf16_accumulator", "ptq_matmul_f32_peel",
            "ptq_selftest_timeout",
            "ptq_selftest_grid_timeout",
@@ -97,6 +99,19 @@ def load(path: str | None = None):
     L.ptq_matmul_pq2.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, ctypes.c_size_t, _P]
     L.ptq_embed.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P]
     L.ptq_embed_ptq1.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P]
+    S = ctypes.c_size_t
+    L.ptq_kv_write.argtypes = [_P, _P, _P, _I64, _I64, _P, _I64, _I32, _P]
+    L.ptq_kv_read.argtypes = [_P, _P, _I64, _P, _P, _I64, _I64, _I32, _P]
+    L.ptq_attn_decode_workspace_bytes.argtypes = [_I64] * 4 + [_I32]
+    L.ptq_attn_decode_workspace_bytes.restype = S
+    L.ptq_attn_decode.argtypes = ([_P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_float,
+                                   _I32, _P, S, _P])
+    L.ptq_attn_prefill_workspace_bytes.argtypes = [_I64] * 6 + [_I32]
+    L.ptq_attn_prefill_workspace_bytes.restype = S
+    L.ptq_attn_prefill.argtypes = ([_P] * 3 + [_I64] * 3 + [_P] * 4 + [_I64] * 6 +
+                                   [ctypes.c_float, ctypes.c_uint, _I32, _P, S, _P])
+    for name in ("ptq_kv_write", "ptq_kv_read", "ptq_attn_decode", "ptq_attn_prefill"):
+        getattr(L, name).restype = _I32
     L.ptq_route.argtypes = [_I64, _I32, ctypes.POINTER(ctypes.c_char_p)]
     L.ptq_gemv_plan.argtypes = [_I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_int32)]
     L.ptq_matmul_f32_peel.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _P]
@@ -475,6 +490,195 @@ def embed_ptq1(wq, scales, ids, signs, out_dtype=None, out=None, stream=None):
                                  _dev(y, out_dtype, "out"), M, V, H, dt, _stream(stream)),
            "ptq_embed_ptq1")
     return y
+
+
+# ---- attention over a paged key-value cache --------------------------------------
+
+PTQ_KV_BF16 = 0
+PTQ_KV_I8 = 1
+PTQ_ATTN_CAUSAL = 1
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """ptq_kv_cache (include/ptq.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] +
+                [(n, ctypes.c_int64) for n in ("pages", "page_tokens", "kv_heads", "head_dim")] +
+                [("type", ctypes.c_int)])
+
+
+class KVCache:
+    """A paged key-value cache over the caller's tensors: k and v are pages x
+    kv_heads x page_tokens x head_dim, bfloat16, or int8 with k_scale and
+    v_scale (pages x kv_heads x page_tokens float32).  Keeps the tensors alive;
+    copies nothing."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be pages x kv_heads x page_tokens x head_dim, of one type")
+        if k.dtype == torch.int8:
+            for s in (k_scale, v_scale):
+                if s is None or s.shape != k.shape[:3]:
+                    raise ValueError("an int8 cache needs k_scale and v_scale, one scale for each row")
+            self.type = PTQ_KV_I8
+            scales = (_dev(k_scale, torch.float32, "k_scale"), _dev(v_scale, torch.float32, "v_scale"))
+        elif k.dtype == torch.bfloat16:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bfloat16 cache takes no scales")
+            self.type = PTQ_KV_BF16
+            scales = (None, None)
+        else:
+            raise TypeError(f"a cache is bfloat16 or int8, got {k.dtype}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self._struct = _KvCacheStruct(_dev(k, None, "k"), _dev(v, None, "v"), *scales, self.pages,
+                                      self.page_tokens, self.kv_heads, self.head_dim, self.type)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_tokens, head_dim, dtype, device="cuda"):
+        """A new cache of torch.bfloat16 or torch.int8 rows."""
+        import torch
+
+        shape = (pages, kv_heads, page_tokens, head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.int8:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.float32, device=device)
+                           for _ in range(2)))
+
+
+def _heads(t, name, dtype, shape=None):
+    """The address and token stride of a tokens x heads x head_dim tensor whose
+    heads are contiguous within a token (tokens may be any stride apart)."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'tokens x heads x head_dim' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    n, h, d = t.shape
+    s = t.stride()
+    if (s[2] != 1 and d != 1) or (s[1] != d and h != 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (s[0] if n > 1 else h * d)
+
+
+def kv_write(cache, k, v, slots, stream=None):
+    """Stores the rows k and v (tokens x kv_heads x head_dim, float32 or
+    bfloat16; heads contiguous, tokens any stride apart) at the int32 `slots`
+    of the cache, rounded or quantised as the cache is; a slot outside the
+    cache skips its token."""
+    import torch
+
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    kp, ks = _heads(k, "k", k.dtype, shape)
+    vp, vs = _heads(v, "v", k.dtype, shape)
+    _check(load().ptq_kv_write(cache._ref, kp, vp, ks, vs, _dev(slots, torch.int32, "slots"), shape[0],
+                               _act_dtype(k), _stream(stream, k.device.index)), "ptq_kv_write")
+
+
+def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
+    """The values that the int32 `slots` of the cache stand for, as (k, v) of
+    float32 or bfloat16 (default); into the given k and v (as for kv_write)
+    or new tensors.  A slot outside the cache gives NaN."""
+    import torch
+
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    kp, ks = _heads(k, "k", dtype, shape)
+    vp, vs = _heads(v, "v", dtype, shape)
+    _check(load().ptq_kv_read(cache._ref, _dev(slots, torch.int32, "slots"), shape[0], kp, vp, ks, vs,
+                              _act_dtype(k), _stream(stream, k.device.index)), "ptq_kv_read")
+    return k, v
+
+
+def attn_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, dtype: int) -> int:
+    return int(load().ptq_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, dtype))
+
+
+def _attn_buffers(q, out, lse, workspace, need):
+    """The output, and the addresses of out, lse and the workspace."""
+    import torch
+
+    B, Hq, D = q.shape
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse is not None and lse.shape != (B, Hq):
+        raise ValueError(f"lse must be {(B, Hq)}, got {tuple(lse.shape)}")
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return (out, _dev(out, q.dtype, "out"), None if lse is None else _dev(lse, torch.float32, "lse"),
+            None if workspace is None else _dev(workspace, None, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), workspace)
+
+
+def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token of each sequence over its cached tokens.
+    q: sequences x q_heads x head_dim, float32 or bfloat16; table: sequences x
+    pages int32 page numbers; lens: int32 token counts.  `scale` defaults to
+    head_dim ** -0.5; `lse` (sequences x q_heads float32), when given, receives
+    the log-sum-exp of the scaled scores.  out and the workspace are allocated
+    by PyTorch when not given."""
+    import torch
+
+    dt = _act_dtype(q)
+    qp, qs = _heads(q, "q", q.dtype)
+    B, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q has head_dim {D}, the cache {cache.head_dim}")
+    if table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+        raise ValueError("table must be sequences x pages, lens one count for each sequence")
+    need = 0 if workspace is not None else attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt)
+    out, op, lp, wp, wb, keep = _attn_buffers(q, out, lse, workspace, need)
+    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, torch.int32, "table"), table.shape[1],
+                                  _dev(lens, torch.int32, "lens"), op, lp, B, Hq,
+                                  D ** -0.5 if scale is None else scale, dt, wp, wb,
+                                  _stream(stream, q.device.index)), "ptq_attn_decode")
+    return out
+
+
+def attn_prefill_workspace_bytes(B: int, Tq: int, Tk: int, q_heads: int, kv_heads: int, head_dim: int,
+                                 dtype: int) -> int:
+    return int(load().ptq_attn_prefill_workspace_bytes(B, Tq, Tk, q_heads, kv_heads, head_dim, dtype))
+
+
+def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=None, workspace=None,
+                 stream=None):
+    """Attention of packed prompts.  q: queries x q_heads x head_dim, k and v:
+    keys x kv_heads x head_dim, bfloat16; cu_q and cu_k: int32 offsets of the
+    sequences in them (one more than there are sequences).  With `causal`
+    query i of nq sees the keys j <= i + nk - nq of its sequence.  scale, out,
+    lse and workspace as for attn_decode."""
+    import torch
+
+    dt = _act_dtype(q)
+    qp, qs = _heads(q, "q", q.dtype)
+    kp, ks = _heads(k, "k", q.dtype)
+    vp, vs = _heads(v, "v", q.dtype, k.shape)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D:
+        raise ValueError(f"q has head_dim {D}, k {Dk}")
+    B = cu_q.numel() - 1
+    if B < 0 or cu_q.shape != cu_k.shape:
+        raise ValueError("cu_q and cu_k must have one offset more than there are sequences")
+    need = 0 if workspace is not None else attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt)
+    out, op, lp, wp, wb, keep = _attn_buffers(q, out, lse, workspace, need)
+    _check(load().ptq_attn_prefill(qp, kp, vp, qs, ks, vs, _dev(cu_q, torch.int32, "cu_q"),
+                                   _dev(cu_k, torch.int32, "cu_k"), op, lp, B, Tq, Tk, Hq, Hkv, D,
+                                   D ** -0.5 if scale is None else scale,
+                                   PTQ_ATTN_CAUSAL if causal else 0, dt, wp, wb,
+                                   _stream(stream, q.device.index)), "ptq_attn_prefill")
+    return out
 
 
 def route(M: int, dtype: int) -> str:

@@ -14,6 +14,8 @@ namespace ptq {
 
 static thread_local char t_msg[512];
 
+void clear_error() { t_msg[0] = 0; }
+
 ptq_status fail(ptq_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -76,22 +78,6 @@ static const Route* find_route(int64_t M, ptq_dtype dt) {
     if (r.dtype == dt && M >= r.m_min && M <= r.m_max) return &r;
   return nullptr;
 }
-
-// ---- validation helpers ----------------------------------------------------
-static bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
-
-static bool aligned(const void* p, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-static bool dtype_ok(ptq_dtype dt) { return dt == PTQ_F32 || dt == PTQ_BF16; }
-
-static size_t dsize(ptq_dtype dt) { return dt == PTQ_F32 ? 4 : 2; }
 
 }  // namespace ptq
 

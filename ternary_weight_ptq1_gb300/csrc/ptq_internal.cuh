@@ -56,10 +56,25 @@ __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Clears the calling thread's failure message: every public call's first act.
+void clear_error();
 // Records a failure message for ptq_last_error() and returns `s`.
 ptq_status fail(ptq_status s, const char* fmt, ...);
 // Maps a CUDA error to PTQ_ERR_CUDA with a message naming `what`.
 ptq_status cuda_fail(cudaError_t e, const char* what);
+
+// ---- argument checks ---------------------------------------------------------
+inline bool mul_ok(int64_t a, int64_t b, int64_t* out) {
+  if (a < 0 || b < 0) return false;
+  if (a != 0 && b > INT64_MAX / a) return false;
+  *out = a * b;
+  return true;
+}
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+inline bool dtype_ok(ptq_dtype dt) { return dt == PTQ_F32 || dt == PTQ_BF16; }
+inline size_t dsize(ptq_dtype dt) { return dt == PTQ_F32 ? 4 : 2; }
 
 // ---- launchers (arguments already validated) -------------------------------
 cudaError_t launch_unpack(const uint8_t* wq, int8_t* trits, int64_t N,
@@ -181,6 +196,49 @@ size_t gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base,
                           uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box_inner,
                           uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
+// Key-value rows into and out of a paged cache (k_kv.cu).
+struct KvRows {
+  void *k, *v;                 // T x kv_heads x head_dim each, F32 or BF16
+  int64_t k_stride, v_stride;  // elements from a token to the next
+  const int32_t* slots;        // T
+  int64_t T;
+  Act t;
+};
+cudaError_t launch_kv_write(const ptq_kv_cache& c, const KvRows& r, cudaStream_t st);
+cudaError_t launch_kv_read(const ptq_kv_cache& c, const KvRows& r, cudaStream_t st);
+
+// Attention of one new token over a paged cache (k_attn_decode.cu).
+struct DecodeArgs {
+  const void* q;
+  int64_t q_stride;
+  ptq_kv_cache c;
+  const int32_t* table;
+  int64_t table_width;
+  const int32_t* lens;
+  void* out;
+  float* lse;
+  int64_t B, Hq;
+  float scale;
+  Act t;
+};
+cudaError_t launch_attn_decode(const DecodeArgs& a, void* ws, cudaStream_t st);
+size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+
+// Attention of packed prompts (k_attn_prefill.cu), bf16.
+struct PrefillArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu_q, *cu_k;
+  uint16_t* out;
+  float* lse;
+  int64_t B, Tq, Tk, Hq, Hkv, D;
+  float scale;
+  bool causal;
+};
+cudaError_t launch_attn_prefill(const PrefillArgs& a, void* ws, cudaStream_t st);
+size_t attn_prefill_workspace(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
+                              int64_t D);
 
 // One CTA waits (bounded) on an mbarrier nothing arrives on and raises the
 // device status word when the wait runs out (k_selftest.cu).
