@@ -240,6 +240,13 @@ cudaError_t launch_attn_prefill(const PrefillArgs& a, void* ws, cudaStream_t st)
 size_t attn_prefill_workspace(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
                               int64_t D);
 
+// 3-D TMA tensor map over a tokens x heads x D array of 16-bit values, tokens
+// `stride` elements apart: boxes of 64 columns x box_heads x box_tokens, rows
+// (head fastest) of 128 swizzled bytes.
+cudaError_t encode_tma_heads(CUtensorMap* map, const void* base, int64_t D, int64_t heads,
+                             int64_t tokens, int64_t stride, uint32_t box_heads,
+                             uint32_t box_tokens);
+
 // One CTA waits (bounded) on an mbarrier nothing arrives on and raises the
 // device status word when the wait runs out (k_selftest.cu).
 cudaError_t launch_selftest_timeout(cudaStream_t st);

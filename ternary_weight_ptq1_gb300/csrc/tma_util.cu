@@ -39,6 +39,19 @@ struct MapCache {
 thread_local MapCache t_maps;
 }  // namespace
 
+static cudaError_t find_encode() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    g_encode_err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                    cudaEnableDefault, &q);
+    if (g_encode_err == cudaSuccess && q != cudaDriverEntryPointSuccess)
+      g_encode_err = cudaErrorNotSupported;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode_err;
+}
+
 cudaError_t encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base,
                           uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box_inner,
                           uint32_t box_rows, CUtensorMapSwizzle swizzle) {
@@ -49,16 +62,8 @@ cudaError_t encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* 
       *map = c.map[i];
       return cudaSuccess;
     }
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    g_encode_err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                    cudaEnableDefault, &q);
-    if (g_encode_err == cudaSuccess && q != cudaDriverEntryPointSuccess)
-      g_encode_err = cudaErrorNotSupported;
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (g_encode_err != cudaSuccess) return g_encode_err;
+  const cudaError_t found = find_encode();
+  if (found != cudaSuccess) return found;
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_inner, box_rows};
@@ -72,6 +77,22 @@ cudaError_t encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* 
   c.key[slot] = k;
   c.map[slot] = *map;
   return cudaSuccess;
+}
+
+cudaError_t encode_tma_heads(CUtensorMap* map, const void* base, int64_t D, int64_t heads,
+                             int64_t tokens, int64_t stride, uint32_t box_heads,
+                             uint32_t box_tokens) {
+  const cudaError_t found = find_encode();
+  if (found != cudaSuccess) return found;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace ptq
