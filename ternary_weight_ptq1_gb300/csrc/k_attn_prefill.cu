@@ -13,15 +13,14 @@
 // operand of the second product, so only K and V pass through shared memory.
 // A CTA holds two Q tiles (head_dim up to 128), neighbours in the sequence,
 // that share each K and V tile; at head_dim 256 one Q tile whose S has two
-// buffers.  Either way the tensor core always has the other S in work while
-// the softmax of one runs:
-//     QK(0) QK(1) PV(0) QK(2) PV(1) QK(3) PV(2) ...
-// and because the tensor core runs in order, PV(i) having been issued before
-// QK(i + 2) is all that keeps a slot's P from being overwritten.
+// buffers.  Either way the tensor core has one S's products in work while the
+// softmax of the other runs.  A slot of TMEM holds S, then P, and one thread
+// issues all of a slot's MMAs, which run in order: that alone keeps P from
+// being overwritten before it is read.
 //
 // Warps: four for the softmax of each Q tile (a thread holds a row: its
-// maximum and sum need no shuffle), one that issues the TMA loads, one that
-// issues the MMAs.  The maximum that P refers to moves only when a row's
+// maximum and sum need no shuffle), one that issues the TMA loads, one for
+// each Q tile that issues its MMAs.  The maximum that P refers to moves only when a row's
 // grows by more than 2^8 over it: P up to 2^8 costs fp32 sums nothing, and
 // rescaling O (TMEM to registers and back) becomes rare.
 //
@@ -47,25 +46,39 @@ constexpr float kSlack = 8.0f;  // log2 of the largest P
 template <int D>
 struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;    // Q tiles of a CTA
-  static constexpr int kCols = D < 128 ? D : 128;    // columns of a ring unit
-  static constexpr int kUnits = D / kCols;           // units of a K or V tile
+  // A K or V tile passes through the ring in one unit, or two: K by columns,
+  // V by keys, as the products use them up.
+  static constexpr int kUnits = D == 256 ? 2 : 1;
+  static constexpr int kCols = D / kUnits;           // columns of a K unit
+  static constexpr int kVKeys = kKeys / kUnits;      // keys of a V unit
   static constexpr int kUnit = kKeys * kCols * 2;    // bytes
   static constexpr int kRing = D == 64 ? 8 : 5;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
-  static constexpr int kThreads = 32 * (kSoftmax + 2);
+  static constexpr int kThreads = 32 * (kSoftmax + 4);  // whole groups of four warps
+  // Registers a thread: 384 threads get 168 each at launch (64,512 in all);
+  // 256 softmax threads take 208 and 128 others keep 80 (63,488).
+  static constexpr bool kSplitRegs = kTiles == 2;
   static constexpr int kOffRing = kTiles * kQ;
   static constexpr int kOffBar = kOffRing + kRing * kUnit;
-  // full[kRing] empty[kRing] q s[2] p[2] o[2] pv done
-  static constexpr int kBars = 2 * kRing + 1 + 2 + 2 + 2 + 1 + 1;
+  // P over S's columns; at head_dim 64 TMEM has room for P beside S, and the
+  // next S is in work as soon as this one has been read.
+  static constexpr bool kApart = D == 64;
+  // full[kRing] empty[kRing] q s[2] read[2] p[2][2] o[2] pv[2] turn[2] done
+  static constexpr int kBars = 2 * kRing + 1 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024 && Cfg<256>::kSmem <= 227 * 1024, "shared memory");
+// A unit is as many bytes as its boxes of 64 columns bring.
+static_assert(Cfg<256>::kUnit == kKeys * Cfg<256>::kCols * 2 &&
+                  Cfg<256>::kUnit == Cfg<256>::kVKeys * 256 * 2 &&
+                  Cfg<64>::kUnit == Cfg<64>::kVKeys * 64 * 2, "ring units");
 
 struct Args {
   PrefillArgs a;
   int G, hg, tpt;  // query heads of a kv head; heads and tokens of a Q tile
+  int heads;       // head blocks in all
 };
 
 __device__ __forceinline__ int clamped(int v, int64_t hi) {
@@ -125,19 +138,24 @@ __device__ __forceinline__ constexpr uint32_t idesc() {
          ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)add)
-      : "memory");
+// kAdd: onto what the accumulator holds.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %4;" ::"r"(d), "l"(a), "l"(b),
+               "r"(id), "n"(kAdd ? 1 : 0)
+               : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)add)
-      : "memory");
+template <bool kAdd>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
+  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, %4;" ::"r"(d), "r"(a), "l"(b),
+               "r"(id), "n"(kAdd ? 1 : 0)
+               : "memory");
+}
+// One lane of the converged warp, the same each time.
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
@@ -186,6 +204,11 @@ __device__ __forceinline__ void tmem_wait_st() {
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -264,8 +287,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing;
-  uint64_t *s_full = q_full + 1, *p_full = s_full + 2, *o_full = p_full + 2, *pv_done = o_full + 2,
-           *all_done = pv_done + 1;
+  // of a slot: S written, S read (kApart), the first and second half of P
+  // written; of a Q tile: O final, a product with V done (not where S's
+  // arrival says it), its turn to issue
+  uint64_t *s_full = q_full + 1, *s_read = s_full + 2, *p_full = s_read + 2, *o_full = p_full + 4,
+           *pv_done = o_full + 2, *turn = pv_done + 2, *all_done = turn + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   int* item = reinterpret_cast<int*>(smem + C::kOffMisc + 8);  // sequence (-1: none), run
@@ -285,23 +311,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (lane == 0) {
       for (int i = 0; i < C::kRing; ++i) {
         mbar_init(full + i, 1);
-        mbar_init(empty + i, 1);
+        mbar_init(empty + i, kTiles);
       }
       mbar_init(q_full, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(s_full + i, 1);
-        mbar_init(p_full + i, 4);  // the four softmax warps of a tile
+        mbar_init(s_read + i, 4);  // the four softmax warps of a tile
+        mbar_init(p_full + 2 * i, 4);
+        mbar_init(p_full + 2 * i + 1, 4);
         mbar_init(o_full + i, 1);
+        mbar_init(pv_done + i, 1);
+        mbar_init(turn + i, 1);
       }
-      mbar_init(pv_done, 1);
-      mbar_init(all_done, 1);
+      mbar_init(all_done, kTiles);
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   } else if (warp == 0) {
     pdl_wait();
     int b = -1, t = 0;
-    if (!find_item(a, kTiles * p.tpt, blockIdx.x, &b, &t)) b = -1;
+    if (!find_item(a, kTiles * p.tpt, blockIdx.x / p.heads, &b, &t)) b = -1;
     if (lane == 0) {
       item[0] = b;
       item[1] = t;
@@ -315,25 +344,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int b = item[0];
   if (b >= 0) {
     const Span sp = span_of(a, b);
-    const int blocks = p.G / p.hg;  // head blocks of a kv head
-    const int h = blockIdx.y / blocks, hq0 = h * p.G + (blockIdx.y % blocks) * p.hg;
+    // heads fastest: the long items of all of them come first
+    const int blocks = p.G / p.hg, head = (int)blockIdx.x % p.heads;
+    const int h = head / blocks, hq0 = h * p.G + (head % blocks) * p.hg;
     // Q tile s: queries tok(s) .. tok(s) + tpt - 1 of the sequence; keys of its
     // last query; K tiles
-    int first[kTiles], n[kTiles];
+    int first[kTiles], keys[kTiles], n[kTiles];
 #pragma unroll
     for (int s = 0; s < kTiles; ++s) {
       first[s] = (item[1] * kTiles + s) * p.tpt;
       const int last = min(first[s] + p.tpt, sp.nq) - 1;
-      const int keys = a.causal ? min(sp.nk, sp.nk - sp.nq + last + 1) : sp.nk;
-      n[s] = first[s] < sp.nq && keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+      keys[s] = a.causal ? min(sp.nk, sp.nk - sp.nq + last + 1) : sp.nk;
+      n[s] = first[s] < sp.nq && keys[s] > 0 ? (keys[s] + kKeys - 1) / kKeys : 0;
     }
     int most = n[0];
     if (kTiles == 2) most = max(most, n[kTiles - 1]);
     const uint32_t ring = smem_addr(smem + C::kOffRing), qs = smem_addr(smem);
     bool ok = true;
 
+    if (warp >= C::kSoftmax) {
+      if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
     if (warp == kLoad) {
-      // ---- loads: Q, then K_0 V_0 K_1 V_1 ... through the ring ----------------------
+      // ---- loads: Q, then K and V tiles through the ring in the order of their use:
+      // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
       if (lane == 0 && most > 0) {
         const int rows = p.hg * p.tpt;
         int tiles = 0;
@@ -344,100 +378,143 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             for (int c = 0; c < D / 64; ++c)
               tma_3d(qs + s * C::kQ + c * kRows * 128, &map_q, 64 * c, hq0, sp.q0 + first[s], q_full);
         int u = 0;  // units issued
-        for (int j = 0; j < most && ok; ++j)
-          for (int kv = 0; kv < 2 && ok; ++kv)
-            for (int i = 0; i < C::kUnits && ok; ++i, ++u) {
-              const int st = u % C::kRing, round = u / C::kRing;
-              if (round > 0) ok = mbar_wait(empty + st, (round - 1) & 1, abort_flag);
-              if (!ok) break;
-              mbar_expect_tx(full + st, C::kUnit);
-              for (int c = 0; c < C::kCols / 64; ++c)
-                tma_3d(ring + st * C::kUnit + c * kKeys * 128, kv ? &map_v : &map_k,
-                       i * C::kCols + 64 * c, h, sp.k0 + j * kKeys, full + st);
-            }
+        auto load = [&](const CUtensorMap* map, int x, int y, int rows, int blocks) {
+          const int st = u % C::kRing, round = u / C::kRing;
+          if (round > 0) ok = mbar_wait(empty + st, (round - 1) & 1, abort_flag);
+          if (!ok) return;
+          mbar_expect_tx(full + st, C::kUnit);
+          for (int c = 0; c < blocks; ++c)  // boxes of 64 columns
+            tma_3d(ring + st * C::kUnit + c * rows * 128, map, x + 64 * c, h, y, full + st);
+          ++u;
+        };
+        auto load_k = [&](int j) {
+          for (int k = 0; k < C::kUnits && ok; ++k)
+            load(&map_k, k * C::kCols, sp.k0 + j * kKeys, kKeys, C::kCols / 64);
+        };
+        auto load_v = [&](int j) {
+          for (int k = 0; k < C::kUnits && ok; ++k)
+            load(&map_v, 0, sp.k0 + j * kKeys + k * C::kVKeys, C::kVKeys, D / 64);
+        };
+        load_k(0);
+        for (int j = 0; j < most && ok; ++j) {
+          if (kTiles == 1 && j + 1 < most) load_k(j + 1);
+          load_v(j);
+          if (kTiles == 2 && j + 1 < most) load_k(j + 1);
+        }
         // whatever becomes of the MMAs, the copies land before the CTA ends
         for (int v = max(0, u - C::kRing); v < u; ++v)
           static_cast<void>(mbar_wait(full + v % C::kRing, (v / C::kRing) & 1, nullptr));
         static_cast<void>(mbar_wait(q_full, 0, nullptr));
       }
-    } else if (warp == kMma) {
-      // ---- MMAs ------------------------------------------------------------------------
-      if (lane == 0) {
-        struct Item {
-          int j, s;
-        };
-        auto valid = [&](Item i) { return i.j < most; };
-        auto next = [&](Item i) {
-          if constexpr (kTiles == 1) {
-            ++i.j;
-          } else {
-            do {
-              i = i.s == 0 ? Item{i.j, 1} : Item{i.j + 1, 0};
-            } while (i.j < most && i.j >= n[i.s]);
-          }
-          return i;
-        };
-        auto slot_of = [&](Item i) { return kTiles == 1 ? i.j & 1 : i.s; };
-        auto use_of = [&](Item i) { return kTiles == 1 ? i.j >> 1 : i.j; };
-        auto last_user = [&](Item i) {
-          return kTiles == 1 || i.s == 1 || i.j >= n[kTiles - 1];
-        };
-        auto qk = [&](Item i) {
-          const uint32_t d = tmem + slot_of(i) * kKeys;
-          for (int k = 0; k < C::kUnits && ok; ++k) {
-            const int u = 2 * i.j * C::kUnits + k, st = u % C::kRing;
-            ok = mbar_wait(full + st, (u / C::kRing) & 1, abort_flag);
-            if (!ok) return;
-            fence_after();
+    } else if (warp >= kMma && warp < kMma + kTiles) {
+      // ---- MMAs.  The warp stays converged and one lane issues each product in
+      // straight-line code.  The tensor core takes few MMAs ahead, so a pause in
+      // the issue is a pause in the products: with two Q tiles each has an issuing
+      // warp of its own, and one waits for barriers while the other's MMAs run ----
+      const int s = warp - kMma, tiles = n[s];
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && __all_sync(~0u, mbar_wait(bar, phase & 1, abort_flag));
+      };
+      auto arrived = [&](int u) { wait(full + u % C::kRing, u / C::kRing); };  // ring unit u
+      // first unit of K_j and V_j (with one Q tile, past the last K there is no
+      // K_(j + 1) before V_j)
+      auto k_unit = [&](int j) { return (kTiles == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * C::kUnits; };
+      auto v_unit = [&](int j) {
+        return (kTiles == 2 || j == most - 1 ? 2 * j + 1 : 2 * j + 2) * C::kUnits;
+      };
+      // A K or V tile that the other Q tile does not use is released for both.
+      auto release = [&](int j, int st) {
+        mma_commit(empty + st);
+        if (kTiles == 2 && j >= n[kTiles - 1 - s]) mma_commit(empty + st);
+      };
+      // S of tile j into its slot: unit k of the columns
+      auto qk = [&](int j, int k) {
+        const int slot = kTiles == 1 ? j & 1 : s, st = (k_unit(j) + k) % C::kRing;
+        const uint64_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
+        const uint64_t kd = tile_desc(ring + st * C::kUnit, 16);
 #pragma unroll
-            for (int c = 0; c < C::kCols / 64; ++c)
+        for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mma_ss(d, tile_desc(qs + i.s * C::kQ + (k * (C::kCols / 64) + c) * kRows * 128 + 32 * e, 16),
-                       tile_desc(ring + st * C::kUnit + c * kKeys * 128 + 32 * e, 16),
-                       idesc<kKeys, false>(), (k | c | e) != 0);
-            if (last_user(i)) mma_commit(empty + st);
+          for (int e = 0; e < 4; ++e) {
+            const int at = c * (kRows * 128 / 16) + 2 * e;
+            if (k == 0 && c == 0 && e == 0)
+              mma_ss<false>(tmem + slot * kKeys, qd + at, kd + at, idesc<kKeys, false>());
+            else
+              mma_ss<true>(tmem + slot * kKeys, qd + at, kd + at, idesc<kKeys, false>());
           }
-          mma_commit(s_full + slot_of(i));
-        };
-        auto pv = [&](Item i) {
-          ok = mbar_wait(p_full + slot_of(i), use_of(i) & 1, abort_flag);
-          if (!ok) return;
-          fence_after();
-          const uint32_t pa = tmem + slot_of(i) * kKeys;
-          for (int k = 0; k < C::kUnits && ok; ++k) {
-            const int u = (2 * i.j + 1) * C::kUnits + k, st = u % C::kRing;
-            ok = mbar_wait(full + st, (u / C::kRing) & 1, abort_flag);
-            if (!ok) return;
-            fence_after();
-            const uint32_t d = tmem + 2 * kKeys + i.s * D + k * C::kCols;
+        release(j, st);
+        if (k == C::kUnits - 1) mma_commit(s_full + slot);
+      };
+      // O += P V of tile j over its first or second 64 keys
+      auto pv = [&](int j, int half) {
+        const int slot = kTiles == 1 ? j & 1 : s;
+        const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
+        const uint32_t d = tmem + 2 * kKeys + s * D;
+        const int st = (v_unit(j) + (C::kUnits == 2 ? half : 0)) % C::kRing;
+        const uint64_t vd = tile_desc(ring + st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
+                                      C::kVKeys * 128);
+        if (j > 0 || half > 0)
+          mma_ts<true>(d, pa, vd, idesc<D, true>());
+        else
+          mma_ts<false>(d, pa, vd, idesc<D, true>());
 #pragma unroll
-            for (int e = 0; e < kKeys / 16; ++e)
-              mma_ts(d, pa + 8 * e, tile_desc(ring + st * C::kUnit + 2048 * e, kKeys * 128),
-                     idesc<C::kCols, true>(), i.j > 0 || e > 0);
-            if (last_user(i)) mma_commit(empty + st);
-          }
-          if constexpr (kTiles == 1) mma_commit(pv_done);
-          if (i.j == n[i.s] - 1) mma_commit(o_full + i.s);
-        };
-        Item i{0, 0};
-        if (most > 0) {
-          ok = mbar_wait(q_full, 0, abort_flag);
-          if (n[0] == 0) i = next(i);
-          if (ok) qk(i);
-          while (ok && valid(i)) {
-            const Item nx = next(i);
-            const bool apart = valid(nx) && slot_of(nx) != slot_of(i);
-            if (apart) qk(nx);
-            if (ok) pv(i);
-            if (ok && valid(nx) && !apart) qk(nx);
-            i = nx;
-          }
+        for (int e = 1; e < 4; ++e)  // 16 keys: 8 columns of P, 2048 bytes of V
+          mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
+        if (half == 1 || C::kUnits == 2) release(j, st);
+        if (half == 1) {
+          if (kTiles == 1 || C::kApart) mma_commit(pv_done + s);
+          if (j == tiles - 1) mma_commit(o_full + s);
         }
-        mma_commit(all_done);
+      };
+      if (tiles > 0) {
+        wait(q_full, 0);
+        auto scores = [&](int j) {
+#pragma unroll
+          for (int k = 0; k < C::kUnits; ++k) {
+            arrived(k_unit(j) + k);
+            fence_after();
+            if (ok && elected()) qk(j, k);
+            __syncwarp();
+          }
+        };
+        scores(0);
+        for (int j = 0; j < tiles && ok; ++j) {
+          const bool more = j + 1 < tiles;
+          const int slot = kTiles == 1 ? j & 1 : s, use = kTiles == 1 ? j >> 1 : j;
+          if (more && kTiles == 1) scores(j + 1);
+          if (more && C::kApart) {
+            wait(s_read + slot, use);
+            scores(j + 1);
+          }
+          for (int k = 0; k < C::kUnits; ++k) arrived(v_unit(j) + k);
+          constexpr bool kAfter = kTiles == 2 && !C::kApart;  // the next S goes where P was
+          if (more && kAfter) arrived(k_unit(j + 1));
+          // Two Q tiles take turns: issued side by side their MMAs would alternate,
+          // both S would arrive together and the tensor core would stand still
+          // during both softmaxes.
+          if (kAfter) {
+            if (s == 1 && j < n[0]) wait(turn + s, j);
+            if (s == 0 && j > 0 && j - 1 < n[kTiles - 1]) wait(turn + s, j - 1);
+          }
+          wait(p_full + 2 * slot, use);
+          fence_after();
+          if (ok && elected()) pv(j, 0);
+          __syncwarp();
+          wait(p_full + 2 * slot + 1, use);
+          fence_after();
+          if (ok && elected()) {
+            pv(j, 1);
+            if (more && kAfter) qk(j + 1, 0);
+            if (kAfter) mbar_arrive(turn + 1 - s);
+          }
+          __syncwarp();
+        }
       }
-    } else {
+      if (elected()) mma_commit(all_done);
+      __syncwarp();
+    } else if (warp < C::kSoftmax) {
       // ---- softmax: thread = row of Q tile s ----------------------------------------
+      if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
       const int s = kTiles == 1 ? 0 : warp >> 2, quarter = warp & 3;
       const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
       const int row = 32 * quarter + lane, tok = first[s] + row / p.hg;
@@ -448,10 +525,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const float scale2 = a.scale * kLog2e;
       const uint32_t o_at = tmem + lanes + 2 * kKeys + s * D;
       float m = kNegInf;  // what P refers to, in units of log2
-      uint64_t sum2 = pair(0.0f, 0.0f);
+      uint64_t sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
       for (int j = 0; j < n[s] && ok; ++j) {
         const int slot = kTiles == 1 ? j & 1 : s, use = kTiles == 1 ? j >> 1 : j;
         const uint32_t at = tmem + lanes + slot * kKeys;
+        const uint32_t p_at = C::kApart ? tmem + lanes + 384 + slot * 64 : at;
         ok = __all_sync(~0u, mbar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
@@ -459,35 +537,49 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_ld32(at + c, v + c);
         tmem_wait_ld();
+        if constexpr (C::kApart) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read + slot);
+        }
         if ((j + 1) * kKeys > all_see) {
           const int left = sees - j * kKeys;
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
             if (c >= left) v[c] = 0xff800000u;
         }
-        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        float top[4];
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 8)
+        for (int e = 0; e < 4; ++e)
+          top[e] = max3(__uint_as_float(v[3 * e]), __uint_as_float(v[3 * e + 1]),
+                        __uint_as_float(v[3 * e + 2]));
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top[e] = fmaxf(top[e], fmaxf(__uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1])));
-        const float t2 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
+        for (int c = 12; c < kKeys; c += 2)  // 116 more in pairs, 14 or 15 a chain
+          top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+        const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
+        if constexpr (C::kApart)
+          if (j > 0) {  // the product with the tile before has read its P
+            ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
+            if (!ok) break;
+          }
         if (j == 0) {
           m = t2;
         } else if (__any_sync(~0u, t2 > m + kSlack)) {
-          // O moves to the new maximum; the product before the last of this
-          // tile's has been waited for with S (one Q tile: here)
-          const float mn = t2 > m + kSlack ? t2 : m;
-          const float f = m == kNegInf ? 0.0f : exp2_fast(m - mn);
-          m = mn;
+          // O moves to the new maximum once the product with the tile before is
+          // done (two Q tiles: it is)
           if constexpr (kTiles == 1) {
             ok = __all_sync(~0u, mbar_wait(pv_done, (j - 1) & 1, abort_flag));
             if (!ok) break;
-            fence_after();
           }
+          const float mn = t2 > m + kSlack ? t2 : m;
+          const float f = m == kNegInf ? 0.0f : exp2_fast(m - mn);
+          m = mn;
+          fence_after();
           float lo, hi;
-          unpair(sum2, lo, hi);
-          sum2 = pair(lo * f, hi * f);
+          unpair(sum2[0], lo, hi);
+          sum2[0] = pair(lo * f, hi * f);
+          unpair(sum2[1], lo, hi);
+          sum2[1] = pair(lo * f, hi * f);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -500,8 +592,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         const float z = m == kNegInf ? 0.0f : -m;
         const uint64_t zz = pair(z, z), ss = pair(scale2, scale2);
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 64) {
+        auto half_p = [&](int c) {  // keys c .. c + 63
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -509,25 +600,39 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             unpair(fma2(pair(__uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1])), ss, zz), x0, x1);
             x0 = exp2_fast(x0);
             x1 = exp2_fast(x1);
-            sum2 = add2(sum2, pair(x0, x1));
+            sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
             w[e] = bf16x2(x0, x1);
           }
-          tmem_st32(at + c / 2, w);
+          tmem_st32(p_at + c / 2, w);
+        };
+        auto publish = [&](int half) {
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 2 * slot + half);
+        };
+        // The product with V starts on the first half.  The branch is worth more
+        // than the work it saves in a last tile: without it the compiler computes
+        // both halves before it stores the first (630 for 500 us, 8192 tokens).
+        half_p(0);
+        publish(0);
+        if (keys[s] - j * kKeys > 64) {
+          half_p(64);
+        } else {
+          const uint32_t none[32] = {};
+          tmem_st32(p_at + 32, none);
         }
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + slot);
+        publish(1);
       }
 
       // ---- epilogue ----------------------------------------------------------------
       float lo, hi;
-      unpair(sum2, lo, hi);
+      unpair(add2(sum2[0], sum2[1]), lo, hi);
       const float l = lo + hi;
       const int64_t tq = sp.q0 + tok;
       const int hq = hq0 + row % p.hg;
-      const bool keys = n[s] > 0;
-      if (ok && keys) ok = __all_sync(~0u, mbar_wait(o_full + s, 0, abort_flag));
+      const bool some = n[s] > 0;
+      if (ok && some) ok = __all_sync(~0u, mbar_wait(o_full + s, 0, abort_flag));
       if (ok && first[s] < sp.nq) {
         fence_after();
         if (mine && a.lse) a.lse[tq * a.Hq + hq] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
@@ -538,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32], w[16];
-          if (keys) {
+          if (some) {
             tmem_ld32(o_at + c, o);
             tmem_wait_ld();
           } else {
@@ -624,7 +729,7 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t st) {
   cudaError_t e = encode_tma_heads(&mq, a.q, D, a.Hq, a.Tq, a.q_stride, p.hg, p.tpt);
   if (a.Tk > 0) {
     if (e == cudaSuccess) e = encode_tma_heads(&mk, a.k, D, a.Hkv, a.Tk, a.k_stride, 1, kKeys);
-    if (e == cudaSuccess) e = encode_tma_heads(&mv, a.v, D, a.Hkv, a.Tk, a.v_stride, 1, kKeys);
+    if (e == cudaSuccess) e = encode_tma_heads(&mv, a.v, D, a.Hkv, a.Tk, a.v_stride, 1, C::kVKeys);
   } else {
     mk = mv = mq;  // never loaded from
   }
@@ -637,8 +742,9 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t st) {
   // every sequence has at most one run that is not whole
   const int64_t run = C::kTiles * p.tpt, items = a.Tq / run + (a.B < a.Tq ? a.B : a.Tq);
   const int64_t heads = a.Hkv * (p.G / p.hg);
-  if (items > INT32_MAX || heads > 65535) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3((unsigned)items, (unsigned)heads), dim3(C::kThreads), C::kSmem, st, mq,
+  if (items * heads > INT32_MAX) return cudaErrorInvalidValue;
+  p.heads = (int)heads;
+  return launch_pdl(kern, dim3((unsigned)(items * heads)), dim3(C::kThreads), C::kSmem, st, mq,
                     mk, mv, p, status);
 }
 
