@@ -489,14 +489,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           for (int k = 0; k < C::kUnits; ++k) arrived(v_unit(j) + k);
           constexpr bool kAfter = kTiles == 2 && !C::kApart;  // the next S goes where P was
           if (more && kAfter) arrived(k_unit(j + 1));
+          wait(p_full + 2 * slot, use);
           // Two Q tiles take turns: issued side by side their MMAs would alternate,
           // both S would arrive together and the tensor core would stand still
-          // during both softmaxes.
+          // during both softmaxes (540 for 442 us, 8192 tokens).
           if (kAfter) {
             if (s == 1 && j < n[0]) wait(turn + s, j);
             if (s == 0 && j > 0 && j - 1 < n[kTiles - 1]) wait(turn + s, j - 1);
           }
-          wait(p_full + 2 * slot, use);
           fence_after();
           if (ok && elected()) pv(j, 0);
           __syncwarp();
@@ -504,8 +504,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           fence_after();
           if (ok && elected()) {
             pv(j, 1);
-            if (more && kAfter) qk(j + 1, 0);
-            if (kAfter) mbar_arrive(turn + 1 - s);
+            if (kAfter) {
+              if (more) qk(j + 1, 0);
+              mbar_arrive(turn + 1 - s);
+            }
           }
           __syncwarp();
         }
@@ -525,12 +527,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const float scale2 = a.scale * kLog2e;
       const uint32_t o_at = tmem + lanes + 2 * kKeys + s * D;
       float m = kNegInf;  // what P refers to, in units of log2
+      bool ready = false;
       uint64_t sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
       for (int j = 0; j < n[s] && ok; ++j) {
         const int slot = kTiles == 1 ? j & 1 : s, use = kTiles == 1 ? j >> 1 : j;
         const uint32_t at = tmem + lanes + slot * kKeys;
         const uint32_t p_at = C::kApart ? tmem + lanes + 384 + slot * 64 : at;
-        ok = __all_sync(~0u, mbar_wait(s_full + slot, use & 1, abort_flag));
+        ok = __all_sync(~0u, ready || mbar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
         uint32_t v[kKeys];
@@ -557,18 +560,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int c = 12; c < kKeys; c += 2)  // 116 more in pairs, 14 or 15 a chain
           top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
         const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
-        if constexpr (C::kApart)
-          if (j > 0) {  // the product with the tile before has read its P
-            ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
-            if (!ok) break;
-          }
         if (j == 0) {
           m = t2;
         } else if (__any_sync(~0u, t2 > m + kSlack)) {
           // O moves to the new maximum once the product with the tile before is
-          // done (two Q tiles: it is)
-          if constexpr (kTiles == 1) {
-            ok = __all_sync(~0u, mbar_wait(pv_done, (j - 1) & 1, abort_flag));
+          // done (where S follows P, S says so)
+          if constexpr (kTiles == 1 || C::kApart) {
+            ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
             if (!ok) break;
           }
           const float mn = t2 > m + kSlack ? t2 : m;
@@ -603,6 +601,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
             w[e] = bf16x2(x0, x1);
           }
+          if constexpr (C::kApart)  // the product with the tile before has read its P
+            if (c == 0 && j > 0)
+              ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
           tmem_st32(p_at + c / 2, w);
         };
         auto publish = [&](int half) {
@@ -613,9 +614,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         };
         // The product with V starts on the first half.  The branch is worth more
         // than the work it saves in a last tile: without it the compiler computes
-        // both halves before it stores the first (630 for 500 us, 8192 tokens).
+        // both halves before it stores the first.
         half_p(0);
         publish(0);
+        {  // whether the next S has arrived: asked now, used at the top
+          const int nj = j + 1, nslot = kTiles == 1 ? nj & 1 : s, nuse = kTiles == 1 ? nj >> 1 : nj;
+          ready = nj < n[s] && mbar_test(s_full + nslot, nuse & 1);
+        }
         if (keys[s] - j * kKeys > 64) {
           half_p(64);
         } else {
