@@ -19,10 +19,17 @@
 // being overwritten before it is read.
 //
 // Warps: four for the softmax of each Q tile (a thread holds a row: its
-// maximum and sum need no shuffle), one that issues the TMA loads, one for
-// each Q tile that issues its MMAs.  The maximum that P refers to moves only when a row's
-// grows by more than 2^8 over it: P up to 2^8 costs fp32 sums nothing, and
-// rescaling O (TMEM to registers and back) becomes rare.
+// maximum and sum need no shuffle), four that store the output while the next
+// item is in work, one that issues the TMA loads, one for each Q tile that
+// issues its MMAs, one that finds the CTA's next item.  The maximum that P
+// refers to moves only when a row's grows by more than 2^8 over it: P up to 2^8
+// costs fp32 sums nothing, and rescaling O (TMEM to registers and back) becomes
+// rare.
+//
+// One CTA an SM goes through items (two neighbouring Q tiles, or one, of one
+// sequence and head block), the longest first, dealt out there and back.  Where
+// the items are few and the keys long, the keys are cut into parts whose sums
+// a second kernel joins in order.
 //
 // A key that a row does not see has P = 0, and 0 times a non-finite value is
 // NaN: rows whose output is not finite though their sum is are computed again
@@ -55,19 +62,26 @@ struct Cfg {
   static constexpr int kRing = D == 64 ? 8 : 5;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
-  static constexpr int kThreads = 32 * (kSoftmax + 4);  // whole groups of four warps
-  // Registers a thread: 384 threads get 168 each at launch (64,512 in all);
-  // 256 softmax threads take 208 and 128 others keep 80 (63,488).
-  static constexpr bool kSplitRegs = kTiles == 2;
+  static constexpr int kThreads = 32 * (kSoftmax + 8);  // four to store, four others
+  // Registers a thread.  Two Q tiles: 512 threads get 128 each at launch (65,536
+  // in all); 256 softmax threads take 168, 128 that store keep 96 and 128 others
+  // 80 (65,536).  One: 384 get 168 (64,512); 128 take 232, 128 keep 128, 128 keep
+  // 104 (59,392).
+  static constexpr int kRegsSoftmax = kTiles == 2 ? 168 : 232;
+  static constexpr int kRegsStore = kTiles == 2 ? 96 : 128;
+  static constexpr int kRegsOther = kTiles == 2 ? 80 : 104;
   static constexpr int kOffRing = kTiles * kQ;
   static constexpr int kOffBar = kOffRing + kRing * kUnit;
   // P over S's columns; at head_dim 64 TMEM has room for P beside S, and the
   // next S is in work as soon as this one has been read.
   static constexpr bool kApart = D == 64;
-  // full[kRing] empty[kRing] q s[2] read[2] p[2][2] o[2] pv[2] turn[2] done
-  static constexpr int kBars = 2 * kRing + 1 + 2 + 2 + 4 + 2 + 2 + 2 + 1;
-  static constexpr int kOffMisc = kOffBar + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 64;
+  // full[kRing] empty[kRing] q[2] q free[2] s[2] read[2] p[2][2] o[2] o free[2] pv[2] turn[2]
+  // item full[2] item empty[2] sums full[2] sums empty[2] done
+  static constexpr int kBars = 2 * kRing + 4 + 2 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
+  static constexpr int kOffSums = kOffItem + 2 * 64;  // (maximum, sum) of each row
+  static constexpr int kOffMisc = kOffSums + kTiles * kRows * 8;
+  static constexpr int kSmem = kOffMisc + 16;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024 && Cfg<256>::kSmem <= 227 * 1024, "shared memory");
 // A unit is as many bytes as its boxes of 64 columns bring.
@@ -79,7 +93,23 @@ struct Args {
   PrefillArgs a;
   int G, hg, tpt;  // query heads of a kv head; heads and tokens of a Q tile
   int heads;       // head blocks in all
+  int splits;      // parts the keys of each item are cut into
+  float* part;     // splits > 1: [splits][Tq Hq][D] output sums, and the (maximum,
+  float2* ml;      // sum) they refer to, [splits][Tq Hq]
 };
+
+// A CTA's next piece of work: Q tiles of one sequence and head block, over one
+// part of the keys.  b < 0: no more.
+struct Item {
+  int b, q0, nq, k0, nk;  // the sequence's place
+  int first;              // first query of Q tile 0
+  int h, hq0;             // kv head, first query head
+  int split;
+  int lo;                 // the part's first tile of 128 keys
+  int n[2];               // its tiles that Q tile s sees some key of
+  int keys[2];            // keys the last query of Q tile s sees
+};
+static_assert(sizeof(Item) <= 64, "its place in shared memory");
 
 __device__ __forceinline__ int clamped(int v, int64_t hi) {
   return v < 0 ? 0 : v > hi ? (int)hi : v;
@@ -102,23 +132,32 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&x)[N]) {
 
 // One query row by a warp: query t (of all), head hq, over keys [k0, end).
 template <int D>
-__device__ __noinline__ void attend_row(const PrefillArgs& a, int t, int hq, int h, int k0, int end) {
+__device__ __noinline__ void attend_row(const Args& p, int split, int t, int hq, int h, int k0, int end) {
   constexpr int N = D / 32;
+  const PrefillArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   float q[N];
   load_bf16(a.q + (int64_t)t * a.q_stride + (int64_t)hq * D + lane * N, q);
   RowState<D> r;
+#pragma unroll 1
   for (int j = k0; j < end; ++j) {
     float k[N], v[N];
     load_bf16(a.k + (int64_t)j * a.k_stride + (int64_t)h * D + lane * N, k);
     load_bf16(a.v + (int64_t)j * a.v_stride + (int64_t)h * D + lane * N, v);
     r.add(q, k, v, a.scale * kLog2e);
   }
+  const int64_t row = (int64_t)t * a.Hq + hq;
+  if (p.splits > 1) {
+    const int64_t at = (int64_t)split * a.Tq * a.Hq + row;
+    if (lane == 0) p.ml[at] = make_float2(r.m, r.l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.part[at * D + lane * N + i] = r.o[i];
+    return;
+  }
   const float inv = r.l == 0.0f ? 0.0f : 1.0f / r.l;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    a.out[((int64_t)t * a.Hq + hq) * D + lane * N + i] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(r.o[i] * inv));
+    a.out[row * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(r.o[i] * inv));
 }
 
 // ---- tensor core -------------------------------------------------------------------
@@ -194,6 +233,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v) {
       PTQ_W8(v, 0), PTQ_W8(v, 8), PTQ_W8(v, 16), PTQ_W8(v, 24)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : PTQ_R8(v, 0), PTQ_R8(v, 8)
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -224,6 +270,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -235,45 +286,57 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 // ---- the order of the work -----------------------------------------------------------
-// Work item i of a head: sequences are cut into runs of `run` queries, the
-// runs that come late in their sequence (under a causal mask those with the
-// most keys) first.  With f(t) = sum over sequences of max(0, runs - t), the
-// items of run number t are [f(t + 1), f(t)).  One warp; false: no such item.
-__device__ bool find_item(const PrefillArgs& a, int run, int64_t i, int* b_out, int* t_out) {
-  const int lane = threadIdx.x & 31;
-  auto runs = [&](int64_t b) { return b < a.B ? (span_of(a, (int)b).nq + run - 1) / run : 0; };
+// Sequences are cut into runs of `run` queries.  The runs that come late in
+// their sequence (under a causal mask those with the most keys) are first:
+// level by level downwards, and through the sequences in each level.  One warp
+// walks them, each time further on.
+struct Walk {
+  int level, before;  // runs of higher levels
+};
+
+__device__ __forceinline__ int runs_of(const PrefillArgs& a, int64_t b, int run) {
+  return b < a.B ? (span_of(a, (int)b).nq + run - 1) / run : 0;
+}
+
+__device__ __forceinline__ Walk walk_from_top(const PrefillArgs& a, int run) {
   int most = 0;
-  const int first = runs(lane);
-  for (int64_t b = lane; b < a.B; b += 32) most = max(most, runs(b));
-  most = __reduce_max_sync(~0u, most);
-  auto f = [&](int t) {
-    int64_t n = max(0, first - t);
-    for (int64_t b = lane + 32; b < a.B; b += 32) n += max(0, runs(b) - t);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) n += __shfl_xor_sync(~0u, n, s);
-    return n;
-  };
-  if (f(0) <= i) return false;
-  int lo = 0, hi = most;  // f(lo) > i >= f(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (f(mid) > i)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  int64_t rank = i - f(lo + 1);  // among the sequences with more than lo runs
-  for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
-    const unsigned has = __ballot_sync(~0u, runs(b0 + lane) > lo);
-    const int n = __popc(has);
-    if (rank < n) {
-      *b_out = (int)b0 + __fns(has, 0, (int)rank + 1);
-      *t_out = lo;
-      return true;
+#pragma unroll 1
+  for (int64_t b = threadIdx.x & 31; b < a.B; b += 32) most = max(most, runs_of(a, b, run));
+  return {(int)__reduce_max_sync(~0u, most) - 1, 0};
+}
+
+// The sequence and level of run i in that order; false: there are not so many.
+__device__ __forceinline__ bool walk_to(const PrefillArgs& a, int run, int i, Walk& w, int* seq) {
+  const int lane = threadIdx.x & 31;
+  const int first = runs_of(a, lane, run);
+#pragma unroll 1
+  for (; w.level >= 0; --w.level) {
+    int n = w.before;
+#pragma unroll 1
+    for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
+      const unsigned has = __ballot_sync(~0u, (b0 ? runs_of(a, b0 + lane, run) : first) > w.level);
+      const int here = __popc(has);
+      if (i < n + here) {
+        *seq = (int)b0 + (int)__fns(has, 0, i - n + 1);
+        return true;
+      }
+      n += here;
     }
-    rank -= n;
+    w.before = n;
   }
   return false;
+}
+
+// 32 bytes of a row, whose alignment is 16 or 32.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), PTQ_W8(w, 0)
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <int D>
@@ -284,21 +347,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         int* status) {
   using C = Cfg<D>;
   constexpr int kTiles = C::kTiles;
+  constexpr bool kAfter = kTiles == 2 && !C::kApart;  // the next S goes where P was
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing;
-  // of a slot: S written, S read (kApart), the first and second half of P
-  // written; of a Q tile: O final, a product with V done (not where S's
-  // arrival says it), its turn to issue
-  uint64_t *s_full = q_full + 1, *s_read = s_full + 2, *p_full = s_read + 2, *o_full = p_full + 4,
-           *pv_done = o_full + 2, *turn = pv_done + 2, *all_done = turn + 2;
+  // ring units; of a Q tile: Q there, Q read; of a slot: S written, S read (kApart), the first
+  // and second half of P written; of a Q tile: O final, O read, a product with V
+  // done (not where S's arrival says it), its turn to issue; items there, read; rows'
+  // maxima and sums there, read
+  uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing, *q_free = q_full + 2;
+  uint64_t *s_full = q_free + 2, *s_read = s_full + 2, *p_full = s_read + 2, *o_full = p_full + 4,
+           *o_free = o_full + 2, *pv_done = o_free + 2, *turn = pv_done + 2, *item_full = turn + 2,
+           *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 2,
+           *all_done = ml_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  int* item = reinterpret_cast<int*>(smem + C::kOffMisc + 8);  // sequence (-1: none), run
 
   const PrefillArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kLoad = C::kSoftmax, kMma = C::kSoftmax + 1;
+  constexpr int kStore = C::kSoftmax, kLoad = kStore + 4, kMma = kLoad + 1, kPlan = kMma + kTiles;
 
   pdl_release();
   if (warp == kMma) {
@@ -307,93 +373,149 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == kLoad) {
-    if (lane == 0) {
-      for (int i = 0; i < C::kRing; ++i) {
-        mbar_init(full + i, 1);
-        mbar_init(empty + i, kTiles);
-      }
-      mbar_init(q_full, 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(s_full + i, 1);
-        mbar_init(s_read + i, 4);  // the four softmax warps of a tile
-        mbar_init(p_full + 2 * i, 4);
-        mbar_init(p_full + 2 * i + 1, 4);
-        mbar_init(o_full + i, 1);
-        mbar_init(pv_done + i, 1);
-        mbar_init(turn + i, 1);
-      }
-      mbar_init(all_done, kTiles);
-      *abort_flag = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kLoad && lane == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kTiles);
     }
-  } else if (warp == 0) {
-    pdl_wait();
-    int b = -1, t = 0;
-    if (!find_item(a, kTiles * p.tpt, blockIdx.x / p.heads, &b, &t)) b = -1;
-    if (lane == 0) {
-      item[0] = b;
-      item[1] = t;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_free + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_read + i, 4);  // the four softmax warps of a tile
+      mbar_init(p_full + 2 * i, 4);
+      mbar_init(p_full + 2 * i + 1, 4);
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, 4);
+      mbar_init(pv_done + i, 1);
+      mbar_init(turn + i, 1);
+      mbar_init(item_full + i, 1);
+      mbar_init(item_free + i, 1 + kTiles + 4 + C::kSoftmax);  // every warp that reads items
+      mbar_init(ml_full + i, 4);
+      mbar_init(ml_free + i, 4);
     }
+    mbar_init(all_done, kTiles);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
   pdl_wait();
   const uint32_t tmem = *tmem_slot;
-  const int b = item[0];
-  if (b >= 0) {
-    const Span sp = span_of(a, b);
-    // heads fastest: the long items of all of them come first
-    const int blocks = p.G / p.hg, head = (int)blockIdx.x % p.heads;
-    const int h = head / blocks, hq0 = h * p.G + (head % blocks) * p.hg;
-    // Q tile s: queries tok(s) .. tok(s) + tpt - 1 of the sequence; keys of its
-    // last query; K tiles
-    int first[kTiles], keys[kTiles], n[kTiles];
-#pragma unroll
-    for (int s = 0; s < kTiles; ++s) {
-      first[s] = (item[1] * kTiles + s) * p.tpt;
-      const int last = min(first[s] + p.tpt, sp.nq) - 1;
-      keys[s] = a.causal ? min(sp.nk, sp.nk - sp.nq + last + 1) : sp.nk;
-      n[s] = first[s] < sp.nq && keys[s] > 0 ? (keys[s] + kKeys - 1) / kKeys : 0;
-    }
-    int most = n[0];
-    if (kTiles == 2) most = max(most, n[kTiles - 1]);
-    const uint32_t ring = smem_addr(smem + C::kOffRing), qs = smem_addr(smem);
-    bool ok = true;
+  const uint32_t ring = smem_addr(smem + C::kOffRing), qs = smem_addr(smem);
+  float2* sums = reinterpret_cast<float2*>(smem + C::kOffSums);
+  bool ok = true;
 
-    if (warp >= C::kSoftmax) {
-      if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  int seen = 0;  // items read
+  auto read_item = [&](Item& it, bool one_lane) {
+    const bool there = mbar_wait(item_full + (seen & 1), (seen >> 1) & 1, abort_flag);
+    ok = one_lane ? there : __all_sync(~0u, there);
+    if (!ok) return false;
+    const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
+    int* to = reinterpret_cast<int*>(&it);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = from[i];
+    if (!one_lane) __syncwarp();
+    if (one_lane || lane == 0) mbar_arrive(item_free + (seen & 1));
+    ++seen;
+    return it.b >= 0;
+  };
+  if (warp >= kLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+  if (warp == kPlan) {
+    // ---- the items of this CTA, one ahead of their use, and their Q tiles, into L2 at
+    // once and into shared memory when the tile before has been read ------------------
+    int qn[kTiles] = {};  // Q tiles loaded
+    const int per = p.heads * p.splits, run = kTiles * p.tpt;
+    Walk walk = walk_from_top(a, run);
+    for (int round = 0; ok; ++round) {
+      // long items first, dealt out there and back, so that the CTAs' sums are alike
+      const int i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      Item it;
+      // heads fastest: the long items of all of them come first
+      const int n = i / per, sub = i - n * per, t_last = walk.level;
+      it.b = -1;
+      if (t_last >= 0 && walk_to(a, run, n, walk, &it.b)) {
+        const int t = walk.level;
+        const Span sp = span_of(a, it.b);
+        const int blocks = p.G / p.hg, head = sub % p.heads;
+        it.q0 = sp.q0, it.nq = sp.nq, it.k0 = sp.k0, it.nk = sp.nk;
+        it.first = t * kTiles * p.tpt;
+        it.h = head / blocks;
+        it.hq0 = it.h * p.G + (head % blocks) * p.hg;
+        it.split = sub / p.heads;
+        // the parts are equal numbers of tiles of the last Q tile's keys
+        auto keys = [&](int queries) {
+          const int last = min(queries, it.nq) - 1;
+          return a.causal ? min(it.nk, it.nk - it.nq + last + 1) : it.nk;
+        };
+        const int most = keys(it.first + kTiles * p.tpt);
+        const int part = most > 0 ? ((most + kKeys - 1) / kKeys + p.splits - 1) / p.splits : 0;
+        it.lo = it.split * part;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          it.keys[s] = keys(it.first + (s + 1) * p.tpt);
+          const int n = it.first + s * p.tpt < it.nq && it.keys[s] > 0 ? (it.keys[s] + kKeys - 1) / kKeys : 0;
+          it.n[s] = s < kTiles ? max(0, min(n, it.lo + part) - it.lo) : 0;
+        }
+      }
+      if (seen >= 2)
+        ok = __all_sync(~0u, mbar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, abort_flag));
+      if (!ok) break;
+      if (lane == 0) {
+        volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
+        const int* from = reinterpret_cast<const int*>(&it);
+#pragma unroll
+        for (int e = 0; e < (int)(sizeof(Item) / 4); ++e) to[e] = from[e];
+        mbar_arrive(item_full + (seen & 1));
+      }
+      __syncwarp();
+      ++seen;
+      if (it.b < 0) break;
+#pragma unroll
+      for (int s = 0; s < kTiles; ++s) {
+        if (it.n[s] == 0) continue;
+        const int y = it.q0 + it.first + s * p.tpt;
+        if (lane < D / 64) tma_3d_prefetch(&map_q, 64 * lane, it.hq0, y);
+        if (qn[s] > 0) ok = ok && __all_sync(~0u, mbar_wait(q_free + s, (qn[s] - 1) & 1, abort_flag));
+        if (!ok) break;
+        ++qn[s];
+        if (lane == 0) {
+          mbar_expect_tx(q_full + s, (uint32_t)(p.hg * p.tpt * D * 2));
+          for (int c = 0; c < D / 64; ++c)
+            tma_3d(qs + s * C::kQ + c * kRows * 128, &map_q, 64 * c, it.hq0, y, q_full + s);
+        }
+        __syncwarp();
+      }
     }
-    if (warp == kLoad) {
-      // ---- loads: Q, then K and V tiles through the ring in the order of their use:
-      // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
-      if (lane == 0 && most > 0) {
-        const int rows = p.hg * p.tpt;
-        int tiles = 0;
-        for (int s = 0; s < kTiles; ++s) tiles += n[s] > 0;
-        mbar_expect_tx(q_full, (uint32_t)(tiles * rows * D * 2));
-        for (int s = 0; s < kTiles; ++s)
-          if (n[s] > 0)
-            for (int c = 0; c < D / 64; ++c)
-              tma_3d(qs + s * C::kQ + c * kRows * 128, &map_q, 64 * c, hq0, sp.q0 + first[s], q_full);
-        int u = 0;  // units issued
+    for (int s = 0; s < kTiles; ++s)  // the copies land before the CTA ends
+      if (qn[s] > 0) static_cast<void>(mbar_wait(q_full + s, (qn[s] - 1) & 1, nullptr));
+  } else if (warp == kLoad) {
+    // ---- loads: K and V tiles through the ring in the order of their use:
+    // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
+    if (lane == 0) {
+      int u = 0;  // units issued
+      Item it;
+      while (read_item(it, true)) {
+        const int most = max(it.n[0], it.n[1]);
+        if (most == 0) continue;
+        const int key0 = it.k0 + it.lo * kKeys;
         auto load = [&](const CUtensorMap* map, int x, int y, int rows, int blocks) {
           const int st = u % C::kRing, round = u / C::kRing;
           if (round > 0) ok = mbar_wait(empty + st, (round - 1) & 1, abort_flag);
           if (!ok) return;
           mbar_expect_tx(full + st, C::kUnit);
           for (int c = 0; c < blocks; ++c)  // boxes of 64 columns
-            tma_3d(ring + st * C::kUnit + c * rows * 128, map, x + 64 * c, h, y, full + st);
+            tma_3d(ring + st * C::kUnit + c * rows * 128, map, x + 64 * c, it.h, y, full + st);
           ++u;
         };
         auto load_k = [&](int j) {
           for (int k = 0; k < C::kUnits && ok; ++k)
-            load(&map_k, k * C::kCols, sp.k0 + j * kKeys, kKeys, C::kCols / 64);
+            load(&map_k, k * C::kCols, key0 + j * kKeys, kKeys, C::kCols / 64);
         };
         auto load_v = [&](int j) {
           for (int k = 0; k < C::kUnits && ok; ++k)
-            load(&map_v, 0, sp.k0 + j * kKeys + k * C::kVKeys, C::kVKeys, D / 64);
+            load(&map_v, 0, key0 + j * kKeys + k * C::kVKeys, C::kVKeys, D / 64);
         };
         load_k(0);
         for (int j = 0; j < most && ok; ++j) {
@@ -401,35 +523,49 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           load_v(j);
           if (kTiles == 2 && j + 1 < most) load_k(j + 1);
         }
-        // whatever becomes of the MMAs, the copies land before the CTA ends
-        for (int v = max(0, u - C::kRing); v < u; ++v)
-          static_cast<void>(mbar_wait(full + v % C::kRing, (v / C::kRing) & 1, nullptr));
-        static_cast<void>(mbar_wait(q_full, 0, nullptr));
+        if (!ok) break;
       }
-    } else if (warp >= kMma && warp < kMma + kTiles) {
-      // ---- MMAs.  The warp stays converged and one lane issues each product in
-      // straight-line code.  The tensor core takes few MMAs ahead, so a pause in
-      // the issue is a pause in the products: with two Q tiles each has an issuing
-      // warp of its own, and one waits for barriers while the other's MMAs run ----
-      const int s = warp - kMma, tiles = n[s];
-      auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(~0u, mbar_wait(bar, phase & 1, abort_flag));
-      };
-      auto arrived = [&](int u) { wait(full + u % C::kRing, u / C::kRing); };  // ring unit u
+      // whatever becomes of the MMAs, the copies land before the CTA ends
+      for (int v = max(0, u - C::kRing); v < u; ++v)
+        static_cast<void>(mbar_wait(full + v % C::kRing, (v / C::kRing) & 1, nullptr));
+    }
+  } else if (warp >= kMma && warp < kMma + kTiles) {
+    // ---- MMAs.  The warp stays converged and an elected lane issues each product
+    // in straight-line code (an MMA costs the issue 110 clocks in a lane's own
+    // branch, where its operands cannot be uniform registers, and the tensor core
+    // 64).  The tensor core takes few MMAs ahead, so a pause in the issue is a
+    // pause in the products: with two Q tiles each has an issuing warp of its own,
+    // and one waits for barriers while the other's MMAs run -------------------------
+    const int s = warp - kMma;
+    auto wait = [&](uint64_t* bar, int phase) {
+      ok = ok && __all_sync(~0u, mbar_wait(bar, phase & 1, abort_flag));
+    };
+    auto arrived = [&](int u) { wait(full + u % C::kRing, u / C::kRing); };  // ring unit u
+    // of the items before: ring units, tiles of this Q tile, rounds of turns, outputs
+    // of this Q tile
+    int ub = 0, done = 0, rounds = 0, outs = 0;
+    Item it;
+    while (read_item(it, false)) {
+      const int tiles = s ? it.n[1] : it.n[0], theirs = s ? it.n[0] : it.n[1], most = max(tiles, theirs);
+      if (most == 0) continue;
       // first unit of K_j and V_j (with one Q tile, past the last K there is no
       // K_(j + 1) before V_j)
-      auto k_unit = [&](int j) { return (kTiles == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * C::kUnits; };
-      auto v_unit = [&](int j) {
-        return (kTiles == 2 || j == most - 1 ? 2 * j + 1 : 2 * j + 2) * C::kUnits;
+      auto k_unit = [&](int j) {
+        return ub + (kTiles == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * C::kUnits;
       };
+      auto v_unit = [&](int j) {
+        return ub + (kTiles == 2 || j == most - 1 ? 2 * j + 1 : 2 * j + 2) * C::kUnits;
+      };
+      auto slot_of = [&](int j) { return kTiles == 1 ? (done + j) & 1 : s; };
+      auto use_of = [&](int j) { return kTiles == 1 ? (done + j) >> 1 : done + j; };
       // A K or V tile that the other Q tile does not use is released for both.
       auto release = [&](int j, int st) {
         mma_commit(empty + st);
-        if (kTiles == 2 && j >= n[kTiles - 1 - s]) mma_commit(empty + st);
+        if (kTiles == 2 && j >= theirs) mma_commit(empty + st);
       };
       // S of tile j into its slot: unit k of the columns
       auto qk = [&](int j, int k) {
-        const int slot = kTiles == 1 ? j & 1 : s, st = (k_unit(j) + k) % C::kRing;
+        const int slot = slot_of(j), st = (k_unit(j) + k) % C::kRing;
         const uint64_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
         const uint64_t kd = tile_desc(ring + st * C::kUnit, 16);
 #pragma unroll
@@ -443,11 +579,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               mma_ss<true>(tmem + slot * kKeys, qd + at, kd + at, idesc<kKeys, false>());
           }
         release(j, st);
-        if (k == C::kUnits - 1) mma_commit(s_full + slot);
+        if (k == C::kUnits - 1) {
+          mma_commit(s_full + slot);
+          if (j == tiles - 1) mma_commit(q_free + s);
+        }
       };
       // O += P V of tile j over its first or second 64 keys
       auto pv = [&](int j, int half) {
-        const int slot = kTiles == 1 ? j & 1 : s;
+        const int slot = slot_of(j);
         const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
         const uint32_t d = tmem + 2 * kKeys + s * D;
         const int st = (v_unit(j) + (C::kUnits == 2 ? half : 0)) % C::kRing;
@@ -466,107 +605,135 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (j == tiles - 1) mma_commit(o_full + s);
         }
       };
-      if (tiles > 0) {
-        wait(q_full, 0);
-        auto scores = [&](int j) {
+      auto scores = [&](int j) {
+        if (C::kApart && done + j > 0) wait(s_read + s, done + j - 1);  // S before it has been read
 #pragma unroll
-          for (int k = 0; k < C::kUnits; ++k) {
-            arrived(k_unit(j) + k);
-            fence_after();
-            if (ok && elected()) qk(j, k);
-            __syncwarp();
-          }
-        };
-        scores(0);
-        for (int j = 0; j < tiles && ok; ++j) {
-          const bool more = j + 1 < tiles;
-          const int slot = kTiles == 1 ? j & 1 : s, use = kTiles == 1 ? j >> 1 : j;
-          if (more && kTiles == 1) scores(j + 1);
-          if (more && C::kApart) {
-            wait(s_read + slot, use);
-            scores(j + 1);
-          }
-          for (int k = 0; k < C::kUnits; ++k) arrived(v_unit(j) + k);
-          constexpr bool kAfter = kTiles == 2 && !C::kApart;  // the next S goes where P was
-          if (more && kAfter) arrived(k_unit(j + 1));
-          wait(p_full + 2 * slot, use);
-          // Two Q tiles take turns: issued side by side their MMAs would alternate,
-          // both S would arrive together and the tensor core would stand still
-          // during both softmaxes (540 for 442 us, 8192 tokens).
-          if (kAfter) {
-            if (s == 1 && j < n[0]) wait(turn + s, j);
-            if (s == 0 && j > 0 && j - 1 < n[kTiles - 1]) wait(turn + s, j - 1);
-          }
+        for (int k = 0; k < C::kUnits; ++k) {
+          arrived(k_unit(j) + k);
           fence_after();
+          if (ok && elected()) qk(j, k);
+          __syncwarp();
+        }
+      };
+      if (tiles > 0) {
+        wait(q_full + s, outs);
+        scores(0);
+      }
+      for (int j = 0; j < (kAfter ? most : tiles) && ok; ++j) {
+        const bool mine = j < tiles, more = j + 1 < tiles;
+        const int slot = slot_of(j), use = use_of(j);
+        if (mine) {
+          if (more && !kAfter) scores(j + 1);
+          for (int k = 0; k < C::kUnits; ++k) arrived(v_unit(j) + k);
+          if (more && kAfter) arrived(k_unit(j + 1));
+          if (j == 0 && outs > 0) wait(o_free + s, outs - 1);
+          wait(p_full + 2 * slot, use);
+        }
+        // Two Q tiles take turns: issued side by side their MMAs would alternate,
+        // both S would arrive together and the tensor core would stand still
+        // during both softmaxes (540 for 442 us, 8192 tokens).
+        if (kAfter) {
+          if (s == 1) wait(turn + s, rounds + j);
+          if (s == 0 && rounds + j > 0) wait(turn + s, rounds + j - 1);
+        }
+        fence_after();
+        if (mine) {
           if (ok && elected()) pv(j, 0);
           __syncwarp();
           wait(p_full + 2 * slot + 1, use);
           fence_after();
           if (ok && elected()) {
             pv(j, 1);
-            if (kAfter) {
-              if (more) qk(j + 1, 0);
-              mbar_arrive(turn + 1 - s);
-            }
+            if (kAfter && more) qk(j + 1, 0);
           }
           __syncwarp();
         }
+        if (kAfter && ok && lane == 0) mbar_arrive(turn + 1 - s);
       }
-      if (elected()) mma_commit(all_done);
-      __syncwarp();
-    } else if (warp < C::kSoftmax) {
-      // ---- softmax: thread = row of Q tile s ----------------------------------------
-      if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-      const int s = kTiles == 1 ? 0 : warp >> 2, quarter = warp & 3;
-      const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-      const int row = 32 * quarter + lane, tok = first[s] + row / p.hg;
-      const bool mine = row < p.hg * p.tpt && tok < sp.nq;
-      // keys this row sees, and those its tile's first row sees
-      const int sees = a.causal ? min(sp.nk, sp.nk - sp.nq + tok + 1) : sp.nk;
-      const int all_see = a.causal ? min(sp.nk, sp.nk - sp.nq + first[s] + 1) : sp.nk;
-      const float scale2 = a.scale * kLog2e;
-      const uint32_t o_at = tmem + lanes + 2 * kKeys + s * D;
+      if (!ok) break;
+      ub += 2 * most * C::kUnits;
+      done += tiles;
+      rounds += most;
+      outs += tiles > 0;
+    }
+    if (elected()) mma_commit(all_done);
+    __syncwarp();
+  } else if (warp < C::kSoftmax) {
+    // ---- softmax: thread = row of Q tile s ------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    const int s = kTiles == 1 ? 0 : warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int row = 32 * quarter + lane;
+    const float scale2 = a.scale * kLog2e;
+    const uint32_t o_at = tmem + lanes + 2 * kKeys + s * D;
+    // this row's token of the tile, and those of the warp's first and last row
+    const int my_tok = row / p.hg, tok_lo = 32 * quarter / p.hg, tok_hi = (32 * quarter + 31) / p.hg;
+    int done = 0, outs = 0;  // tiles and items before this one
+    Item it;
+    while (read_item(it, false)) {
+      const int first = it.first + s * p.tpt, tiles = s ? it.n[1] : it.n[0];
+      // keys of this part that a row sees: this one, the warp's first and its last
+      auto sees_of = [&](int t) {
+        return (a.causal ? min(it.nk, it.nk - it.nq + first + t + 1) : it.nk) - it.lo * kKeys;
+      };
+      const int sees = sees_of(my_tok), least = sees_of(tok_lo), best = sees_of(tok_hi);
       float m = kNegInf;  // what P refers to, in units of log2
       bool ready = false;
       uint64_t sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-      for (int j = 0; j < n[s] && ok; ++j) {
-        const int slot = kTiles == 1 ? j & 1 : s, use = kTiles == 1 ? j >> 1 : j;
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int g = done + j, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
         const uint32_t at = tmem + lanes + slot * kKeys;
         const uint32_t p_at = C::kApart ? tmem + lanes + 384 + slot * 64 : at;
         ok = __all_sync(~0u, ready || mbar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
-        uint32_t v[kKeys];
+        // The second 64 columns are read twice, for the maximum and again for their
+        // exponentials: 128 values held beside P's do not fit the registers.
+        uint32_t v[64];
+        auto read_s = [&](uint32_t* to, int c0) {
+          tmem_ld32(at + c0, to);
+          tmem_ld32(at + c0 + 32, to + 32);
+        };
+        const int left = sees - j * kKeys, left_lo = least - j * kKeys, left_hi = best - j * kKeys;
+        // keys past what a row sees: by groups of 32, those that some row does not
+        // see whole
+        auto mask = [&](uint32_t* x, int c0) {
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) tmem_ld32(at + c, v + c);
-        tmem_wait_ld();
-        if constexpr (C::kApart) {
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_read + slot);
+          for (int c = 0; c < 64; c += 32) {
+            if (__builtin_expect(c0 + c + 32 > left_lo, 0)) {
+              const int in = left - c0 - c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e >= in) x[c + e] = 0xff800000u;
+            }
+          }
+        };
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        auto take_max = [&](const uint32_t* x) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        };
+        {
+          uint32_t second[64];
+          read_s(v, 0);
+          read_s(second, 64);
+          tmem_wait_ld();
+          mask(v, 0);
+          take_max(v);
+          if (left_hi > 64) {
+            mask(second, 64);
+            take_max(second);
+          }
         }
-        if ((j + 1) * kKeys > all_see) {
-          const int left = sees - j * kKeys;
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c >= left) v[c] = 0xff800000u;
-        }
-        float top[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top[e] = max3(__uint_as_float(v[3 * e]), __uint_as_float(v[3 * e + 1]),
-                        __uint_as_float(v[3 * e + 2]));
-#pragma unroll
-        for (int c = 12; c < kKeys; c += 2)  // 116 more in pairs, 14 or 15 a chain
-          top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
         const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
         if (j == 0) {
           m = t2;
-        } else if (__any_sync(~0u, t2 > m + kSlack)) {
+        } else if (__builtin_expect(__any_sync(~0u, t2 > m + kSlack), 0)) {
           // O moves to the new maximum once the product with the tile before is
           // done (where S follows P, S says so)
-          if constexpr (kTiles == 1 || C::kApart) {
-            ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
+          if constexpr (!kAfter) {
+            ok = __all_sync(~0u, mbar_wait(pv_done + s, (g - 1) & 1, abort_flag));
             if (!ok) break;
           }
           const float mn = t2 > m + kSlack ? t2 : m;
@@ -590,21 +757,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         const float z = m == kNegInf ? 0.0f : -m;
         const uint64_t zz = pair(z, z), ss = pair(scale2, scale2);
-        auto half_p = [&](int c) {  // keys c .. c + 63
-          uint32_t w[32];
+        auto half_p = [&](int half) {  // of v
+          uint32_t x[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float x0, x1;
-            unpair(fma2(pair(__uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1])), ss, zz), x0, x1);
+            unpair(fma2(pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ss, zz), x0, x1);
             x0 = exp2_fast(x0);
             x1 = exp2_fast(x1);
             sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
-            w[e] = bf16x2(x0, x1);
+            x[e] = bf16x2(x0, x1);
           }
           if constexpr (C::kApart)  // the product with the tile before has read its P
-            if (c == 0 && j > 0)
-              ok = __all_sync(~0u, mbar_wait(pv_done + s, (j - 1) & 1, abort_flag));
-          tmem_st32(p_at + c / 2, w);
+            if (half == 0 && g > 0)
+              ok = __all_sync(~0u, mbar_wait(pv_done + s, (g - 1) & 1, abort_flag));
+          tmem_st32(p_at + 32 * half, x);
         };
         auto publish = [&](int half) {
           tmem_wait_st();
@@ -612,91 +779,151 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full + 2 * slot + half);
         };
+        auto read_all = [&] {  // S may be written again
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read + slot);
+        };
         // The product with V starts on the first half.  The branch is worth more
         // than the work it saves in a last tile: without it the compiler computes
         // both halves before it stores the first.
         half_p(0);
         publish(0);
         {  // whether the next S has arrived: asked now, used at the top
-          const int nj = j + 1, nslot = kTiles == 1 ? nj & 1 : s, nuse = kTiles == 1 ? nj >> 1 : nj;
-          ready = nj < n[s] && mbar_test(s_full + nslot, nuse & 1);
+          const int ng = g + 1, nslot = kTiles == 1 ? ng & 1 : s, nuse = kTiles == 1 ? ng >> 1 : ng;
+          ready = j + 1 < tiles && mbar_test(s_full + nslot, nuse & 1);
         }
-        if (keys[s] - j * kKeys > 64) {
-          half_p(64);
+        if (left_hi > 64) {
+          read_s(v, 64);
+          tmem_wait_ld();
+          if constexpr (C::kApart) read_all();
+          mask(v, 64);
+          half_p(1);
         } else {
+          if constexpr (C::kApart) read_all();
           const uint32_t none[32] = {};
           tmem_st32(p_at + 32, none);
         }
         publish(1);
       }
+      done += tiles;
+      if (!ok) break;
+      if (first >= it.nq) continue;
 
-      // ---- epilogue ----------------------------------------------------------------
+      // the rows' maxima and sums, for the warps that store
       float lo, hi;
       unpair(add2(sum2[0], sum2[1]), lo, hi);
-      const float l = lo + hi;
-      const int64_t tq = sp.q0 + tok;
-      const int hq = hq0 + row % p.hg;
-      const bool some = n[s] > 0;
-      if (ok && some) ok = __all_sync(~0u, mbar_wait(o_full + s, 0, abort_flag));
-      if (ok && first[s] < sp.nq) {
-        fence_after();
-        if (mine && a.lse) a.lse[tq * a.Hq + hq] = l == 0.0f ? kNegInf : m * kLn2 + logf(l);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        // rows go through the dead Q tile so that a row's bytes are stored together
-        unsigned char* stage = smem + s * C::kQ + row * 128;
-        bool bad = false;
+      if (outs > 0) {
+        ok = __all_sync(~0u, mbar_wait(ml_free + s, (outs - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+      ++outs;
+      sums[s * kRows + row] = make_float2(m, lo + hi);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ml_full + s);
+    }
+  } else if (warp < kLoad) {
+    // ---- the output: O over its sum, while the next item is in work ---------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsStore));
+    const int quarter = warp & 3, row = 32 * quarter + lane;
+    const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0, parts = p.splits > 1;
+    const int my_tok = row / p.hg, my_head = row % p.hg;
+    unsigned told = 0, outs = 0;  // bit s: parity of Q tile s's items, of its outputs
+    Item it;
+    while (read_item(it, false)) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32], w[16];
-          if (some) {
-            tmem_ld32(o_at + c, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0 = __uint_as_float(o[e]), x1 = __uint_as_float(o[e + 1]);
-            if (l == 0.0f) x0 = x1 = 0.0f;
-            bad |= !(fabsf(x0) <= 3.4028235e38f) | !(fabsf(x1) <= 3.4028235e38f);
-            w[e / 2] = bf16x2(x0 * inv, x1 * inv);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage + (c / 64) * kRows * 128 +
-                                      ((((c % 64) / 8 + e) ^ (row & 7)) << 4)) =
-                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        }
+      for (int s = 0; s < kTiles; ++s) {
+        const int first = it.first + s * p.tpt, tiles = s ? it.n[1] : it.n[0];
+        if (first >= it.nq) break;
+        const int tok = first + my_tok, hq = it.hq0 + my_head;
+        const bool mine = row < p.hg * p.tpt && tok < it.nq;
+        const int64_t out_row = (int64_t)(it.q0 + tok) * a.Hq + hq;
+        ok = __all_sync(~0u, mbar_wait(ml_full + s, (told >> s) & 1, abort_flag));
+        if (!ok) break;
+        told ^= 1u << s;
+        const float2 ml = sums[s * kRows + row];
         __syncwarp();
-        constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-#pragma unroll 4
-        for (int i = lane; i < 32 * kPieces; i += 32) {
-          const int r = 32 * quarter + i / kPieces, piece = i % kPieces;
-          const int tr = first[s] + r / p.hg;
-          if (r < p.hg * p.tpt && tr < sp.nq)
-            *reinterpret_cast<uint4*>(a.out + ((int64_t)(sp.q0 + tr) * a.Hq + hq0 + r % p.hg) * D +
-                                      8 * piece) =
-                *reinterpret_cast<const uint4*>(smem + s * C::kQ + (piece / 8) * kRows * 128 + r * 128 +
-                                                (((piece % 8) ^ (r & 7)) << 4));
+        if (lane == 0) mbar_arrive(ml_free + s);
+        const float l = ml.y;
+        if (mine) {
+          if (parts)
+            p.ml[(int64_t)it.split * a.Tq * a.Hq + out_row] = ml;
+          else if (a.lse)
+            a.lse[out_row] = l == 0.0f ? kNegInf : ml.x * kLn2 + logf(l);
+        }
+        if (tiles > 0) {
+          ok = __all_sync(~0u, mbar_wait(o_full + s, (outs >> s) & 1, abort_flag));
+          if (!ok) break;
+          outs ^= 1u << s;
+          fence_after();
+        }
+        uint64_t checked = pair(0.0f, 0.0f);
+        if (tiles > 0 || !parts) {
+          const uint32_t o_at = tmem + ((uint32_t)(32 * quarter) << 16) + 2 * kKeys + s * D;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          char* to = parts ? reinterpret_cast<char*>(p.part + ((int64_t)it.split * a.Tq * a.Hq + out_row) * D)
+                           : reinterpret_cast<char*>(a.out + out_row * D);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            if (tiles > 0) {
+              tmem_ld16(o_at + c, o);
+              tmem_wait_ld();
+            }
+            if (l == 0.0f) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0u;
+            }
+            const uint64_t zero2 = pair(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)  // 0 as long as every value is finite
+              checked = fma2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), zero2, checked);
+            if (!mine) continue;
+            if (parts) {
+              store32(to, o, true);
+              store32(to + 32, o + 8, true);
+              to += 64;
+            } else {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float y0, y1;
+                unpair(mul2(pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), pair(inv, inv)),
+                       y0, y1);
+                y[e] = bf16x2(y0, y1);
+              }
+              store32(to, y, aligned32);
+              to += 32;
+            }
+          }
+          if (tiles > 0) {  // the next item's product may come
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free + s);
+          }
         }
         // rows whose sum is finite and whose output is not
-        unsigned again = __ballot_sync(~0u, mine && bad && l == l);
+        float lo, hi;
+        unpair(checked, lo, hi);
+        unsigned again = __ballot_sync(~0u, mine && !(lo + hi == 0.0f) && l == l);
         while (again) {
           const int who = __ffs(again) - 1;
           again &= again - 1;
           __syncwarp();
-          attend_row<D>(a, __shfl_sync(~0u, (int)tq, who), __shfl_sync(~0u, hq, who), h, sp.k0,
-                        sp.k0 + __shfl_sync(~0u, sees, who));
+          const int sees = (a.causal ? min(it.nk, it.nk - it.nq + tok + 1) : it.nk) - it.lo * kKeys;
+          const int key0 = it.k0 + it.lo * kKeys;
+          attend_row<D>(p, it.split, it.q0 + __shfl_sync(~0u, tok, who), __shfl_sync(~0u, hq, who), it.h,
+                        key0, key0 + __shfl_sync(~0u, min(sees, tiles * kKeys), who));
         }
       }
+      if (!ok) break;
     }
-    if (!ok) {
-      *abort_flag = 1;
-      if (lane == 0) atomicOr(status, kDevTimeout);
-    }
-    if (*abort_flag && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
   }
+  if (!ok) {
+    *abort_flag = 1;
+    if (lane == 0) atomicOr(status, kDevTimeout);
+  }
+  if (*abort_flag && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
   fence_before();
   __syncthreads();
   if (warp == kMma) {
@@ -706,30 +933,109 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
+// Joins the parts of each row, in order: a warp a row, rows of the sequences.
+template <int D>
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(Args p) {
+  constexpr int N = D / 32;
+  pdl_release();
+  pdl_wait();
+  const PrefillArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = a.Tq * a.Hq, row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int64_t t = row / a.Hq;
+  if (t < clamped(__ldg(a.cu_q), a.Tq) || t >= clamped(__ldg(a.cu_q + a.B), a.Tq)) return;
+  RowState<D> r;
+  for (int i = 0; i < p.splits; ++i) {
+    const float2 ml = p.ml[i * rows + row];
+    if (ml.y == 0.0f) continue;  // a part without keys: its sums were not written
+    float o[N];
+    const float* from = p.part + (i * rows + row) * D + lane * N;
+    if constexpr (N == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(from);
+      o[0] = v.x, o[1] = v.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from + e);
+        o[e] = v.x, o[e + 1] = v.y, o[e + 2] = v.z, o[e + 3] = v.w;
+      }
+    }
+    r.join(ml.x, ml.y, o);
+  }
+  const float inv = r.l == 0.0f ? 0.0f : 1.0f / r.l;
+  if (a.lse && lane == 0) a.lse[row] = r.l == 0.0f ? kNegInf : r.m * kLn2 + logf(r.l);
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + lane * N + i) = bf16x2(r.o[i] * inv, r.o[i + 1] * inv);
+}
+
+constexpr int64_t kSms = 152;
+
 // The heads of a Q tile: of the divisors of G, the one whose tiles of
 // floor(128 / heads) tokens waste the fewest rows on sequences of the mean
-// length; the most heads where several do (fewer K and V loads a row).
-int heads_of_tile(int64_t G, int64_t B, int64_t Tq) {
-  const double mean = B > 0 ? (double)Tq / (double)B : 1.0;
+// length (one sequence: on it; several: half a run each); the most heads where
+// several do (fewer K and V loads a row).
+int heads_of_tile(int64_t G, int64_t B, int64_t Tq, int tiles) {
+  const double mean = (double)Tq / (double)(B < 1 ? 1 : B < Tq ? B : Tq);
   int best = 1;
   double most = -1.0;
   for (int hg = 1; hg <= G && hg <= kRows; ++hg) {
     if (G % hg) continue;
-    const double tpt = kRows / hg, tiles = mean <= tpt ? 1.0 : mean / tpt;
-    const double use = mean * hg / (kRows * (tiles < 2.0 ? (double)(int)(tiles + 0.999) : tiles + 0.5));
+    const int64_t tpt = kRows / hg, run = tiles * tpt;
+    const double rows = B == 1 ? (double)((Tq + tpt - 1) / tpt * tpt)
+                        : mean < (double)run ? (mean > (double)tpt ? (double)run : (double)tpt)
+                                             : mean + 0.5 * (double)run;
+    const double use = mean / rows * (double)(hg * tpt) / kRows;
     if (use >= most) most = use, best = hg;
   }
   return best;
 }
 
+struct Plan {
+  int hg, tpt, splits;
+  int64_t items, heads;
+};
+
+// Where the items fill less than half the SMs and the keys are long, each
+// item's keys are cut into parts of at least eight tiles, for about one item an
+// SM.  (An item costs about four tiles of its own: with 180 items of up to 55
+// tiles two parts took 84 us and one 78.)  A function of the shapes alone, so
+// the workspace query and the launch agree.
+Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
+  Plan r;
+  const int tiles = D == 256 ? 1 : 2;
+  const int64_t G = Hq / Hkv;
+  r.hg = heads_of_tile(G, B, Tq, tiles);
+  r.tpt = kRows / r.hg;
+  r.heads = Hkv * (G / r.hg);
+  // every sequence has at most one run that is not whole
+  const int64_t run = tiles * r.tpt;
+  r.items = Tq / run + (B < Tq ? B : Tq);
+  const int64_t likely = (B == 1 ? (Tq + run - 1) / run : r.items) * r.heads;
+  const int64_t long_keys = B > 0 ? Tk / B / kKeys / 8 : 0;
+  int64_t n = likely > 0 ? kSms / likely : 1;
+  n = n < long_keys ? n : long_keys;
+  r.splits = (int)(n < 2 ? 1 : n > 32 ? 32 : n);
+  return r;
+}
+
+size_t workspace_of(const Plan& r, int64_t Tq, int64_t Hq, int64_t D) {
+  return r.splits > 1 ? (size_t)r.splits * (size_t)(Tq * Hq) * (size_t)(D * 4 + 8) + 256 : 0;
+}
+
 template <int D>
-cudaError_t launch(const PrefillArgs& a, cudaStream_t st) {
+cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
   using C = Cfg<D>;
+  const Plan plan = plan_of(a.B, a.Tq, a.Tk, a.Hq, a.Hkv, D);
   Args p;
   p.a = a;
   p.G = (int)(a.Hq / a.Hkv);
-  p.hg = heads_of_tile(p.G, a.B, a.Tq);
-  p.tpt = kRows / p.hg;
+  p.hg = plan.hg;
+  p.tpt = plan.tpt;
+  p.splits = plan.splits;
+  p.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~(uintptr_t)255);
+  p.ml = reinterpret_cast<float2*>(p.part + (size_t)plan.splits * a.Tq * a.Hq * D);
   CUtensorMap mq, mk, mv;
   cudaError_t e = encode_tma_heads(&mq, a.q, D, a.Hq, a.Tq, a.q_stride, p.hg, p.tpt);
   if (a.Tk > 0) {
@@ -744,24 +1050,29 @@ cudaError_t launch(const PrefillArgs& a, cudaStream_t st) {
   auto kern = attn_prefill_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  // every sequence has at most one run that is not whole
-  const int64_t run = C::kTiles * p.tpt, items = a.Tq / run + (a.B < a.Tq ? a.B : a.Tq);
-  const int64_t heads = a.Hkv * (p.G / p.hg);
-  if (items * heads > INT32_MAX) return cudaErrorInvalidValue;
-  p.heads = (int)heads;
-  return launch_pdl(kern, dim3((unsigned)(items * heads)), dim3(C::kThreads), C::kSmem, st, mq,
-                    mk, mv, p, status);
+  int64_t work;
+  if (!mul_ok(plan.items, plan.heads * plan.splits, &work) || work > INT32_MAX / 2)
+    return cudaErrorInvalidValue;
+  p.heads = (int)plan.heads;
+  e = launch_pdl(kern, dim3((unsigned)(work < kSms ? work : kSms)), dim3(C::kThreads), C::kSmem, st,
+                 mq, mk, mv, p, status);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  return launch_pdl(attn_prefill_join_kernel<D>, dim3((unsigned)((a.Tq * a.Hq + 7) / 8)), dim3(256), 0,
+                    st, p);
 }
 
 }  // namespace
 
-size_t attn_prefill_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t attn_prefill_workspace(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (B == 0 || Tq == 0) return 0;
+  return workspace_of(plan_of(B, Tq, Tk, Hq, Hkv, D), Tq, Hq, D);
+}
 
-cudaError_t launch_attn_prefill(const PrefillArgs& a, void*, cudaStream_t st) {
+cudaError_t launch_attn_prefill(const PrefillArgs& a, void* ws, cudaStream_t st) {
   switch (a.D) {
-    case 64: return launch<64>(a, st);
-    case 128: return launch<128>(a, st);
-    default: return launch<256>(a, st);
+    case 64: return launch<64>(a, ws, st);
+    case 128: return launch<128>(a, ws, st);
+    default: return launch<256>(a, ws, st);
   }
 }
 
