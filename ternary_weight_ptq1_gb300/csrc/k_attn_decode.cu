@@ -8,13 +8,15 @@
 // 4 head_dim bytes a token and kv head.
 //
 // Split.  The tokens of one (sequence, kv head) are cut into tiles of kT; the
-// tiles of all of them, in order, are dealt to the CTAs in equal runs, so
-// ragged batches keep every SM busy to the end whatever the lengths are.  The
-// lengths are on the device: each CTA adds them up itself.  The part of a
-// (sequence, kv head) inside one CTA's run is a segment; a segment that is a
-// whole (sequence, kv head) writes its output, the others write their maximum,
-// sum and output sums to the workspace and a second kernel joins them in
-// order.
+// tiles of all of them, in order, are dealt to the CTAs in runs of equal cost,
+// so ragged batches keep every SM busy to the end whatever the lengths are.
+// (The start and end of a (sequence, kv head) cost as much as kLead tiles:
+// without them the CTA that got the shortest sequences of a ragged batch took
+// three times as long as the others.)  The lengths are on the device: each CTA
+// adds them up itself.  The part of a (sequence, kv head) inside one CTA's run
+// is a segment; a segment that is a whole (sequence, kv head) writes its
+// output, the others write their maximum, sum and output sums to the workspace
+// and a second kernel joins them in order.
 //
 // Inside a CTA each warp owns its tiles alone: it copies them into a ring of
 // its own in shared memory (cp.async, the copies of the next tiles always in
@@ -48,6 +50,7 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kWarps = 4;
+constexpr int kLead = 16;
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100, the smallest reference value scale
 constexpr float kPScale = 1024.0f;               // fp16 probabilities are stored times this
 
@@ -55,10 +58,10 @@ template <Act T, int D, bool kI8, int kBlocks>
 struct Cfg {
   static constexpr int kT = kI8 || D == 64 ? 32 : 16;  // tokens of a tile
   static constexpr int kRow = D * (kI8 ? 1 : 2);       // bytes of a cached row
-  static constexpr int kChunks = kRow / 16;
+  static constexpr int kChunks = kRow / 16;            // 16-byte pieces of a row
   static constexpr int kTile = kT * kRow;
   static constexpr int kStage = 2 * kTile + (kI8 ? 2 * kT * 4 : 0);
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr bool kThree = T == Act::F32 && !kI8;
   static constexpr bool kFresh = T == Act::F32 || kBlocks > 1;
   static constexpr int kHeads = 8 * kBlocks;            // query heads a warp serves
@@ -92,6 +95,7 @@ struct Args {
   float2* ml;     // [2 ctas][heads]
   Note* note;     // [ctas]
   int G, VH, HC;  // query heads of a kv head; row blocks in all, of one kv head
+  bool whole;     // pages hold whole tiles
 };
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -174,20 +178,30 @@ __device__ __forceinline__ int length(const DecodeArgs& a, int b) {
   return n < 0 ? 0 : n > most ? (int)most : n;
 }
 
+// The units a (sequence, row block) of n tiles is dealt out in: kLead units for
+// its start, then its tiles.
+__device__ __forceinline__ int units(int n) { return n ? n + kLead : 0; }
+
 // The part of one (sequence, row block) inside a CTA's run: tiles t0 .. t1 - 1
 // of n.  b < 0: past the end of the run.
 struct Segment {
   int b, vh, t0, t1, n, len;
-  int64_t u;  // tile t0's place among all
+  int64_t u;  // its first unit's place among all
 };
+
+// The tiles of the segment's (sequence, row block) in units [u0, u1); false: none.
+__device__ __forceinline__ bool clip(Segment& s, int64_t u0, int64_t u1) {
+  s.t0 = (int)max((int64_t)0, u0 - s.u - kLead);
+  s.t1 = (int)min((int64_t)s.n, u1 - s.u - kLead);
+  return s.t0 < s.t1;
+}
 
 template <int kT>
 __device__ __forceinline__ void next_segment(Segment& s, const Args& p, int64_t u1) {
-  s.u += s.t1 - s.t0;
-  s.t0 = 0;
+  s.u += units(s.n);
+  s.t0 = s.t1 = 0;
   if (s.u >= u1) {
     s.b = -1;
-    s.t1 = 0;
     return;
   }
   if (++s.vh == p.VH) {
@@ -196,7 +210,7 @@ __device__ __forceinline__ void next_segment(Segment& s, const Args& p, int64_t 
     while (s.len == 0);
     s.n = (s.len + kT - 1) / kT;
   }
-  s.t1 = (int)min((int64_t)s.n, u1 - s.u);
+  if (!clip(s, s.u, u1)) s.b = -1;  // the run ends before its first tile
 }
 
 template <Act T>
@@ -231,7 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
   // ---- the run of this CTA ---------------------------------------------------------
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kOffScan);  // [2][kWarps]
   int64_t mine = 0;
-  for (int b = tid; b < a.B; b += kWarps * 32) mine += (length(a, b) + kT - 1) / kT;
+  for (int b = tid; b < a.B; b += kWarps * 32) mine += units((length(a, b) + kT - 1) / kT);
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // no key: 0 and -infinity
     if (length(a, b) == 0) {
       for (int64_t e = 4 * tid; e < a.Hq * D; e += 4 * kWarps * 32)
@@ -247,21 +261,19 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += scan[w];
   total *= p.VH;
-  // equal runs, of whole rounds of the CTA's warps
+  // runs of equal cost, of whole rounds of the CTA's warps
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
   per = (per + kWarps - 1) / kWarps * kWarps;
   const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, total);
-  if (u0 >= total) {
-    if (tid == 0) p.note[blockIdx.x] = Note{-1, 0, 0, 0};
-    return;
-  }
-  // the sequence that holds tile u0: sequences are added up kWarps * 32 at a time
-  Segment seg{-1, 0, 0, 0, 0, 0, u0};
+  if (tid == 0) p.note[blockIdx.x] = Note{-1, 0, 0, 0};
+  if (u0 >= total) return;
+  // the sequence that holds unit u0: sequences are added up kWarps * 32 at a time
+  Segment seg{-1, 0, 0, 0, 0, 0, 0};
   int* found = reinterpret_cast<int*>(scan + 2 * kWarps);
   if (tid == 0) *found = -1;
   for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
     const int64_t b = b0 + tid;
-    const int n = b < a.B ? (length(a, (int)b) + kT - 1) / kT : 0;
+    const int n = b < a.B ? units((length(a, (int)b) + kT - 1) / kT) : 0;
     int64_t incl = (int64_t)n * p.VH;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
@@ -291,9 +303,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     const int64_t in = u0 - scan[kWarps];
     seg.len = length(a, seg.b);
     seg.n = (seg.len + kT - 1) / kT;
-    seg.vh = (int)(in / seg.n);
-    seg.t0 = (int)(in - (int64_t)seg.vh * seg.n);
-    seg.t1 = (int)min((int64_t)seg.n, seg.t0 + (u1 - u0));
+    seg.vh = (int)(in / units(seg.n));
+    seg.u = scan[kWarps] + (int64_t)seg.vh * units(seg.n);
+    // (a run that ends within its first kLead units has no tile)
+    if (!clip(seg, u0, u1)) seg.b = -1;
   }
 
   // ---- the ring --------------------------------------------------------------------
@@ -309,33 +322,57 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     }
   };
   settle();
+  // where this lane's piece (16 bytes) of a group of 32 pieces goes: the piece's
+  // place in its row is exchanged by row, so that eight rows read together use
+  // different banks
+  auto place = [&](int i) {
+    const int r = (i * 32 + lane) / C::kChunks, c = lane % C::kChunks;
+    return (uint32_t)(r * C::kRow + ((c ^ (C::kChunks >= 8 ? r & 7 : (r >> 1) & 3)) << 4));
+  };
   auto prefetch = [&](int stage) {
     if (ahead.b >= 0) {
-      const int j = at * kT + (lane % kT);
-      int64_t row = -1;
-      bool wrong = false;
-      if (j < ahead.len) {
-        const int page = __ldg(a.table + ahead.b * a.table_width + (unsigned)j / (unsigned)ps);
-        wrong = (unsigned)page >= (unsigned)a.c.pages;
-        if (!wrong) row = ((int64_t)page * heads + ahead.vh / p.HC) * ps + (unsigned)j % (unsigned)ps;
-      }
-      const uint32_t any = __ballot_sync(~0u, wrong);
-      if (lane == 0) bad[stage] = any;
       const uint32_t dst = ring_at + stage * C::kStage;
+      const int32_t* pages = a.table + ahead.b * a.table_width;
+      const int j0 = at * kT, head = ahead.vh / p.HC;
+      if (p.whole && j0 + kT <= ahead.len) {  // a tile inside one page: one stretch of rows
+        const int page = __ldg(pages + (unsigned)j0 / (unsigned)ps);
+        const bool in = (unsigned)page < (unsigned)a.c.pages;
+        if (lane == 0) bad[stage] = !in;
+        const int64_t row = ((int64_t)(in ? page : 0) * heads + head) * ps + (unsigned)j0 % (unsigned)ps;
+        const char* k = static_cast<const char*>(a.c.k) + row * C::kRow + lane * 16;
+        const char* v = static_cast<const char*>(a.c.v) + row * C::kRow + lane * 16;
 #pragma unroll
-      for (int i = 0; i < kT * C::kChunks / 32; ++i) {
-        const int r = (i * 32 + lane) / C::kChunks, c = lane % C::kChunks;
-        const int64_t src = __shfl_sync(~0u, row, r);
-        const uint32_t to = dst + r * C::kRow +
-                            ((c ^ (C::kChunks >= 8 ? r & 7 : (r >> 1) & 3)) << 4);
-        const int64_t off = (src < 0 ? 0 : src) * C::kRow + c * 16;
-        copy16(to, static_cast<const char*>(a.c.k) + off, src >= 0);
-        copy16(to + C::kTile, static_cast<const char*>(a.c.v) + off, src >= 0);
-      }
-      if constexpr (kI8) {
-        const int64_t off = row < 0 ? 0 : row;
-        copy4(dst + 2 * C::kTile + 4 * lane, a.c.k_scale + off, row >= 0);
-        copy4(dst + 2 * C::kTile + 4 * kT + 4 * lane, a.c.v_scale + off, row >= 0);
+        for (int i = 0; i < kT * C::kChunks / 32; ++i) {
+          copy16(dst + place(i), k + i * 512, true);
+          copy16(dst + place(i) + C::kTile, v + i * 512, true);
+        }
+        if constexpr (kI8) {
+          copy4(dst + 2 * C::kTile + 4 * lane, a.c.k_scale + row + lane, true);
+          copy4(dst + 2 * C::kTile + 4 * kT + 4 * lane, a.c.v_scale + row + lane, true);
+        }
+      } else {
+        const int j = j0 + (lane % kT);
+        int64_t row = -1;
+        bool wrong = false;
+        if (j < ahead.len) {
+          const int page = __ldg(pages + (unsigned)j / (unsigned)ps);
+          wrong = (unsigned)page >= (unsigned)a.c.pages;
+          if (!wrong) row = ((int64_t)page * heads + head) * ps + (unsigned)j % (unsigned)ps;
+        }
+        const uint32_t any = __ballot_sync(~0u, wrong);
+        if (lane == 0) bad[stage] = any;
+#pragma unroll
+        for (int i = 0; i < kT * C::kChunks / 32; ++i) {
+          const int64_t src = __shfl_sync(~0u, row, (i * 32 + lane) / C::kChunks);
+          const int64_t off = (src < 0 ? 0 : src) * C::kRow + lane % C::kChunks * 16;
+          copy16(dst + place(i), static_cast<const char*>(a.c.k) + off, src >= 0);
+          copy16(dst + place(i) + C::kTile, static_cast<const char*>(a.c.v) + off, src >= 0);
+        }
+        if constexpr (kI8) {
+          const int64_t off = row < 0 ? 0 : row;
+          copy4(dst + 2 * C::kTile + 4 * lane, a.c.k_scale + off, row >= 0);
+          copy4(dst + 2 * C::kTile + 4 * kT + 4 * lane, a.c.v_scale + off, row >= 0);
+        }
       }
       at += kWarps;
       settle();
@@ -349,7 +386,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
   uint2* q3 = reinterpret_cast<uint2*>(smem + C::kOffQ3);
   float* qfac = reinterpret_cast<float*>(smem + C::kOffF);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-  bool first = true;  // the run's first segment
 
   while (seg.b >= 0) {
     const int h0 = (seg.vh / p.HC) * p.G, r0 = (seg.vh % p.HC) * C::kHeads;
@@ -395,6 +431,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       }
     }
     __syncthreads();
+    {  // the next segment's query rows, into L2
+      Segment nx = seg;
+      next_segment<kT>(nx, p, u1);
+      constexpr int kBytes = D * (T == Act::F32 ? 4 : 2);
+      if (nx.b >= 0 && tid < C::kHeads * (kBytes / 128)) {
+        const int r = (nx.vh % p.HC) * C::kHeads + tid / (kBytes / 128);
+        if (r < p.G) {
+          const char* q = static_cast<const char*>(a.q) +
+                          (nx.b * a.q_stride + (int64_t)((nx.vh / p.HC) * p.G + r) * D) * (kBytes / D);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + tid % (kBytes / 128) * 128));
+        }
+      }
+    }
+
     // head 8 h + g of the block: its maximum and sum so far, and its output
     // (first terms' rows, and without kFresh the second terms' rows apart)
     float fac[kBlocks], m[kBlocks], l[kBlocks], vref = kTiny;
@@ -619,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     if (lane == 0) where[warp] = (warp * C::kStages + stage) * C::kStage;
     __syncthreads();
     const bool whole = seg.t0 == 0 && seg.t1 == seg.n;
-    const int slot = 2 * blockIdx.x + (first && seg.t0 > 0 ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (seg.t0 > 0 ? 0 : 1);
     for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), d4 = i % (D / 4);
       float2 w[kWarps];
@@ -656,12 +706,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       }
     }
     __syncthreads();
-    if (tid == 0 && seg.u + (seg.t1 - seg.t0) >= u1) {  // the run's last segment
-      const int64_t end = seg.u + (seg.n - seg.t0);      // its (sequence, row block)'s end
-      const bool goes_on = seg.t1 < seg.n && !(first && seg.t0 > 0);
-      p.note[blockIdx.x] = goes_on ? Note{seg.b, seg.vh, (int)((end - 1) / per), 0} : Note{-1, 0, 0, 0};
-    }
-    first = false;
+    // a (sequence, row block) that begins here and goes on in the next CTAs
+    if (tid == 0 && seg.t0 == 0 && seg.t1 < seg.n)
+      p.note[blockIdx.x] = Note{seg.b, seg.vh, (int)((seg.u + units(seg.n) - 1) / per), 0};
     next_segment<kT>(seg, p, u1);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -738,6 +785,7 @@ cudaError_t launch(const DecodeArgs& a, void* ws, cudaStream_t st) {
   p.G = (int)(a.Hq / a.c.kv_heads);
   p.HC = (p.G + C::kHeads - 1) / C::kHeads;
   p.VH = (int)a.c.kv_heads * p.HC;
+  p.whole = a.c.page_tokens % C::kT == 0;
   p.part = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.part + (size_t)2 * kCtas * C::kHeads * D);
   p.note = reinterpret_cast<Note*>(p.ml + (size_t)2 * kCtas * C::kHeads);
