@@ -7,8 +7,8 @@
 // values alone; the row stands for c_d s.  Both kernels move each byte once
 // and compute a few operations a value: HBM bounds them, the launch at a
 // decode step's sizes.  A thread holds eight consecutive values (16 or 32
-// bytes in, 8 or 16 out), so head_dim / 8 neighbouring threads share a row
-// and its maximum is three to five shuffles.
+// bytes in, 8 or 16 out) of a key and the same of its value, so head_dim / 8
+// neighbouring threads share a row and its maximum is three to five shuffles.
 #include <cuda_bf16.h>
 
 #include "ptq_internal.cuh"
@@ -16,28 +16,50 @@
 namespace ptq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kVec = 8;  // values a thread holds of a row
+
+// Division of 0 <= n < 2^31 by a fixed d: with 2^s >= d and m = ceil(2^(31 + s)
+// / d), the excess n (m d - 2^(31 + s)) stays below 2^(31 + s), so n m >> (31 +
+// s) is the quotient.  (The compiler's division by a variable took a third of
+// the kernels' instructions.)
+struct Divider {
+  uint32_t m;
+  int shift, d;
+  explicit Divider(int64_t by) : d((int)by) {
+    int s = 0;
+    while (((int64_t)1 << s) < by) ++s;
+    shift = 31 + s;
+    m = (uint32_t)((((uint64_t)1 << shift) + by - 1) / by);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * m) >> shift);
+  }
+};
 
 struct Geometry {
   int pages_slots;  // pages * page_tokens
-  int page_tokens, heads;
+  Divider page_tokens, heads;
 };
 
-// Row r of 2 T heads rows: head fastest, then key (0) or value (1), then token.
+// Row r of T heads rows: head fastest, then token.
 struct RowId {
   int64_t t;
-  int h, kv;
+  int h;
 };
-__device__ __forceinline__ RowId row_id(int64_t r, int heads) {
-  const int64_t q = r / heads;
-  return {q >> 1, (int)(r - q * heads), (int)(q & 1)};
+__device__ __forceinline__ RowId row_id(int64_t r, const Geometry& g) {
+  if (r <= 0x7fffffff) {
+    const int t = g.heads((int)r);
+    return {t, (int)r - t * g.heads.d};
+  }
+  const int64_t t = r / g.heads.d;
+  return {t, (int)(r - t * g.heads.d)};
 }
 
 // The row of the cache that (slot, h) names, in units of rows.
 __device__ __forceinline__ int64_t cache_row(int slot, int h, const Geometry& g) {
-  const int page = slot / g.page_tokens, p = slot - page * g.page_tokens;
-  return ((int64_t)page * g.heads + h) * g.page_tokens + p;
+  const int page = g.page_tokens(slot), p = slot - page * g.page_tokens.d;
+  return ((int64_t)page * g.heads.d + h) * g.page_tokens.d + p;
 }
 
 template <Act T>
@@ -75,6 +97,16 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float (&x)[kVec
   }
 }
 
+// round_half_even(x / s) for |x| <= 127 s, given r near 1 / s: x r is within
+// 1e-4 of the quotient, and where that leaves the rounding open (or r is not
+// finite) the division decides.
+__device__ __forceinline__ int code_of(float x, float s, float r) {
+  const float t = x * r;
+  float n = rintf(t);
+  if (!(fabsf(t - n) < 0.4999f)) n = rintf(x / s);
+  return (int)n;
+}
+
 template <Act T, int D, bool kI8>
 __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(const void* __restrict__ k, const void* __restrict__ v, int64_t k_stride,
@@ -82,40 +114,50 @@ __global__ void __launch_bounds__(kThreads)
                     void* __restrict__ ck, void* __restrict__ cv, float* __restrict__ ks,
                     float* __restrict__ vs) {
   constexpr int kLanes = D / kVec;
+  pdl_release();
+  pdl_wait();
   const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   const int e = (int)(threadIdx.x % kLanes) * kVec;
   const bool in = r < rows;
-  const RowId id = row_id(in ? r : 0, g.heads);
+  const RowId id = row_id(in ? r : 0, g);
   const int slot = in ? __ldg(slots + id.t) : -1;
   const bool ok = (unsigned)slot < (unsigned)g.pages_slots;
-  float x[kVec] = {};
-  if (ok) load8<T>(id.kv ? v : k, id.t * (id.kv ? v_stride : k_stride) + (int64_t)id.h * D + e, x);
-  if constexpr (!kI8) {
-    if (ok) store8<Act::BF16>(id.kv ? cv : ck, cache_row(slot, id.h, g) * D + e, x);
-  } else {
-    float m = 0.0f;
-    bool bad = false;
+  float x[2][kVec] = {};
+  if (ok) {
+    load8<T>(k, id.t * k_stride + (int64_t)id.h * D + e, x[0]);
+    load8<T>(v, id.t * v_stride + (int64_t)id.h * D + e, x[1]);
+  }
+  const int64_t row = ok ? cache_row(slot, id.h, g) : 0;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      m = fmaxf(m, fabsf(x[i]));
-      bad |= !(fabsf(x[i]) < __int_as_float(0x7f800000));
+  for (int n = 0; n < 2; ++n) {
+    void* to = n ? cv : ck;
+    if constexpr (!kI8) {
+      if (ok) store8<Act::BF16>(to, row * D + e, x[n]);
+    } else {
+      float m = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        m = fmaxf(m, fabsf(x[n][i]));
+        bad |= !(fabsf(x[n][i]) < __int_as_float(0x7f800000));
+      }
+      if (bad) m = __int_as_float(0x7f800000);  // fmaxf drops NaN: a non-finite row is infinite
+#pragma unroll
+      for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
+      const bool finite = m < __int_as_float(0x7f800000);
+      const float s = finite ? m / 127.0f : __int_as_float(0x7fc00000);
+      uint32_t w[2] = {0, 0};
+      if (s > 0.0f) {  // a row of zeros (or of values whose scale underflows) keeps zero codes
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          w[i >> 2] |= ((uint32_t)code_of(x[n][i], s, inv) & 0xffu) << (8 * (i & 3));
+      }
+      if (ok) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to) + row * D + e) = make_uint2(w[0], w[1]);
+        if (e == 0) (n ? vs : ks)[row] = s;
+      }
     }
-    if (bad) m = __int_as_float(0x7f800000);  // fmaxf drops NaN: a non-finite row is infinite
-#pragma unroll
-    for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
-    if (!ok) return;
-    const bool finite = m < __int_as_float(0x7f800000);
-    const float s = finite ? m / 127.0f : __int_as_float(0x7fc00000);
-    uint32_t w[2] = {0, 0};
-    if (s > 0.0f) {  // a row of zeros (or of values whose scale underflows) keeps zero codes
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        w[i >> 2] |= ((uint32_t)__float2int_rn(x[i] / s) & 0xffu) << (8 * (i & 3));
-    }
-    const int64_t row = cache_row(slot, id.h, g);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(id.kv ? cv : ck) + row * D + e) =
-        make_uint2(w[0], w[1]);
-    if (e == 0) (id.kv ? vs : ks)[row] = s;
   }
 }
 
@@ -126,43 +168,49 @@ __global__ void __launch_bounds__(kThreads)
                    const int32_t* __restrict__ slots, int64_t rows, Geometry g,
                    void* __restrict__ k, void* __restrict__ v, int64_t k_stride, int64_t v_stride) {
   constexpr int kLanes = D / kVec;
+  pdl_release();
+  pdl_wait();
   const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   const int e = (int)(threadIdx.x % kLanes) * kVec;
   if (r >= rows) return;
-  const RowId id = row_id(r, g.heads);
+  const RowId id = row_id(r, g);
   const int slot = __ldg(slots + id.t);
-  float x[kVec];
+  float x[2][kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) x[i] = __int_as_float(0x7fc00000);
+  for (int i = 0; i < kVec; ++i) x[0][i] = x[1][i] = __int_as_float(0x7fc00000);
   if ((unsigned)slot < (unsigned)g.pages_slots) {
     const int64_t row = cache_row(slot, id.h, g);
     if constexpr (!kI8) {
-      load8<Act::BF16>(id.kv ? cv : ck, row * D + e, x);
+      load8<Act::BF16>(ck, row * D + e, x[0]);
+      load8<Act::BF16>(cv, row * D + e, x[1]);
     } else {
-      const uint2 w =
-          *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(id.kv ? cv : ck) + row * D + e);
-      const float s = (id.kv ? vs : ks)[row];
+      const uint2 wk = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(ck) + row * D + e);
+      const uint2 wv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cv) + row * D + e);
+      const float sk = ks[row], sv = vs[row];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        x[i] = (float)(int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * s;
+      for (int i = 0; i < kVec; ++i) {
+        x[0][i] = (float)(int8_t)((i < 4 ? wk.x : wk.y) >> (8 * (i & 3))) * sk;
+        x[1][i] = (float)(int8_t)((i < 4 ? wv.x : wv.y) >> (8 * (i & 3))) * sv;
+      }
     }
   }
-  store8<T>(id.kv ? v : k, id.t * (id.kv ? v_stride : k_stride) + (int64_t)id.h * D + e, x);
+  store8<T>(k, id.t * k_stride + (int64_t)id.h * D + e, x[0]);
+  store8<T>(v, id.t * v_stride + (int64_t)id.h * D + e, x[1]);
 }
 
 template <Act T, int D, bool kI8>
 cudaError_t launch(const ptq_kv_cache& c, const KvRows& r, bool write, cudaStream_t st) {
-  const Geometry g{(int)(c.pages * c.page_tokens), (int)c.page_tokens, (int)c.kv_heads};
-  const int64_t rows = 2 * r.T * c.kv_heads;
+  const Geometry g{(int)(c.pages * c.page_tokens), Divider(c.page_tokens), Divider(c.kv_heads)};
+  const int64_t rows = r.T * c.kv_heads;
   const int64_t per = kThreads / (D / kVec), ctas = (rows + per - 1) / per;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas), block(kThreads);
   if (write)
-    kv_write_kernel<T, D, kI8><<<(unsigned)ctas, kThreads, 0, st>>>(
-        r.k, r.v, r.k_stride, r.v_stride, r.slots, rows, g, c.k, c.v, c.k_scale, c.v_scale);
-  else
-    kv_read_kernel<T, D, kI8><<<(unsigned)ctas, kThreads, 0, st>>>(
-        c.k, c.v, c.k_scale, c.v_scale, r.slots, rows, g, r.k, r.v, r.k_stride, r.v_stride);
-  return cudaGetLastError();
+    return launch_pdl(kv_write_kernel<T, D, kI8>, grid, block, 0, st, (const void*)r.k, (const void*)r.v,
+                      r.k_stride, r.v_stride, r.slots, rows, g, c.k, c.v, c.k_scale, c.v_scale);
+  return launch_pdl(kv_read_kernel<T, D, kI8>, grid, block, 0, st, (const void*)c.k, (const void*)c.v,
+                    (const float*)c.k_scale, (const float*)c.v_scale, r.slots, rows, g, r.k, r.v,
+                    r.k_stride, r.v_stride);
 }
 
 template <Act T, bool kI8>
