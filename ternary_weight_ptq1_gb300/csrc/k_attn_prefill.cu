@@ -93,6 +93,7 @@ struct Args {
   PrefillArgs a;
   int G, hg, tpt;  // query heads of a kv head; heads and tokens of a Q tile
   int heads;       // head blocks in all
+  Divider by_per, by_heads, by_G, by_hg;  // by_per: head blocks times parts
   int splits;      // parts the keys of each item are cut into
   float* part;     // splits > 1: [splits][Tq Hq][D] output sums, and the (maximum,
   float2* ml;      // sum) they refer to, [splits][Tq Hq]
@@ -111,16 +112,34 @@ struct Item {
 };
 static_assert(sizeof(Item) <= 64, "its place in shared memory");
 
-__device__ __forceinline__ int clamped(int v, int64_t hi) {
-  return v < 0 ? 0 : v > hi ? (int)hi : v;
+__device__ __forceinline__ int clamped(int v, int hi) { return min(max(v, 0), hi); }
+
+// A bounded wait, in few instructions: the warps' roles together are larger than
+// the instruction cache.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t at = smem_addr(bar);
+#pragma unroll 1
+  for (uint32_t i = kWaitLimit; i > 0; --i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*abort) return false;
+  }
+  return false;
 }
 
 struct Span {
   int q0, nq, k0, nk;
 };
 __device__ __forceinline__ Span span_of(const PrefillArgs& a, int b) {
-  const int q0 = clamped(__ldg(a.cu_q + b), a.Tq), q1 = clamped(__ldg(a.cu_q + b + 1), a.Tq);
-  const int k0 = clamped(__ldg(a.cu_k + b), a.Tk), k1 = clamped(__ldg(a.cu_k + b + 1), a.Tk);
+  const int Tq = (int)a.Tq, Tk = (int)a.Tk;
+  const int q0 = clamped(__ldg(a.cu_q + b), Tq), q1 = clamped(__ldg(a.cu_q + b + 1), Tq);
+  const int k0 = clamped(__ldg(a.cu_k + b), Tk), k1 = clamped(__ldg(a.cu_k + b + 1), Tk);
   return {q0, max(0, q1 - q0), k0, max(0, k1 - k0)};
 }
 
@@ -294,33 +313,36 @@ struct Walk {
   int level, before;  // runs of higher levels
 };
 
-__device__ __forceinline__ int runs_of(const PrefillArgs& a, int64_t b, int run) {
-  return b < a.B ? (span_of(a, (int)b).nq + run - 1) / run : 0;
+__device__ __forceinline__ int queries_of(const PrefillArgs& a, int b) {
+  if (b >= (int)a.B) return 0;
+  const int Tq = (int)a.Tq;
+  return max(0, clamped(__ldg(a.cu_q + b + 1), Tq) - clamped(__ldg(a.cu_q + b), Tq));
 }
 
 __device__ __forceinline__ Walk walk_from_top(const PrefillArgs& a, int run) {
   int most = 0;
 #pragma unroll 1
-  for (int64_t b = threadIdx.x & 31; b < a.B; b += 32) most = max(most, runs_of(a, b, run));
-  return {(int)__reduce_max_sync(~0u, most) - 1, 0};
+  for (int b = threadIdx.x & 31; b < (int)a.B; b += 32) most = max(most, queries_of(a, b));
+  return {((int)__reduce_max_sync(~0u, most) + run - 1) / run - 1, 0};
 }
 
 // The sequence and level of run i in that order; false: there are not so many.
 __device__ __forceinline__ bool walk_to(const PrefillArgs& a, int run, int i, Walk& w, int* seq) {
-  const int lane = threadIdx.x & 31;
-  const int first = runs_of(a, lane, run);
+  const int lane = threadIdx.x & 31, first = queries_of(a, lane);
 #pragma unroll 1
   for (; w.level >= 0; --w.level) {
     int n = w.before;
 #pragma unroll 1
-    for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
-      const unsigned has = __ballot_sync(~0u, (b0 ? runs_of(a, b0 + lane, run) : first) > w.level);
-      const int here = __popc(has);
-      if (i < n + here) {
-        *seq = (int)b0 + (int)__fns(has, 0, i - n + 1);
+    for (int b0 = 0; b0 < (int)a.B; b0 += 32) {
+      const bool mine = (b0 ? queries_of(a, b0 + lane) : first) > w.level * run;
+      const unsigned has = __ballot_sync(~0u, mine);
+      const int rank = n + __popc(has & ((1u << lane) - 1));
+      const unsigned at = __ballot_sync(~0u, mine && rank == i);
+      if (at) {
+        *seq = b0 + __ffs(at) - 1;
         return true;
       }
-      n += here;
+      n += __popc(has);
     }
     w.before = n;
   }
@@ -328,12 +350,12 @@ __device__ __forceinline__ bool walk_to(const PrefillArgs& a, int run, int i, Wa
 }
 
 // 32 bytes of a row, whose alignment is 16 or 32.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool aligned32) {
+__device__ __forceinline__ void store32(char* p, const uint32_t* w, bool aligned32) {
   if (aligned32) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), PTQ_W8(w, 0)
                  : "memory");
   } else {
-    uint4* q = static_cast<uint4*>(p);
+    uint4* q = reinterpret_cast<uint4*>(p);
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
@@ -409,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
   int seen = 0;  // items read
   auto read_item = [&](Item& it, bool one_lane) {
-    const bool there = mbar_wait(item_full + (seen & 1), (seen >> 1) & 1, abort_flag);
+    const bool there = bar_wait(item_full + (seen & 1), (seen >> 1) & 1, abort_flag);
     ok = one_lane ? there : __all_sync(~0u, there);
     if (!ok) return false;
     const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -426,31 +448,31 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // ---- the items of this CTA, one ahead of their use, and their Q tiles, into L2 at
     // once and into shared memory when the tile before has been read ------------------
     int qn[kTiles] = {};  // Q tiles loaded
-    const int per = p.heads * p.splits, run = kTiles * p.tpt;
+    const int run = kTiles * p.tpt;
     Walk walk = walk_from_top(a, run);
     for (int round = 0; ok; ++round) {
       // long items first, dealt out there and back, so that the CTAs' sums are alike
       const int i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       Item it;
       // heads fastest: the long items of all of them come first
-      const int n = i / per, sub = i - n * per, t_last = walk.level;
+      const int n = p.by_per(i), sub = i - n * p.by_per.d;
       it.b = -1;
-      if (t_last >= 0 && walk_to(a, run, n, walk, &it.b)) {
+      if (walk_to(a, run, n, walk, &it.b)) {
         const int t = walk.level;
         const Span sp = span_of(a, it.b);
-        const int blocks = p.G / p.hg, head = sub % p.heads;
+        it.split = p.by_heads(sub);
         it.q0 = sp.q0, it.nq = sp.nq, it.k0 = sp.k0, it.nk = sp.nk;
         it.first = t * kTiles * p.tpt;
-        it.h = head / blocks;
-        it.hq0 = it.h * p.G + (head % blocks) * p.hg;
-        it.split = sub / p.heads;
+        it.hq0 = (sub - it.split * p.heads) * p.hg;
+        it.h = p.by_G(it.hq0);
         // the parts are equal numbers of tiles of the last Q tile's keys
         auto keys = [&](int queries) {
           const int last = min(queries, it.nq) - 1;
           return a.causal ? min(it.nk, it.nk - it.nq + last + 1) : it.nk;
         };
         const int most = keys(it.first + kTiles * p.tpt);
-        const int part = most > 0 ? ((most + kKeys - 1) / kKeys + p.splits - 1) / p.splits : 0;
+        int part = most > 0 ? (most + kKeys - 1) / kKeys : 0;
+        if (p.splits > 1) part = (part + p.splits - 1) / p.splits;
         it.lo = it.split * part;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -460,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
       }
       if (seen >= 2)
-        ok = __all_sync(~0u, mbar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, abort_flag));
       if (!ok) break;
       if (lane == 0) {
         volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -477,11 +499,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (it.n[s] == 0) continue;
         const int y = it.q0 + it.first + s * p.tpt;
         if (lane < D / 64) tma_3d_prefetch(&map_q, 64 * lane, it.hq0, y);
-        if (qn[s] > 0) ok = ok && __all_sync(~0u, mbar_wait(q_free + s, (qn[s] - 1) & 1, abort_flag));
+        if (qn[s] > 0) ok = ok && __all_sync(~0u, bar_wait(q_free + s, (qn[s] - 1) & 1, abort_flag));
         if (!ok) break;
         ++qn[s];
         if (lane == 0) {
           mbar_expect_tx(q_full + s, (uint32_t)(p.hg * p.tpt * D * 2));
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c)
             tma_3d(qs + s * C::kQ + c * kRows * 128, &map_q, 64 * c, it.hq0, y, q_full + s);
         }
@@ -493,42 +516,41 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else if (warp == kLoad) {
     // ---- loads: K and V tiles through the ring in the order of their use:
     // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
-    if (lane == 0) {
-      int u = 0;  // units issued
-      Item it;
-      while (read_item(it, true)) {
-        const int most = max(it.n[0], it.n[1]);
-        if (most == 0) continue;
-        const int key0 = it.k0 + it.lo * kKeys;
-        auto load = [&](const CUtensorMap* map, int x, int y, int rows, int blocks) {
-          const int st = u % C::kRing, round = u / C::kRing;
-          if (round > 0) ok = mbar_wait(empty + st, (round - 1) & 1, abort_flag);
-          if (!ok) return;
-          mbar_expect_tx(full + st, C::kUnit);
-          for (int c = 0; c < blocks; ++c)  // boxes of 64 columns
-            tma_3d(ring + st * C::kUnit + c * rows * 128, map, x + 64 * c, it.h, y, full + st);
-          ++u;
-        };
-        auto load_k = [&](int j) {
-          for (int k = 0; k < C::kUnits && ok; ++k)
-            load(&map_k, k * C::kCols, key0 + j * kKeys, kKeys, C::kCols / 64);
-        };
-        auto load_v = [&](int j) {
-          for (int k = 0; k < C::kUnits && ok; ++k)
-            load(&map_v, 0, key0 + j * kKeys + k * C::kVKeys, C::kVKeys, D / 64);
-        };
-        load_k(0);
-        for (int j = 0; j < most && ok; ++j) {
-          if (kTiles == 1 && j + 1 < most) load_k(j + 1);
-          load_v(j);
-          if (kTiles == 2 && j + 1 < most) load_k(j + 1);
+    int u = 0;  // units issued
+    Item it;
+    while (read_item(it, false)) {
+      const int most = max(it.n[0], it.n[1]), key0 = it.k0 + it.lo * kKeys;
+#pragma unroll 1
+      for (int i = 0; i < 2 * most && ok; ++i) {
+        bool v = i & 1;
+        int j = i / 2;
+        if (kTiles == 1 && i > 0 && i < 2 * most - 1) v = !v, j = v ? j - 1 : j + 1;
+#pragma unroll 1
+        for (int k = 0; k < C::kUnits; ++k, ++u) {
+          const int st = u % C::kRing, round = u / C::kRing, y = key0 + j * kKeys;
+          if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, abort_flag));
+          if (!ok) break;
+          if (elected()) {  // boxes of 64 columns: K by columns, V by keys
+            const uint32_t to = ring + st * C::kUnit;
+            mbar_expect_tx(full + st, C::kUnit);
+            if (v) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_3d(to + c * C::kVKeys * 128, &map_v, 64 * c, it.h, y + k * C::kVKeys, full + st);
+            } else {
+#pragma unroll
+              for (int c = 0; c < C::kCols / 64; ++c)
+                tma_3d(to + c * kKeys * 128, &map_k, k * C::kCols + 64 * c, it.h, y, full + st);
+            }
+          }
+          __syncwarp();
         }
-        if (!ok) break;
       }
-      // whatever becomes of the MMAs, the copies land before the CTA ends
-      for (int v = max(0, u - C::kRing); v < u; ++v)
-        static_cast<void>(mbar_wait(full + v % C::kRing, (v / C::kRing) & 1, nullptr));
+      if (!ok) break;
     }
+    // whatever becomes of the MMAs, the copies land before the CTA ends
+    for (int v = max(0, u - C::kRing); v < u; ++v)
+      static_cast<void>(mbar_wait(full + v % C::kRing, (v / C::kRing) & 1, nullptr));
   } else if (warp >= kMma && warp < kMma + kTiles) {
     // ---- MMAs.  The warp stays converged and an elected lane issues each product
     // in straight-line code (an MMA costs the issue 110 clocks in a lane's own
@@ -538,24 +560,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // and one waits for barriers while the other's MMAs run -------------------------
     const int s = warp - kMma;
     auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(~0u, mbar_wait(bar, phase & 1, abort_flag));
+      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, abort_flag));
     };
-    auto arrived = [&](int u) { wait(full + u % C::kRing, u / C::kRing); };  // ring unit u
-    // of the items before: ring units, tiles of this Q tile, rounds of turns, outputs
-    // of this Q tile
-    int ub = 0, done = 0, rounds = 0, outs = 0;
+    struct Place {  // in the ring
+      int st;
+      uint32_t phase;
+    } next{0, 0};
+    auto step = [&](Place& x) {
+      if (++x.st == C::kRing) x.st = 0, x.phase ^= 1;
+    };
+    auto take = [&] {  // the next K or V tile's
+      const Place x = next;
+      for (int k = 0; k < C::kUnits; ++k) step(next);
+      return x;
+    };
+    // of the items before: tiles of this Q tile, rounds of turns, outputs of this Q tile
+    int done = 0, rounds = 0, outs = 0;
     Item it;
     while (read_item(it, false)) {
       const int tiles = s ? it.n[1] : it.n[0], theirs = s ? it.n[0] : it.n[1], most = max(tiles, theirs);
       if (most == 0) continue;
-      // first unit of K_j and V_j (with one Q tile, past the last K there is no
-      // K_(j + 1) before V_j)
-      auto k_unit = [&](int j) {
-        return ub + (kTiles == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * C::kUnits;
-      };
-      auto v_unit = [&](int j) {
-        return ub + (kTiles == 2 || j == most - 1 ? 2 * j + 1 : 2 * j + 2) * C::kUnits;
-      };
       auto slot_of = [&](int j) { return kTiles == 1 ? (done + j) & 1 : s; };
       auto use_of = [&](int j) { return kTiles == 1 ? (done + j) >> 1 : done + j; };
       // A K or V tile that the other Q tile does not use is released for both.
@@ -563,95 +587,96 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         mma_commit(empty + st);
         if (kTiles == 2 && j >= theirs) mma_commit(empty + st);
       };
-      // S of tile j into its slot: unit k of the columns
-      auto qk = [&](int j, int k) {
-        const int slot = slot_of(j), st = (k_unit(j) + k) % C::kRing;
-        const uint64_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
-        const uint64_t kd = tile_desc(ring + st * C::kUnit, 16);
-#pragma unroll
-        for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = c * (kRows * 128 / 16) + 2 * e;
-            if (k == 0 && c == 0 && e == 0)
-              mma_ss<false>(tmem + slot * kKeys, qd + at, kd + at, idesc<kKeys, false>());
-            else
-              mma_ss<true>(tmem + slot * kKeys, qd + at, kd + at, idesc<kKeys, false>());
-          }
-        release(j, st);
-        if (k == C::kUnits - 1) {
-          mma_commit(s_full + slot);
-          if (j == tiles - 1) mma_commit(q_free + s);
-        }
-      };
-      // O += P V of tile j over its first or second 64 keys
-      auto pv = [&](int j, int half) {
+      // S of tile j into its slot
+      auto scores = [&](int j, Place at) {
         const int slot = slot_of(j);
-        const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
-        const uint32_t d = tmem + 2 * kKeys + s * D;
-        const int st = (v_unit(j) + (C::kUnits == 2 ? half : 0)) % C::kRing;
-        const uint64_t vd = tile_desc(ring + st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
-                                      C::kVKeys * 128);
-        if (j > 0 || half > 0)
-          mma_ts<true>(d, pa, vd, idesc<D, true>());
-        else
-          mma_ts<false>(d, pa, vd, idesc<D, true>());
-#pragma unroll
-        for (int e = 1; e < 4; ++e)  // 16 keys: 8 columns of P, 2048 bytes of V
-          mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
-        if (half == 1 || C::kUnits == 2) release(j, st);
-        if (half == 1) {
-          if (kTiles == 1 || C::kApart) mma_commit(pv_done + s);
-          if (j == tiles - 1) mma_commit(o_full + s);
-        }
-      };
-      auto scores = [&](int j) {
+        if (j == 0) wait(q_full + s, outs);
         if (C::kApart && done + j > 0) wait(s_read + s, done + j - 1);  // S before it has been read
 #pragma unroll
-        for (int k = 0; k < C::kUnits; ++k) {
-          arrived(k_unit(j) + k);
-          fence_after();
-          if (ok && elected()) qk(j, k);
-          __syncwarp();
-        }
-      };
-      if (tiles > 0) {
-        wait(q_full + s, outs);
-        scores(0);
-      }
-      for (int j = 0; j < (kAfter ? most : tiles) && ok; ++j) {
-        const bool mine = j < tiles, more = j + 1 < tiles;
-        const int slot = slot_of(j), use = use_of(j);
-        if (mine) {
-          if (more && !kAfter) scores(j + 1);
-          for (int k = 0; k < C::kUnits; ++k) arrived(v_unit(j) + k);
-          if (more && kAfter) arrived(k_unit(j + 1));
-          if (j == 0 && outs > 0) wait(o_free + s, outs - 1);
-          wait(p_full + 2 * slot, use);
-        }
-        // Two Q tiles take turns: issued side by side their MMAs would alternate,
-        // both S would arrive together and the tensor core would stand still
-        // during both softmaxes (540 for 442 us, 8192 tokens).
-        if (kAfter) {
-          if (s == 1) wait(turn + s, rounds + j);
-          if (s == 0 && rounds + j > 0) wait(turn + s, rounds + j - 1);
-        }
-        fence_after();
-        if (mine) {
-          if (ok && elected()) pv(j, 0);
-          __syncwarp();
-          wait(p_full + 2 * slot + 1, use);
+        for (int k = 0; k < C::kUnits; ++k) {  // by columns
+          if (!kAfter || j == 0) wait(full + at.st, at.phase);
           fence_after();
           if (ok && elected()) {
-            pv(j, 1);
-            if (kAfter && more) qk(j + 1, 0);
+            const uint64_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
+            const uint64_t kd = tile_desc(ring + at.st * C::kUnit, 16);
+#pragma unroll
+            for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int o = c * (kRows * 128 / 16) + 2 * e;
+                if (k == 0 && c == 0 && e == 0)
+                  mma_ss<false>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
+                else
+                  mma_ss<true>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
+              }
+            release(j, at.st);
+            if (k == C::kUnits - 1) {
+              mma_commit(s_full + slot);
+              if (j == tiles - 1) mma_commit(q_free + s);
+            }
           }
           __syncwarp();
+          step(at);
         }
-        if (kAfter && ok && lane == 0) mbar_arrive(turn + 1 - s);
+      };
+      if (!kAfter) {
+        const Place k = take();
+        if (tiles > 0) scores(0, k);
+      }
+#pragma unroll 1
+      for (int j = kAfter ? -1 : 0; j < most && ok; ++j) {
+        const bool mine = j >= 0 && (kTiles == 1 || j < tiles), more = j + 1 < tiles;
+        Place v{0, 0}, k{0, 0};  // V_j, K_(j + 1), in the order of the loads
+        if (kTiles == 1 && j + 1 < most) k = take();
+        if (j >= 0) v = take();
+        if (kTiles == 2 && j + 1 < most) k = take();
+        if (!kAfter && more) scores(j + 1, k);
+        // O += P V, over the first and second 64 keys
+        const int slot = slot_of(j), use = use_of(j);
+        if (mine) {
+          Place x = v;
+#pragma unroll
+          for (int k = 0; k < C::kUnits; ++k, step(x)) wait(full + x.st, x.phase);
+          if (j == 0 && outs > 0) wait(o_free + s, outs - 1);
+        }
+        if (kAfter && j >= 0 && more) wait(full + k.st, k.phase);
+#pragma unroll
+        for (int half = 0; half < 2 && j >= 0; ++half) {
+          if (mine) wait(p_full + 2 * slot + half, use);
+          // Two Q tiles take turns: issued side by side their MMAs would alternate,
+          // both S would arrive together and the tensor core would stand still
+          // during both softmaxes (540 for 442 us, 8192 tokens).
+          if (kAfter && half == 0) {
+            const int t = rounds + j - (s == 0);
+            if (t >= 0) wait(turn + s, t);
+          }
+          if (!mine) break;
+          fence_after();
+          if (ok && elected()) {
+            const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
+            const uint32_t d = tmem + 2 * kKeys + s * D;
+            const uint64_t vd = tile_desc(ring + v.st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
+                                          C::kVKeys * 128);
+            if (half > 0 || j > 0)
+              mma_ts<true>(d, pa, vd, idesc<D, true>());
+            else
+              mma_ts<false>(d, pa, vd, idesc<D, true>());
+#pragma unroll
+            for (int e = 1; e < 4; ++e)  // 16 keys: 8 columns of P, 2048 bytes of V
+              mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
+            if (half == 1 || C::kUnits == 2) release(j, v.st);
+            if (half == 1) {
+              if (kTiles == 1 || C::kApart) mma_commit(pv_done + s);
+              if (j == tiles - 1) mma_commit(o_full + s);
+            }
+          }
+          __syncwarp();
+          if (C::kUnits == 2) step(v);
+        }
+        if (kAfter && more) scores(j + 1, k);
+        if (kAfter && j >= 0 && ok && lane == 0) mbar_arrive(turn + 1 - s);
       }
       if (!ok) break;
-      ub += 2 * most * C::kUnits;
       done += tiles;
       rounds += most;
       outs += tiles > 0;
@@ -667,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const float scale2 = a.scale * kLog2e;
     const uint32_t o_at = tmem + lanes + 2 * kKeys + s * D;
     // this row's token of the tile, and those of the warp's first and last row
-    const int my_tok = row / p.hg, tok_lo = 32 * quarter / p.hg, tok_hi = (32 * quarter + 31) / p.hg;
+    const int my_tok = p.by_hg(row), tok_lo = p.by_hg(32 * quarter), tok_hi = p.by_hg(32 * quarter + 31);
     int done = 0, outs = 0;  // tiles and items before this one
     Item it;
     while (read_item(it, false)) {
@@ -684,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int g = done + j, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
         const uint32_t at = tmem + lanes + slot * kKeys;
         const uint32_t p_at = C::kApart ? tmem + lanes + 384 + slot * 64 : at;
-        ok = __all_sync(~0u, ready || mbar_wait(s_full + slot, use & 1, abort_flag));
+        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
         // The second 64 columns are read twice, for the maximum and again for their
@@ -722,7 +747,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           mask(v, 0);
           take_max(v);
           if (left_hi > 64) {
-            mask(second, 64);
+            if (__builtin_expect(128 > left_lo, 0)) {  // and for the second reading
+              mask(second, 64);
+              tmem_st32(at + 64, second);
+              tmem_st32(at + 96, second + 32);
+              tmem_wait_st();
+            }
             take_max(second);
           }
         }
@@ -733,7 +763,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           // O moves to the new maximum once the product with the tile before is
           // done (where S follows P, S says so)
           if constexpr (!kAfter) {
-            ok = __all_sync(~0u, mbar_wait(pv_done + s, (g - 1) & 1, abort_flag));
+            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, abort_flag));
             if (!ok) break;
           }
           const float mn = t2 > m + kSlack ? t2 : m;
@@ -770,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           }
           if constexpr (C::kApart)  // the product with the tile before has read its P
             if (half == 0 && g > 0)
-              ok = __all_sync(~0u, mbar_wait(pv_done + s, (g - 1) & 1, abort_flag));
+              ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, abort_flag));
           tmem_st32(p_at + 32 * half, x);
         };
         auto publish = [&](int half) {
@@ -797,7 +827,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           read_s(v, 64);
           tmem_wait_ld();
           if constexpr (C::kApart) read_all();
-          mask(v, 64);
           half_p(1);
         } else {
           if constexpr (C::kApart) read_all();
@@ -814,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       float lo, hi;
       unpair(add2(sum2[0], sum2[1]), lo, hi);
       if (outs > 0) {
-        ok = __all_sync(~0u, mbar_wait(ml_free + s, (outs - 1) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait(ml_free + s, (outs - 1) & 1, abort_flag));
         if (!ok) break;
       }
       ++outs;
@@ -827,7 +856,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsStore));
     const int quarter = warp & 3, row = 32 * quarter + lane;
     const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0, parts = p.splits > 1;
-    const int my_tok = row / p.hg, my_head = row % p.hg;
+    const int my_tok = p.by_hg(row), my_head = row - my_tok * p.hg;
     unsigned told = 0, outs = 0;  // bit s: parity of Q tile s's items, of its outputs
     Item it;
     while (read_item(it, false)) {
@@ -838,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int tok = first + my_tok, hq = it.hq0 + my_head;
         const bool mine = row < p.hg * p.tpt && tok < it.nq;
         const int64_t out_row = (int64_t)(it.q0 + tok) * a.Hq + hq;
-        ok = __all_sync(~0u, mbar_wait(ml_full + s, (told >> s) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait(ml_full + s, (told >> s) & 1, abort_flag));
         if (!ok) break;
         told ^= 1u << s;
         const float2 ml = sums[s * kRows + row];
@@ -849,10 +878,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (parts)
             p.ml[(int64_t)it.split * a.Tq * a.Hq + out_row] = ml;
           else if (a.lse)
-            a.lse[out_row] = l == 0.0f ? kNegInf : ml.x * kLn2 + logf(l);
+            a.lse[out_row] = l == 0.0f ? kNegInf : (ml.x + __log2f(l)) * kLn2;
         }
         if (tiles > 0) {
-          ok = __all_sync(~0u, mbar_wait(o_full + s, (outs >> s) & 1, abort_flag));
+          ok = __all_sync(~0u, bar_wait(o_full + s, (outs >> s) & 1, abort_flag));
           if (!ok) break;
           outs ^= 1u << s;
           fence_after();
@@ -860,7 +889,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         uint64_t checked = pair(0.0f, 0.0f);
         if (tiles > 0 || !parts) {
           const uint32_t o_at = tmem + ((uint32_t)(32 * quarter) << 16) + 2 * kKeys + s * D;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
           char* to = parts ? reinterpret_cast<char*>(p.part + ((int64_t)it.split * a.Tq * a.Hq + out_row) * D)
                            : reinterpret_cast<char*>(a.out + out_row * D);
 #pragma unroll 1
@@ -1028,9 +1057,12 @@ template <int D>
 cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
   using C = Cfg<D>;
   const Plan plan = plan_of(a.B, a.Tq, a.Tk, a.Hq, a.Hkv, D);
-  Args p;
-  p.a = a;
-  p.G = (int)(a.Hq / a.Hkv);
+  int64_t work;
+  if (!mul_ok(plan.items, plan.heads * plan.splits, &work) || work > INT32_MAX / 2)
+    return cudaErrorInvalidValue;
+  const int G = (int)(a.Hq / a.Hkv);
+  Args p{a, G, 0, 0, 0, Divider(plan.heads * plan.splits), Divider(plan.heads), Divider(G), Divider(plan.hg),
+         0, nullptr, nullptr};
   p.hg = plan.hg;
   p.tpt = plan.tpt;
   p.splits = plan.splits;
@@ -1050,9 +1082,6 @@ cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
   auto kern = attn_prefill_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  int64_t work;
-  if (!mul_ok(plan.items, plan.heads * plan.splits, &work) || work > INT32_MAX / 2)
-    return cudaErrorInvalidValue;
   p.heads = (int)plan.heads;
   e = launch_pdl(kern, dim3((unsigned)(work < kSms ? work : kSms)), dim3(C::kThreads), C::kSmem, st,
                  mq, mk, mv, p, status);

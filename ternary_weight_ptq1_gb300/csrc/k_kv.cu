@@ -19,24 +19,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kVec = 8;  // values a thread holds of a row
 
-// Division of 0 <= n < 2^31 by a fixed d: with 2^s >= d and m = ceil(2^(31 + s)
-// / d), the excess n (m d - 2^(31 + s)) stays below 2^(31 + s), so n m >> (31 +
-// s) is the quotient.  (The compiler's division by a variable took a third of
-// the kernels' instructions.)
-struct Divider {
-  uint32_t m;
-  int shift, d;
-  explicit Divider(int64_t by) : d((int)by) {
-    int s = 0;
-    while (((int64_t)1 << s) < by) ++s;
-    shift = 31 + s;
-    m = (uint32_t)((((uint64_t)1 << shift) + by - 1) / by);
-  }
-  __device__ __forceinline__ int operator()(int n) const {
-    return (int)(((uint64_t)(uint32_t)n * m) >> shift);
-  }
-};
-
 struct Geometry {
   int pages_slots;  // pages * page_tokens
   Divider page_tokens, heads;
