@@ -182,10 +182,11 @@ __device__ __noinline__ void attend_row(const Args& p, int split, int t, int hq,
 // ---- tensor core -------------------------------------------------------------------
 
 // Shared-memory descriptor of a 128-byte-swizzled tile: 8-row atoms 1024
-// bytes apart; lead: bytes between column blocks of 64 (N-major operands).
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// bytes apart; lead: bytes between column blocks of 64 (N-major operands).  The
+// upper word is the same for all, the lower moves along by 16 bytes a unit.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr, uint32_t lead) {
+  return (addr >> 4) | (lead >> 4) << 16;
 }
 
 // Instruction descriptor: fp32 sums, A and B bf16, M = 128; bit 16: B is
@@ -198,16 +199,20 @@ __device__ __forceinline__ constexpr uint32_t idesc() {
 
 // kAdd: onto what the accumulator holds.
 template <bool kAdd>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
-  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %4;" ::"r"(d), "l"(a), "l"(b),
-               "r"(id), "n"(kAdd ? 1 : 0)
-               : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+  asm volatile(
+      "{\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, %4;\n}" ::"r"(d), "r"(a), "r"(b),
+      "r"(id), "n"(kAdd ? 1 : 0), "n"(kDescHi)
+      : "memory");
 }
 template <bool kAdd>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
-  asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, %4;" ::"r"(d), "r"(a), "l"(b),
-               "r"(id), "n"(kAdd ? 1 : 0)
-               : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+  asm volatile(
+      "{\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, %4;\n}" ::"r"(d), "r"(a), "r"(b),
+      "r"(id), "n"(kAdd ? 1 : 0), "n"(kDescHi)
+      : "memory");
 }
 // One lane of the converged warp, the same each time.
 __device__ __forceinline__ bool elected() {
@@ -597,8 +602,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (!kAfter || j == 0) wait(full + at.st, at.phase);
           fence_after();
           if (ok && elected()) {
-            const uint64_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
-            const uint64_t kd = tile_desc(ring + at.st * C::kUnit, 16);
+            const uint32_t qd = tile_desc(qs + s * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
+            const uint32_t kd = tile_desc(ring + at.st * C::kUnit, 16);
 #pragma unroll
             for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
 #pragma unroll
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (ok && elected()) {
             const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
             const uint32_t d = tmem + 2 * kKeys + s * D;
-            const uint64_t vd = tile_desc(ring + v.st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
+            const uint32_t vd = tile_desc(ring + v.st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
                                           C::kVKeys * 128);
             if (half > 0 || j > 0)
               mma_ts<true>(d, pa, vd, idesc<D, true>());
@@ -712,26 +717,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
+        const int left = sees - j * kKeys, left_lo = least - j * kKeys, left_hi = best - j * kKeys;
+        if (__builtin_expect(left_lo < kKeys, 0)) {
+          // Keys past what a row sees, in TMEM: a loop that fits the instruction cache
+          // (short sequences are masked tiles for the most part).
+#pragma unroll 1
+          for (int c = left_lo < 32 ? 0 : left_lo & ~31; c < (left_hi > 64 ? kKeys : 64); c += 32) {
+            uint32_t x[32];
+            tmem_ld32(at + c, x);
+            tmem_wait_ld();
+            const int in = left - c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e >= in) x[e] = 0xff800000u;
+            tmem_st32(at + c, x);
+          }
+          tmem_wait_st();
+        }
         // The second 64 columns are read twice, for the maximum and again for their
         // exponentials: 128 values held beside P's do not fit the registers.
         uint32_t v[64];
         auto read_s = [&](uint32_t* to, int c0) {
           tmem_ld32(at + c0, to);
           tmem_ld32(at + c0 + 32, to + 32);
-        };
-        const int left = sees - j * kKeys, left_lo = least - j * kKeys, left_hi = best - j * kKeys;
-        // keys past what a row sees: by groups of 32, those that some row does not
-        // see whole
-        auto mask = [&](uint32_t* x, int c0) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            if (__builtin_expect(c0 + c + 32 > left_lo, 0)) {
-              const int in = left - c0 - c;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e >= in) x[c + e] = 0xff800000u;
-            }
-          }
         };
         float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
         auto take_max = [&](const uint32_t* x) {
@@ -744,17 +752,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           read_s(v, 0);
           read_s(second, 64);
           tmem_wait_ld();
-          mask(v, 0);
           take_max(v);
-          if (left_hi > 64) {
-            if (__builtin_expect(128 > left_lo, 0)) {  // and for the second reading
-              mask(second, 64);
-              tmem_st32(at + 64, second);
-              tmem_st32(at + 96, second + 32);
-              tmem_wait_st();
-            }
-            take_max(second);
-          }
+          if (left_hi > 64) take_max(second);
         }
         const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
         if (j == 0) {
