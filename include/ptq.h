@@ -415,8 +415,10 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_embed_ptq1(
  *     s_j = softmax_scale * sum_d q_d k_jd
  *     lse = ln sum_j e^(s_j)
  *     out = sum_j e^(s_j - lse) v_j
- * With J empty out is 0 and lse is -infinity.  Scores, the softmax's maximum
- * and sum, and the output's sums are fp32; a bf16 output is rounded once. */
+ * With J empty out is 0 and lse is -infinity; so they are where every s_j is
+ * -infinity.  A NaN score, or one of +infinity, makes the row NaN.  Scores, the
+ * softmax's maximum and sum, and the output's sums are fp32; a bf16 output is
+ * rounded once. */
 
 /* PTQ_KV_BF16: rows are rounded to nearest-even bf16.
  * PTQ_KV_I8: a row x (one token, one head) is stored as
@@ -493,8 +495,10 @@ PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64
  *   out    B x q_heads x head_dim of dtype, contiguous
  *   lse    B x q_heads fp32, or NULL
  * softmax_scale is finite and positive.  With PTQ_F32 the arithmetic keeps
- * fp32 accuracy over both cache types.  The work is split over the lengths by
- * a rule on the lengths alone, and the parts are joined in a fixed order:
+ * fp32 accuracy over both cache types (over a bf16 cache an infinite key or
+ * value that is seen makes the row NaN: the factors are split).  The work is
+ * split by a rule on the lengths alone, and the parts are joined in a fixed
+ * order:
  * results are bitwise reproducible.  B = 0 is a no-op.
  * workspace: device scratch of ptq_attn_decode_workspace_bytes(...) bytes,
  * 16-byte aligned, caller-owned, any initial contents.  Calls whose kernels

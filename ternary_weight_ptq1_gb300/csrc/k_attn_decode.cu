@@ -63,6 +63,7 @@ struct Cfg {
   static constexpr int kStage = 2 * kTile + (kI8 ? 2 * kT * 4 : 0);
   static constexpr int kStages = 2;
   static constexpr bool kThree = T == Act::F32 && !kI8;
+  static constexpr bool kExactQ = T == Act::BF16 && !kI8;  // q's second terms are 0
   static constexpr bool kFresh = T == Act::F32 || kBlocks > 1;
   static constexpr int kHeads = 8 * kBlocks;            // query heads a warp serves
   static constexpr int kQ = kBlocks * D / 16 * 32 * 16;  // bytes of the query's fragments
@@ -172,10 +173,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// The sums of the first and the second terms; an infinite value's second
+// product may be infinite the other way (kInf: values may be infinite).
+template <bool kInf>
+__device__ __forceinline__ float both(float first, float second) {
+  return kInf && !(fabsf(first) < __int_as_float(0x7f800000)) ? first : first + second;
+}
+
+// 1 / sum; a row whose scores are all -infinity is one that sees no key.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+
 __device__ __forceinline__ int length(const DecodeArgs& a, int b) {
   const int64_t most = a.table_width * a.c.page_tokens;
   const int n = __ldg(a.lens + b);
   return n < 0 ? 0 : n > most ? (int)most : n;
+}
+
+template <int kT>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (int)(((unsigned)len + kT - 1) / kT);
 }
 
 // The units a (sequence, row block) of n tiles is dealt out in: kLead units for
@@ -208,7 +224,7 @@ __device__ __forceinline__ void next_segment(Segment& s, const Args& p, int64_t 
     s.vh = 0;
     do s.len = length(p.a, ++s.b);
     while (s.len == 0);
-    s.n = (s.len + kT - 1) / kT;
+    s.n = tiles_of<kT>(s.len);
   }
   if (!clip(s, s.u, u1)) s.b = -1;  // the run ends before its first tile
 }
@@ -245,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
   // ---- the run of this CTA ---------------------------------------------------------
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kOffScan);  // [2][kWarps]
   int64_t mine = 0;
-  for (int b = tid; b < a.B; b += kWarps * 32) mine += units((length(a, b) + kT - 1) / kT);
+  for (int b = tid; b < a.B; b += kWarps * 32) mine += units(tiles_of<kT>(length(a, b)));
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // no key: 0 and -infinity
     if (length(a, b) == 0) {
       for (int64_t e = 4 * tid; e < a.Hq * D; e += 4 * kWarps * 32)
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
   if (tid == 0) *found = -1;
   for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
     const int64_t b = b0 + tid;
-    const int n = b < a.B ? units((length(a, (int)b) + kT - 1) / kT) : 0;
+    const int n = b < a.B ? units(tiles_of<kT>(length(a, (int)b))) : 0;
     int64_t incl = (int64_t)n * p.VH;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     seg.b = *found;
     const int64_t in = u0 - scan[kWarps];
     seg.len = length(a, seg.b);
-    seg.n = (seg.len + kT - 1) / kT;
+    seg.n = tiles_of<kT>(seg.len);
     seg.vh = (int)(in / units(seg.n));
     seg.u = scan[kWarps] + (int64_t)seg.vh * units(seg.n);
     // (a run that ends within its first kLead units has no tile)
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       const uint32_t dst = ring_at + stage * C::kStage;
       const int32_t* pages = a.table + ahead.b * a.table_width;
       const int j0 = at * kT, head = ahead.vh / p.HC;
-      if (p.whole && j0 + kT <= ahead.len) {  // a tile inside one page: one stretch of rows
+      if (p.whole && ahead.len - j0 >= kT) {  // a tile inside one page: one stretch of rows
         const int page = __ldg(pages + (unsigned)j0 / (unsigned)ps);
         const bool in = (unsigned)page < (unsigned)a.c.pages;
         if (lane == 0) bad[stage] = !in;
@@ -351,13 +367,13 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
           copy4(dst + 2 * C::kTile + 4 * kT + 4 * lane, a.c.v_scale + row + lane, true);
         }
       } else {
-        const int j = j0 + (lane % kT);
+        const unsigned j = (unsigned)j0 + lane % kT;
         int64_t row = -1;
         bool wrong = false;
-        if (j < ahead.len) {
-          const int page = __ldg(pages + (unsigned)j / (unsigned)ps);
+        if (lane % kT < ahead.len - j0) {
+          const int page = __ldg(pages + j / (unsigned)ps);
           wrong = (unsigned)page >= (unsigned)a.c.pages;
-          if (!wrong) row = ((int64_t)page * heads + head) * ps + (unsigned)j % (unsigned)ps;
+          if (!wrong) row = ((int64_t)page * heads + head) * ps + j % (unsigned)ps;
         }
         const uint32_t any = __ballot_sync(~0u, wrong);
         if (lane == 0) bad[stage] = any;
@@ -532,8 +548,13 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
             const float2 c = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * t4);
             c0 *= c.x, c1 *= c.y;
           }
-          s[h][n][0] = (s[h][n][0] + s[h][n][2]) * c0;
-          s[h][n][1] = (s[h][n][1] + s[h][n][3]) * c1;
+          if constexpr (C::kExactQ) {
+            s[h][n][0] *= c0;
+            s[h][n][1] *= c1;
+          } else {
+            s[h][n][0] = (s[h][n][0] + s[h][n][2]) * c0;
+            s[h][n][1] = (s[h][n][1] + s[h][n][3]) * c1;
+          }
           if (left < kT) {
             if (8 * n + 2 * t4 >= left) s[h][n][0] = kNegInf;
             if (8 * n + 2 * t4 + 1 >= left) s[h][n][1] = kNegInf;
@@ -623,8 +644,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             if constexpr (C::kFresh) {
-              o[h][n + i][0] = fmaf(o[h][n + i][0], fade[h], acc[h][i][0] + acc[h][i][2]);
-              o[h][n + i][1] = fmaf(o[h][n + i][1], fade[h], acc[h][i][1] + acc[h][i][3]);
+              o[h][n + i][0] = fmaf(o[h][n + i][0], fade[h], both<C::kExactQ>(acc[h][i][0], acc[h][i][2]));
+              o[h][n + i][1] = fmaf(o[h][n + i][1], fade[h], both<C::kExactQ>(acc[h][i][1], acc[h][i][3]));
             } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[h][n + i][e] = acc[h][i][e];
@@ -650,7 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
         if constexpr (C::kFresh)
           return o[h][n][e] * back;
         else
-          return (o[h][n][e] + o[h][n][e + 2]) * back;
+          return both<C::kExactQ>(o[h][n][e], o[h][n][e + 2]) * back;
       };
       if constexpr (kI8) {  // columns 16 c + 4 t4 .. + 3
 #pragma unroll
@@ -693,7 +714,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
         acc.w = fmaf(v.w, f, acc.w);
       }
       if (whole) {
-        const float inv = 1.0f / sum;
+        const float inv = inverse(sum);
         const int64_t row = (int64_t)seg.b * a.Hq + h0 + r0 + r;
         store_out4<T>(a.out, row * D + 4 * d4,
                       sum == sum ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)
@@ -767,7 +788,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(Args p) {
     acc.z += v.z;
     acc.w += v.w;
   }
-  const float inv = 1.0f / sum;
+  const float inv = inverse(sum);
   const int64_t row = (int64_t)note.b * p.a.Hq + (note.vh / p.HC) * p.G + r0 + r;
   store_out4<T>(p.a.out, row * D + 4 * d4,
                 sum == sum ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)

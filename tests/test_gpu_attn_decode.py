@@ -387,3 +387,30 @@ def test_offsets_past_32_bits(P, kv):
     for h in range(Hkv):
         ref = R.attend(q[0, h:h + 1], _stored(k, kv)[:, h], _stored(v, kv)[:, h], 1 / 16)
         R.check(_host(out)[0, h:h + 1], _host(lse)[0, h:h + 1], ref, True, False)
+
+
+def test_infinite_keys(P):
+    """A key whose score is -infinity counts for nothing, and a row of such keys
+    alone is empty; +infinity and infinite values leave no finite row."""
+    import torch
+
+    rng = np.random.default_rng(31)
+    D, n = 64, 40
+    s = Paged(P, rng, [n, n, n, n], 1, D, 16, "bf16", "bf16")
+    s.k[0][17, 0, 3] = s.k[1][:, 0, 3] = -np.inf
+    s.k[2][17, 0, 3] = np.inf
+    s.v[3][17, 0, 5] = np.inf
+    P.kv_write(s.cache, _dev(np.concatenate(s.k), "bf16"), _dev(np.concatenate(s.v), "bf16"),
+               torch.from_numpy(s.slots).cuda())
+    q = R.bf16(rng.standard_normal((4, 2, D)))
+    q[:, :, 3] = 1.0
+    lse = torch.empty((4, 2), device="cuda")
+    out = _host(P.attn_decode(_dev(q, "bf16"), s.cache, s.table_d, s.lens_d, lse=lse))
+    lse = _host(lse)
+    use = np.arange(n) != 17
+    for h in range(2):
+        ref = R.attend(q[0, h:h + 1], s.k[0][use, 0], s.v[0][use, 0], D ** -0.5)
+        R.check(out[0, h:h + 1], lse[0, h:h + 1], ref, True, False)
+    assert (out[1] == 0).all() and np.isneginf(lse[1]).all()
+    assert np.isnan(out[2]).all() and np.isnan(lse[2]).all()
+    assert (out[3, :, 5] == np.inf).all() and np.isfinite(out[3][:, np.arange(D) != 5]).all()
