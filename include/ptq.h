@@ -497,8 +497,8 @@ PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64
  * softmax_scale is finite and positive.  With PTQ_F32 the arithmetic keeps
  * fp32 accuracy over both cache types (over a bf16 cache an infinite key or
  * value that is seen makes the row NaN: the factors are split).  The work is
- * split by a rule on the lengths alone, and the parts are joined in a fixed
- * order:
+ * split by a rule on the shapes and the lengths alone, and the parts are joined
+ * in a fixed order:
  * results are bitwise reproducible.  B = 0 is a no-op.
  * workspace: device scratch of ptq_attn_decode_workspace_bytes(...) bytes,
  * 16-byte aligned, caller-owned, any initial contents.  Calls whose kernels

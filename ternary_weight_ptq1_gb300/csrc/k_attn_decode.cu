@@ -16,7 +16,9 @@
 // adds them up itself.  The part of a (sequence, kv head) inside one CTA's run
 // is a segment; a segment that is a whole (sequence, kv head) writes its
 // output, the others write their maximum, sum and output sums to the workspace
-// and a second kernel joins them in order.
+// and a second kernel joins them in order.  Where the sequences are few and
+// short, a cluster of CTAs shares each (sequence, kv head) instead and joins
+// its parts through distributed shared memory, in one launch.
 //
 // Inside a CTA each warp owns its tiles alone: it copies them into a ring of
 // its own in shared memory (cp.async, the copies of the next tiles always in
@@ -41,6 +43,8 @@
 // sums are rounded below the bf16 output's own rounding.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "attn_row.cuh"
 #include "ptq_internal.cuh"
@@ -73,14 +77,17 @@ struct Cfg {
   static constexpr int kOffMl = kOffF + 16 * 4;         // (m, l) of each warp and head
   static constexpr int kOffBad = kOffMl + kWarps * 16 * 8;
   static constexpr int kOffScan = kOffBad + kWarps * kStages * 4;
-  static constexpr int kSmem = (kOffScan + 2 * kWarps * 8 + 32 + 15) / 16 * 16;
+  static constexpr int kOffPart = (kOffScan + 2 * kWarps * 8 + 32 + 15) / 16 * 16;  // (m, l) of each head
+  static constexpr int kSmem = kOffPart + 16 * 8;
   static constexpr int kFit = (227 * 1024) / (kSmem + 1024);
   static constexpr int kPerSm = kFit < 1 ? 1 : kFit > 3 ? 3 : kFit;
-  // a warp's output (kHeads rows of fp32) is handed over in a stage
-  static_assert(kStage >= kHeads * D * 4, "stage holds a warp's output");
+  // a warp's output (kHeads rows of fp32) is handed over in a stage, a cluster's
+  // CTA's where the query's fragments were
+  static_assert(kStage >= kHeads * D * 4 && kQ >= kHeads * D * 4, "room for an output");
 };
 
 constexpr int kMaxCtas = 3 * kSms;
+constexpr int kCluster = 8;  // CTAs of a cluster
 
 // Workspace: for each CTA two segments (one that began before its run, one
 // that goes on after it), each kHeads rows of D sums, then their (m, l), then
@@ -97,6 +104,7 @@ struct Args {
   Note* note;     // [ctas]
   int G, VH, HC;  // query heads of a kv head; row blocks in all, of one kv head
   bool whole;     // pages hold whole tiles
+  int cluster;    // CTAs of a (sequence, row block); 0: runs
 };
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -240,6 +248,28 @@ __device__ __forceinline__ void store_out4(void* out, int64_t e, float4 v) {
   }
 }
 
+__device__ __forceinline__ uint32_t peer(uint32_t at, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 peer_ld2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // The weight of a part with maximum m and sum l in a whole with maximum top.
 // l = 0: the part has no key.  m = -inf with l != 0: its scores are NaN.
 __device__ __forceinline__ float part_weight(float2 ml, float top) {
@@ -260,8 +290,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
 
   // ---- the run of this CTA ---------------------------------------------------------
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kOffScan);  // [2][kWarps]
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += kWarps * 32) mine += units(tiles_of<kT>(length(a, b)));
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // no key: 0 and -infinity
     if (length(a, b) == 0) {
       for (int64_t e = 4 * tid; e < a.Hq * D; e += 4 * kWarps * 32)
@@ -269,61 +297,78 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       if (a.lse)
         for (int64_t h = tid; h < a.Hq; h += kWarps * 32) a.lse[b * a.Hq + h] = kNegInf;
     }
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) mine += __shfl_xor_sync(~0u, mine, i);
-  if (lane == 0) scan[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += scan[w];
-  total *= p.VH;
-  // runs of equal cost, of whole rounds of the CTA's warps
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  per = (per + kWarps - 1) / kWarps * kWarps;
-  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, total);
-  if (tid == 0) p.note[blockIdx.x] = Note{-1, 0, 0, 0};
-  if (u0 >= total) return;
-  // the sequence that holds unit u0: sequences are added up kWarps * 32 at a time
   Segment seg{-1, 0, 0, 0, 0, 0, 0};
-  int* found = reinterpret_cast<int*>(scan + 2 * kWarps);
-  if (tid == 0) *found = -1;
-  for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
-    const int64_t b = b0 + tid;
-    const int n = b < a.B ? units(tiles_of<kT>(length(a, (int)b))) : 0;
-    int64_t incl = (int64_t)n * p.VH;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const int64_t o = __shfl_up_sync(~0u, incl, i);
-      if (lane >= i) incl += o;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t before = base, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += scan[w];
-      all += scan[w];
-    }
-    const int64_t end = before + incl, start = end - (int64_t)n * p.VH;
-    if (u0 >= start && u0 < end) {
-      *found = (int)b;
-      scan[kWarps] = start;
-    }
-    base += all;
-    if (u0 < base) break;
-  }
-  __syncthreads();
-  {
-    seg.b = *found;
-    const int64_t in = u0 - scan[kWarps];
-    seg.len = length(a, seg.b);
+  int64_t u1 = 1, per = 1;
+  if (p.cluster) {  // an equal part of this cluster's (sequence, row block)
+    const int id = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    seg.vh = id % p.VH;
+    seg.len = length(a, id / p.VH);
     seg.n = tiles_of<kT>(seg.len);
-    seg.vh = (int)(in / units(seg.n));
-    seg.u = scan[kWarps] + (int64_t)seg.vh * units(seg.n);
-    // (a run that ends within its first kLead units has no tile)
-    if (!clip(seg, u0, u1)) seg.b = -1;
+    seg.t0 = (int)((int64_t)seg.n * rank / p.cluster);
+    seg.t1 = (int)((int64_t)seg.n * (rank + 1) / p.cluster);
+    if (seg.n == 0) return;  // the whole cluster
+    if (seg.t0 < seg.t1) seg.b = id / p.VH;
+  } else {
+    int64_t mine = 0;
+    for (int b = tid; b < a.B; b += kWarps * 32) mine += units(tiles_of<kT>(length(a, b)));
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) mine += __shfl_xor_sync(~0u, mine, i);
+    if (lane == 0) scan[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += scan[w];
+    total *= p.VH;
+    // runs of equal cost, of whole rounds of the CTA's warps
+    per = (total + gridDim.x - 1) / gridDim.x;
+    per = (per + kWarps - 1) / kWarps * kWarps;
+    const int64_t u0 = blockIdx.x * per;
+    u1 = min(u0 + per, total);
+    if (tid == 0) p.note[blockIdx.x] = Note{-1, 0, 0, 0};
+    if (u0 >= total) return;
+    // the sequence that holds unit u0: sequences are added up kWarps * 32 at a time
+    int* found = reinterpret_cast<int*>(scan + 2 * kWarps);
+    if (tid == 0) *found = -1;
+    for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
+      const int64_t b = b0 + tid;
+      const int n = b < a.B ? units(tiles_of<kT>(length(a, (int)b))) : 0;
+      int64_t incl = (int64_t)n * p.VH;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, incl, i);
+        if (lane >= i) incl += o;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      int64_t before = base, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
+      }
+      const int64_t end = before + incl, start = end - (int64_t)n * p.VH;
+      if (u0 >= start && u0 < end) {
+        *found = (int)b;
+        scan[kWarps] = start;
+      }
+      base += all;
+      if (u0 < base) break;
+    }
+    __syncthreads();
+    {
+      seg.b = *found;
+      const int64_t in = u0 - scan[kWarps];
+      seg.len = length(a, seg.b);
+      seg.n = tiles_of<kT>(seg.len);
+      seg.vh = (int)(in / units(seg.n));
+      seg.u = scan[kWarps] + (int64_t)seg.vh * units(seg.n);
+      // (a run that ends within its first kLead units has no tile)
+      if (!clip(seg, u0, u1)) seg.b = -1;
+    }
   }
+
+  const int mine_tiles = seg.b < 0 ? 0 : seg.t1 - seg.t0;
 
   // ---- the ring --------------------------------------------------------------------
   unsigned char* ring = smem + warp * C::kStages * C::kStage;
@@ -691,6 +736,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     __syncthreads();
     const bool whole = seg.t0 == 0 && seg.t1 == seg.n;
     const int slot = 2 * blockIdx.x + (seg.t0 > 0 ? 0 : 1);
+    float* cl_out = reinterpret_cast<float*>(smem + C::kOffQ);
     for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), d4 = i % (D / 4);
       float2 w[kWarps];
@@ -713,7 +759,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
         acc.z = fmaf(v.z, f, acc.z);
         acc.w = fmaf(v.w, f, acc.w);
       }
-      if (whole) {
+      if (p.cluster) {
+        *reinterpret_cast<float4*>(cl_out + r * D + 4 * d4) = acc;
+        if (d4 == 0) reinterpret_cast<float2*>(smem + C::kOffPart)[r] = make_float2(top, sum);
+      } else if (whole) {
         const float inv = inverse(sum);
         const int64_t row = (int64_t)seg.b * a.Hq + h0 + r0 + r;
         store_out4<T>(a.out, row * D + 4 * d4,
@@ -728,11 +777,49 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     }
     __syncthreads();
     // a (sequence, row block) that begins here and goes on in the next CTAs
-    if (tid == 0 && seg.t0 == 0 && seg.t1 < seg.n)
+    if (tid == 0 && seg.t0 == 0 && seg.t1 < seg.n && !p.cluster)
       p.note[blockIdx.x] = Note{seg.b, seg.vh, (int)((seg.u + units(seg.n) - 1) / per), 0};
     next_segment<kT>(seg, p, u1);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.cluster == 0) return;
+
+  // ---- the cluster's parts, joined in order by all its CTAs ------------------------------
+  const int id = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster, vh = id % p.VH;
+  float2* part_ml = reinterpret_cast<float2*>(smem + C::kOffPart);
+  if (mine_tiles == 0 && tid < 16) part_ml[tid] = make_float2(kNegInf, 0.0f);
+  cluster_sync();
+  const int r0 = (vh % p.HC) * C::kHeads, rows = min(p.G - r0, C::kHeads);
+  for (int i = rank * kWarps * 32 + tid; i < rows * (D / 4); i += p.cluster * kWarps * 32) {
+    const int r = i / (D / 4), d4 = i % (D / 4);
+    float2 w[kCluster];
+    float top = kNegInf, sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kCluster; ++j)
+      if (j < p.cluster) {
+        w[j] = peer_ld2(peer(smem_at(part_ml + r), j));
+        top = fmaxf(top, w[j].x);
+      }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kCluster; ++j)
+      if (j < p.cluster && !(w[j].y == 0.0f)) {  // (a CTA without a tile has no sums)
+        const float f = part_weight(w[j], top);
+        const float4 v = peer_ld4(peer(smem_at(smem + C::kOffQ) + 4 * (r * D + 4 * d4), j));
+        sum = fmaf(w[j].y, f, sum);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+    const float inv = inverse(sum);
+    const int64_t row = (int64_t)(id / p.VH) * a.Hq + (vh / p.HC) * p.G + r0 + r;
+    store_out4<T>(a.out, row * D + 4 * d4,
+                  sum == sum ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)
+                             : make_float4(sum, sum, sum, sum));
+    if (a.lse && d4 == 0) a.lse[row] = top * kLn2 + logf(sum);
+  }
+  cluster_sync();  // a CTA's shared memory stays until all have read it
 }
 
 // Joins the parts of a (sequence, row block) that begins in CTA blockIdx.x of
@@ -796,6 +883,35 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(Args p) {
   if (p.a.lse && d4 == 0) p.a.lse[row] = top * kLn2 + logf(sum);
 }
 
+// How many clusters of the kernel the current device runs at once (0: not
+// known; asked once a device).
+template <Act T, int D, bool kI8, int kBlocks>
+int resident_clusters() {
+  using C = Cfg<T, D, kI8, kBlocks>;
+  static std::atomic<int> known[64];  // one more than the answer
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, attn_decode_kernel<T, D, kI8, kBlocks>, &cfg) != cudaSuccess) {
+      static_cast<void>(cudaGetLastError());
+      n = 0;
+    }
+    known[dev].store(++n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
 template <Act T, int D, bool kI8, int kBlocks>
 cudaError_t launch(const DecodeArgs& a, void* ws, cudaStream_t st) {
   using C = Cfg<T, D, kI8, kBlocks>;
@@ -813,6 +929,18 @@ cudaError_t launch(const DecodeArgs& a, void* ws, cudaStream_t st) {
   auto kern = attn_decode_kernel<T, D, kI8, kBlocks>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
+  // Few short sequences: a cluster a (sequence, row block), whose CTAs join their
+  // parts themselves (one launch).  Up to two tiles a warp: one sequence of 8 x 5
+  // heads of 128, fp32 over bf16, takes 6.4 us for 8.1 at 1 token, 8.9 for 9.8 at
+  // 1000, and 11.1 for 10.2 at 2000.  And while all run at once: at 56 clusters,
+  // which do not, 14.1 for 10.0.
+  p.cluster = a.table_width * a.c.page_tokens <= 2 * kCluster * kWarps * C::kT &&
+                      a.B * p.VH <= resident_clusters<T, D, kI8, kBlocks>()
+                  ? kCluster
+                  : 0;
+  if (p.cluster)
+    return launch_pdl_cluster(kern, dim3((unsigned)(a.B * p.VH * p.cluster)), (unsigned)p.cluster,
+                              dim3(kWarps * 32), C::kSmem, st, p);
   e = launch_pdl(kern, dim3(kCtas), dim3(kWarps * 32), C::kSmem, st, p);
   if (e != cudaSuccess) return e;
   const int rows = p.G < C::kHeads ? p.G : C::kHeads;

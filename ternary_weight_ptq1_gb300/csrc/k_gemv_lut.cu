@@ -603,26 +603,6 @@ int64_t gemv_lut_ctas_per_chunk(int64_t sms, int64_t nch, int64_t N) {
   return ctas_per_chunk(sms, nch, N);
 }
 
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned ctas, unsigned cl,
-                                      size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cl;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 // How many clusters of nch one-token CTAs the device runs at once (0: none;
 // asked once per device, format and nch).
 template <bool kPQ2>
@@ -699,8 +679,8 @@ static cudaError_t launch_lut_tma(const void* wq, const uint16_t* scales, const 
   T.cpc = (int)cpc;
   T.M = (int)M;
   if (clustered)
-    return launch_pdl_cluster(gemv_lut_tma_kernel<kPQ2, true, true>, (unsigned)(nch * cpc),
-                              (unsigned)nch, kSmemTma, st, T);
+    return launch_pdl_cluster(gemv_lut_tma_kernel<kPQ2, true, true>, dim3((unsigned)(nch * cpc)),
+                              (unsigned)nch, dim3(kThreads), kSmemTma, st, T);
   if (M == 1)
     return launch_pdl(gemv_lut_tma_kernel<kPQ2, true>, dim3((unsigned)(nch * cpc)),
                       dim3(kThreads), kSmemTma, st, T);

@@ -414,3 +414,18 @@ def test_infinite_keys(P):
     assert (out[1] == 0).all() and np.isneginf(lse[1]).all()
     assert np.isnan(out[2]).all() and np.isnan(lse[2]).all()
     assert (out[3, :, 5] == np.inf).all() and np.isfinite(out[3][:, np.arange(D) != 5]).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("B,Hkv,G,D,width", [(1, 8, 5, 128, 64), (1, 8, 5, 128, 65), (1, 8, 5, 128, 128),
+                                             (1, 8, 5, 128, 129), (3, 4, 6, 256, 40), (1, 4, 6, 256, 40),
+                                             (40, 1, 3, 64, 40), (86, 1, 3, 64, 40), (2, 2, 20, 64, 40)])
+def test_few_sequences_in_clusters_and_in_runs(P, B, Hkv, G, D, width, kv):
+    """Both sides of where a cluster of CTAs takes each (sequence, kv head)."""
+    rng = np.random.default_rng(41)
+    lens = [int(x) for x in rng.integers(0, 600, B)]
+    lens[0] = 601
+    act = "f32" if G == 5 else "bf16"
+    s = Paged(P, rng, lens, Hkv, D, 16, kv, act, width=width)
+    q, out, lse = _run(P, rng, s, Hkv * G, act)
+    s.check(q, out, lse, D ** -0.5, act == "bf16", only=sorted(set([0, B - 1, B // 2])))
