@@ -144,36 +144,44 @@ def _check(status: int, call: str) -> None:
 def _stream(stream=None, device=None) -> int:
     """The raw handle of `stream`, else of PyTorch's current stream on
     `device` (an index; the current device when None)."""
-    import torch
-
+    global _raw_stream
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:  # no Stream object per call
-        return raw(torch.cuda.current_device() if device is None else device)
-    return torch.cuda.current_stream(device).cuda_stream
+    if device is None or _raw_stream is None:
+        import torch
+
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or  # no Stream object per call
+                       (lambda d: torch.cuda.current_stream(d).cuda_stream))
+        if device is None:
+            device = torch.cuda.current_device()
+    return _raw_stream(device)
+
+
+_raw_stream = None
 
 
 def _dev(t, dtype=None, name="tensor"):
-    import torch
-
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
 
 
 def _act_dtype(t):
-    import torch
+    if not _act_dtypes:
+        import torch
 
-    if t.dtype == torch.float32:
-        return PTQ_F32
-    if t.dtype == torch.bfloat16:
-        return PTQ_BF16
-    raise TypeError(f"activations must be float32 or bfloat16, got {t.dtype}")
+        _act_dtypes.update({torch.float32: PTQ_F32, torch.bfloat16: PTQ_BF16})
+    dt = _act_dtypes.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"activations must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+_act_dtypes = {}
 
 
 # ---- host encoder ------------------------------------------------------------
@@ -531,6 +539,7 @@ class KVCache:
         else:
             raise TypeError(f"a cache is bfloat16 or int8, got {k.dtype}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._int32, self._bfloat16 = torch.int32, torch.bfloat16
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
         self._struct = _KvCacheStruct(_dev(k, None, "k"), _dev(v, None, "v"), *scales, self.pages,
                                       self.page_tokens, self.kv_heads, self.head_dim, self.type)
@@ -552,14 +561,17 @@ class KVCache:
 def _heads(t, name, dtype, shape=None):
     """The address and token stride of a tokens x heads x head_dim tensor whose
     heads are contiguous within a token (tokens may be any stride apart)."""
-    if not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+    s = t.shape
+    if len(s) != 3 or (shape is not None and s != shape):
         raise ValueError(f"{name} must be {'tokens x heads x head_dim' if shape is None else tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
-    n, h, d = t.shape
+                         f"got {tuple(s)}")
+    n, h, d = s
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     s = t.stride()
     if (s[2] != 1 and d != 1) or (s[1] != d and h != 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -571,31 +583,30 @@ def kv_write(cache, k, v, slots, stream=None):
     bfloat16; heads contiguous, tokens any stride apart) at the int32 `slots`
     of the cache, rounded or quantised as the cache is; a slot outside the
     cache skips its token."""
-    import torch
-
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
-    kp, ks = _heads(k, "k", k.dtype, shape)
-    vp, vs = _heads(v, "v", k.dtype, shape)
-    _check(load().ptq_kv_write(cache._ref, kp, vp, ks, vs, _dev(slots, torch.int32, "slots"), shape[0],
-                               _act_dtype(k), _stream(stream, k.device.index)), "ptq_kv_write")
+    dtype = k.dtype
+    kp, ks = _heads(k, "k", dtype, shape)
+    vp, vs = _heads(v, "v", dtype, shape)
+    _check(load().ptq_kv_write(cache._ref, kp, vp, ks, vs, _dev(slots, cache._int32, "slots"), shape[0],
+                               _act_dtype(k), _stream(stream, k.get_device())), "ptq_kv_write")
 
 
 def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     """The values that the int32 `slots` of the cache stand for, as (k, v) of
     float32 or bfloat16 (default); into the given k and v (as for kv_write)
     or new tensors.  A slot outside the cache gives NaN."""
-    import torch
-
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
-    dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
+    if dtype is None:
+        dtype = k.dtype if k is not None else cache._bfloat16
+    sp = _dev(slots, cache._int32, "slots")
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        k = slots.new_empty(shape, dtype=dtype)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        v = slots.new_empty(shape, dtype=dtype)
     kp, ks = _heads(k, "k", dtype, shape)
     vp, vs = _heads(v, "v", dtype, shape)
-    _check(load().ptq_kv_read(cache._ref, _dev(slots, torch.int32, "slots"), shape[0], kp, vp, ks, vs,
-                              _act_dtype(k), _stream(stream, k.device.index)), "ptq_kv_read")
+    _check(load().ptq_kv_read(cache._ref, sp, shape[0], kp, vp, ks, vs, _act_dtype(k),
+                              _stream(stream, k.get_device())), "ptq_kv_read")
     return k, v
 
 
@@ -604,21 +615,27 @@ def attn_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: i
 
 
 def _attn_buffers(q, out, lse, workspace, need):
-    """The output, and the addresses of out, lse and the workspace."""
-    import torch
-
-    B, Hq, D = q.shape
+    """The output, the addresses of out and lse, the workspace, its address and size."""
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     elif out.shape != q.shape:
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-    if lse is not None and lse.shape != (B, Hq):
-        raise ValueError(f"lse must be {(B, Hq)}, got {tuple(lse.shape)}")
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    return (out, _dev(out, q.dtype, "out"), None if lse is None else _dev(lse, torch.float32, "lse"),
-            None if workspace is None else _dev(workspace, None, "workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), workspace)
+    op = _dev(out, q.dtype, "out")
+    lp = wp = None
+    wb = 0
+    if lse is not None:
+        import torch
+
+        if lse.shape != q.shape[:2]:
+            raise ValueError(f"lse must be {tuple(q.shape[:2])}, got {tuple(lse.shape)}")
+        lp = _dev(lse, torch.float32, "lse")
+    if workspace is None and need() > 0:
+        import torch
+
+        workspace = q.new_empty(need(), dtype=torch.uint8)
+    if workspace is not None:
+        wp, wb = _dev(workspace, None, "workspace"), workspace.nbytes
+    return out, op, lp, wp, wb, workspace
 
 
 def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace=None, stream=None):
@@ -628,21 +645,20 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
     head_dim ** -0.5; `lse` (sequences x q_heads float32), when given, receives
     the log-sum-exp of the scaled scores.  out and the workspace are allocated
     by PyTorch when not given."""
-    import torch
-
     dt = _act_dtype(q)
     qp, qs = _heads(q, "q", q.dtype)
     B, Hq, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q has head_dim {D}, the cache {cache.head_dim}")
-    if table.dim() != 2 or table.shape[0] != B or lens.shape != (B,):
+    ts, int32 = table.shape, cache._int32
+    if len(ts) != 2 or ts[0] != B or lens.shape != (B,):
         raise ValueError("table must be sequences x pages, lens one count for each sequence")
-    need = 0 if workspace is not None else attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt)
-    out, op, lp, wp, wb, keep = _attn_buffers(q, out, lse, workspace, need)
-    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, torch.int32, "table"), table.shape[1],
-                                  _dev(lens, torch.int32, "lens"), op, lp, B, Hq,
+    out, op, lp, wp, wb, keep = _attn_buffers(
+        q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt))
+    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, int32, "table"), ts[1],
+                                  _dev(lens, int32, "lens"), op, lp, B, Hq,
                                   D ** -0.5 if scale is None else scale, dt, wp, wb,
-                                  _stream(stream, q.device.index)), "ptq_attn_decode")
+                                  _stream(stream, q.get_device())), "ptq_attn_decode")
     return out
 
 
@@ -660,24 +676,24 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     lse and workspace as for attn_decode."""
     import torch
 
-    dt = _act_dtype(q)
-    qp, qs = _heads(q, "q", q.dtype)
-    kp, ks = _heads(k, "k", q.dtype)
-    vp, vs = _heads(v, "v", q.dtype, k.shape)
+    dt, dtype, shape = _act_dtype(q), q.dtype, k.shape
+    qp, qs = _heads(q, "q", dtype)
+    kp, ks = _heads(k, "k", dtype)
+    vp, vs = _heads(v, "v", dtype, shape)
     Tq, Hq, D = q.shape
-    Tk, Hkv, Dk = k.shape
+    Tk, Hkv, Dk = shape
     if Dk != D:
         raise ValueError(f"q has head_dim {D}, k {Dk}")
     B = cu_q.numel() - 1
     if B < 0 or cu_q.shape != cu_k.shape:
         raise ValueError("cu_q and cu_k must have one offset more than there are sequences")
-    need = 0 if workspace is not None else attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt)
-    out, op, lp, wp, wb, keep = _attn_buffers(q, out, lse, workspace, need)
+    out, op, lp, wp, wb, keep = _attn_buffers(
+        q, out, lse, workspace, lambda: attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt))
     _check(load().ptq_attn_prefill(qp, kp, vp, qs, ks, vs, _dev(cu_q, torch.int32, "cu_q"),
                                    _dev(cu_k, torch.int32, "cu_k"), op, lp, B, Tq, Tk, Hq, Hkv, D,
                                    D ** -0.5 if scale is None else scale,
                                    PTQ_ATTN_CAUSAL if causal else 0, dt, wp, wb,
-                                   _stream(stream, q.device.index)), "ptq_attn_prefill")
+                                   _stream(stream, q.get_device())), "ptq_attn_prefill")
     return out
 
 
