@@ -72,12 +72,9 @@ struct Cfg {
   static constexpr int kRegsOther = kTiles == 2 ? 80 : 104;
   static constexpr int kOffRing = kTiles * kQ;
   static constexpr int kOffBar = kOffRing + kRing * kUnit;
-  // P over S's columns; at head_dim 64 TMEM has room for P beside S, and the
-  // next S is in work as soon as this one has been read.
-  static constexpr bool kApart = D == 64;
-  // full[kRing] empty[kRing] q[2] q free[2] s[2] read[2] p[2][2] o[2] o free[2] pv[2] turn[2]
+  // full[kRing] empty[kRing] q[2] q free[2] s[2] p[2][2] o[2] o free[2] pv[2] turn[2]
   // item full[2] item empty[2] sums full[2] sums empty[2] done
-  static constexpr int kBars = 2 * kRing + 4 + 2 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
   static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
   static constexpr int kOffSums = kOffItem + 2 * 64;  // (maximum, sum) of each row
   static constexpr int kOffMisc = kOffSums + kTiles * kRows * 8;
@@ -374,15 +371,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         int* status) {
   using C = Cfg<D>;
   constexpr int kTiles = C::kTiles;
-  constexpr bool kAfter = kTiles == 2 && !C::kApart;  // the next S goes where P was
+  constexpr bool kAfter = kTiles == 2;  // the next S goes where P was
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  // ring units; of a Q tile: Q there, Q read; of a slot: S written, S read (kApart), the first
-  // and second half of P written; of a Q tile: O final, O read, a product with V
+  // ring units; of a Q tile: Q there, Q read; of a slot: S written, the first and
+  // second half of P written; of a Q tile: O final, O read, a product with V
   // done (not where S's arrival says it), its turn to issue; items there, read; rows'
   // maxima and sums there, read
   uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing, *q_free = q_full + 2;
-  uint64_t *s_full = q_free + 2, *s_read = s_full + 2, *p_full = s_read + 2, *o_full = p_full + 4,
+  uint64_t *s_full = q_free + 2, *p_full = s_full + 2, *o_full = p_full + 4,
            *o_free = o_full + 2, *pv_done = o_free + 2, *turn = pv_done + 2, *item_full = turn + 2,
            *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 2,
            *all_done = ml_free + 2;
@@ -409,8 +406,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(q_full + i, 1);
       mbar_init(q_free + i, 1);
       mbar_init(s_full + i, 1);
-      mbar_init(s_read + i, 4);  // the four softmax warps of a tile
-      mbar_init(p_full + 2 * i, 4);
+      mbar_init(p_full + 2 * i, 4);  // the four softmax warps of a tile
       mbar_init(p_full + 2 * i + 1, 4);
       mbar_init(o_full + i, 1);
       mbar_init(o_free + i, 4);
@@ -596,7 +592,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       auto scores = [&](int j, Place at) {
         const int slot = slot_of(j);
         if (j == 0) wait(q_full + s, outs);
-        if (C::kApart && done + j > 0) wait(s_read + s, done + j - 1);  // S before it has been read
 #pragma unroll
         for (int k = 0; k < C::kUnits; ++k) {  // by columns
           if (!kAfter || j == 0) wait(full + at.st, at.phase);
@@ -658,7 +653,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (!mine) break;
           fence_after();
           if (ok && elected()) {
-            const uint32_t pa = tmem + (C::kApart ? 384 + slot * 64 : slot * kKeys) + 32 * half;
+            const uint32_t pa = tmem + slot * kKeys + 32 * half;
             const uint32_t d = tmem + 2 * kKeys + s * D;
             const uint32_t vd = tile_desc(ring + v.st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
                                           C::kVKeys * 128);
@@ -671,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
             if (half == 1 || C::kUnits == 2) release(j, v.st);
             if (half == 1) {
-              if (kTiles == 1 || C::kApart) mma_commit(pv_done + s);
+              if (kTiles == 1) mma_commit(pv_done + s);
               if (j == tiles - 1) mma_commit(o_full + s);
             }
           }
@@ -713,7 +708,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       for (int j = 0; j < tiles && ok; ++j) {
         const int g = done + j, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
         const uint32_t at = tmem + lanes + slot * kKeys;
-        const uint32_t p_at = C::kApart ? tmem + lanes + 384 + slot * 64 : at;
         ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, abort_flag));
         if (!ok) break;
         fence_after();
@@ -797,21 +791,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
             x[e] = bf16x2(x0, x1);
           }
-          if constexpr (C::kApart)  // the product with the tile before has read its P
-            if (half == 0 && g > 0)
-              ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, abort_flag));
-          tmem_st32(p_at + 32 * half, x);
+          tmem_st32(at + 32 * half, x);
         };
         auto publish = [&](int half) {
           tmem_wait_st();
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full + 2 * slot + half);
-        };
-        auto read_all = [&] {  // S may be written again
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_read + slot);
         };
         // The product with V starts on the first half.  The branch is worth more
         // than the work it saves in a last tile: without it the compiler computes
@@ -825,12 +811,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (left_hi > 64) {
           read_s(v, 64);
           tmem_wait_ld();
-          if constexpr (C::kApart) read_all();
           half_p(1);
         } else {
-          if constexpr (C::kApart) read_all();
           const uint32_t none[32] = {};
-          tmem_st32(p_at + 32, none);
+          tmem_st32(at + 32, none);
         }
         publish(1);
       }
