@@ -80,7 +80,11 @@ struct Cfg {
   static constexpr int kOffPart = (kOffScan + 2 * kWarps * 8 + 32 + 15) / 16 * 16;  // (m, l) of each head
   static constexpr int kSmem = kOffPart + 16 * 8;
   static constexpr int kFit = (227 * 1024) / (kSmem + 1024);
-  static constexpr int kPerSm = kFit < 1 ? 1 : kFit > 3 ? 3 : kFit;
+  // CTAs of an SM: two keep HBM busy (64 x 4096 tokens, 8 x 8 heads of 128, bf16
+  // cache: 164 us for 173 with three); at head_dim 64 the starts of short
+  // sequences count more (96 x 350 tokens, 16 heads: 31.7 us with three for 34.7).
+  static constexpr int kWish = D == 64 && kBlocks == 1 ? 3 : 2;
+  static constexpr int kPerSm = kFit < 1 ? 1 : kFit > kWish ? kWish : kFit;
   // a warp's output (kHeads rows of fp32) is handed over in a stage, a cluster's
   // CTA's where the query's fragments were
   static_assert(kStage >= kHeads * D * 4 && kQ >= kHeads * D * 4, "room for an output");
@@ -931,9 +935,10 @@ cudaError_t launch(const DecodeArgs& a, void* ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // Few short sequences: a cluster a (sequence, row block), whose CTAs join their
   // parts themselves (one launch).  Up to two tiles a warp: one sequence of 8 x 5
-  // heads of 128, fp32 over bf16, takes 6.4 us for 8.1 at 1 token, 8.9 for 9.8 at
-  // 1000, and 11.1 for 10.2 at 2000.  And while all run at once: at 56 clusters,
-  // which do not, 14.1 for 10.0.
+  // heads of 128, fp32 over bf16, takes 6.1 us for 6.9 at 1 token, 8.4 for 9.3 at
+  // 1000, but 11.1 for 10.2 at 2000; 4 x 7 heads of 64 in bf16 5.3 for 8.4 and 6.6
+  // for 9.5.  And while all run at once: 56 clusters, which do not, took 14.1 for
+  // 10.0.
   p.cluster = a.table_width * a.c.page_tokens <= 2 * kCluster * kWarps * C::kT &&
                       a.B * p.VH <= resident_clusters<T, D, kI8, kBlocks>()
                   ? kCluster
