@@ -4,8 +4,18 @@
 //   S = Q K^T,  P = 2^(S scale log2(e) - m),  O = P V,  out = O / sum P
 //
 // 4 head_dim operations a visible (query, key) pair and query head against
-// one exponential: the tensor cores bound it, the exponentials at head_dim
-// 64.
+// one exponential.  On long prompts the tensor cores and the shared memory that
+// feeds them bound it (at head_dim 64 the exponentials): a step of 128 keys and
+// two Q tiles of 128 columns is 2048 clocks of products, which read 192 KB and
+// for which 64 KB arrive, 2000 clocks at 128 bytes each; a step of one Q tile
+// of 256 columns is 2048 clocks of products and 320 KB, 2500 clocks.  On short
+// ones the chain S, softmax, P, O of each item's few steps bounds it.
+//
+// Measured, causal, bf16: 8192 tokens of 8 x 5 heads of 128 in 450 to 480 us
+// (1430 to 1525 TFLOP/s, 77 to 82% of a library product's rate), of 4 x 6 heads
+// of 256 at 1480 TFLOP/s, of 4 x 7 of 64 in 270 us (890); 16 prompts of up to
+// 1100 tokens in 75 us (800); two of up to 515 over prefixes of up to 7000,
+// 4 x 6 of 256, in 79 us (830, on 1.2 items an SM); 77 tokens in 7.4 us.
 //
 // Tile.  128 rows of Q are tpt tokens of hg query heads that share a kv head
 // (row = token * hg + head, one TMA box), against tiles of 128 keys.  S and O
@@ -34,6 +44,13 @@
 // A key that a row does not see has P = 0, and 0 times a non-finite value is
 // NaN: rows whose output is not finite though their sum is are computed again
 // one by one over the keys they see.
+//
+// All roles' code together is larger than the instruction cache: what runs once
+// an item is kept short, in loops where that costs nothing (a fifth of the
+// fetches missed when the kernel had 74 KB; at 53 KB 3% do, and the packed
+// prompts went from 101 us to 75).  Only the products and the softmax of a
+// tile are unrolled: the MMAs of both halves of P issued by one loop, whose
+// operands are then no constants, took 583 us for 466 at 8192 tokens.
 //
 // Every wait is bounded; one that runs out raises the device status word and
 // the CTA drains what it has in flight and exits.
@@ -987,7 +1004,9 @@ constexpr int64_t kSms = 152;
 // The heads of a Q tile: of the divisors of G, the one whose tiles of
 // floor(128 / heads) tokens waste the fewest rows on sequences of the mean
 // length (one sequence: on it; several: half a run each); the most heads where
-// several do (fewer K and V loads a row).
+// several do (fewer K and V loads a row).  Against one head a tile, five of
+// 128: 16 prompts of 25 tokens 6.4 us for 15.4, of 550 68 for 91; one of 8192
+// takes 450 either way.
 int heads_of_tile(int64_t G, int64_t B, int64_t Tq, int tiles) {
   const double mean = (double)Tq / (double)(B < 1 ? 1 : B < Tq ? B : Tq);
   int best = 1;
@@ -1011,8 +1030,9 @@ struct Plan {
 
 // Where the items fill less than half the SMs and the keys are long, each
 // item's keys are cut into parts of at least eight tiles, for about one item an
-// SM.  (An item costs about four tiles of its own: with 180 items of up to 55
-// tiles two parts took 84 us and one 78.)  A function of the shapes alone, so
+// SM: 64 queries over 8192 keys, 8 x 5 heads of 128, take 28 us so and 90 whole.
+// (An item costs about four tiles of its own: with 180 items of up to 55 tiles
+// two parts took 84 us and one 78.)  A function of the shapes alone, so
 // the workspace query and the launch agree.
 Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
   Plan r;
