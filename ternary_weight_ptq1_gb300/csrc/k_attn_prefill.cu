@@ -11,8 +11,8 @@
 // of 256 columns is 2048 clocks of products and 320 KB, 2500 clocks.  On short
 // ones the chain S, softmax, P, O of each item's few steps bounds it.
 //
-// Measured, causal, bf16: 8192 tokens of 8 x 5 heads of 128 in 450 to 480 us
-// (1430 to 1525 TFLOP/s, 77 to 82% of a library product's rate), of 4 x 6 heads
+// Measured, causal, bf16: 8192 tokens of 8 x 5 heads of 128 in 450 to 483 us
+// (1420 to 1525 TFLOP/s, 76 to 82% of a library product's rate), of 4 x 6 heads
 // of 256 at 1480 TFLOP/s, of 4 x 7 of 64 in 270 us (890); 16 prompts of up to
 // 1100 tokens in 75 us (800); two of up to 515 over prefixes of up to 7000,
 // 4 x 6 of 256, in 79 us (830, on 1.2 items an SM); 77 tokens in 7.4 us.

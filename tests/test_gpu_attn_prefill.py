@@ -241,3 +241,30 @@ def test_refusals(P):
     with pytest.raises(P.PTQError, match="ALIGN"):
         flat = torch.zeros(4 * 2 * 128 + 8, device="cuda", dtype=torch.bfloat16)
         P.attn_prefill(q, flat[4:-4].view(4, 2, 128), k, _cu([4]), _cu([4]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinite_keys(P, D):
+    """A key whose score is -infinity counts for nothing, and a row of such keys
+    alone is empty; +infinity and infinite values leave no finite row."""
+    import torch
+
+    rng = np.random.default_rng(53)
+    n, nq, Hq = 200, 3, 2
+    q = _values(rng, (4 * nq, Hq, D))
+    k, v = (_values(rng, (4, n, 1, D)) for _ in range(2))
+    q[:, :, 3] = 1.0
+    k[0, 17, 0, 3] = k[1, :, 0, 3] = -np.inf
+    k[2, 17, 0, 3] = np.inf
+    v[3, 17, 0, 5] = np.inf
+    lse = torch.full((4 * nq, Hq), 7.0, device="cuda")
+    out = _host(P.attn_prefill(_dev(q), _dev(k.reshape(-1, 1, D)), _dev(v.reshape(-1, 1, D)), _cu([nq] * 4),
+                               _cu([n] * 4), causal=False, lse=lse)).reshape(4, nq, Hq, D)
+    lse, q = _host(lse).reshape(4, nq, Hq), q.reshape(4, nq, Hq, D)
+    use = np.arange(n) != 17
+    for h in range(Hq):
+        ref = R.attend(q[0, :, h], k[0][use, 0], v[0][use, 0], D ** -0.5)
+        R.check(out[0, :, h], lse[0, :, h], ref, True, True)
+    assert (out[1] == 0).all() and np.isneginf(lse[1]).all()
+    assert np.isnan(out[2]).all() and np.isnan(lse[2]).all()
+    assert (out[3, ..., 5] == np.inf).all() and np.isfinite(out[3][..., np.arange(D) != 5]).all()
