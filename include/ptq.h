@@ -499,7 +499,7 @@ PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64
  * value that is seen makes the row NaN: the factors are split).  The work is
  * split by a rule on the shapes and the lengths alone, and the parts are joined
  * in a fixed order:
- * results are bitwise reproducible.  B = 0 is a no-op.
+ * results are bitwise reproducible.  B = 0 is a no-op; B is under 2^30.
  * workspace: device scratch of ptq_attn_decode_workspace_bytes(...) bytes,
  * 16-byte aligned, caller-owned, any initial contents.  Calls whose kernels
  * overlap on the GPU need separate workspaces.
@@ -535,7 +535,8 @@ PTQ_API size_t ptq_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t T
  * no effect on it, NaN and infinities included.
  * dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED (the fp32
  * route serves decode).  Probabilities enter the second product as bf16.
- * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op.  workspace
+ * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; B, Tq and Tk
+ * are under 2^30.  workspace
  * as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
  * Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for unknown flags. */
 #define PTQ_ATTN_CAUSAL 1u

@@ -84,13 +84,13 @@ ptq_status check_workspace(const void* ws, size_t ws_bytes, size_t need, const c
 
 bool decode_shape_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   int64_t t;
-  return B >= 0 && B <= INT32_MAX && heads_ok(Hq, Hkv) && D >= 1 && mul_ok(B, Hq, &t) &&
+  return B >= 0 && B <= INT32_MAX / 2 && heads_ok(Hq, Hkv) && D >= 1 && mul_ok(B, Hq, &t) &&
          t <= INT32_MAX && mul_ok(t, D, &t) && mul_ok(t, 4, &t);
 }
 
 bool prefill_shape_ok(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
   int64_t t;
-  return B >= 0 && B < INT32_MAX && Tq >= 0 && Tq <= INT32_MAX / 2 && Tk >= 0 &&
+  return B >= 0 && B <= INT32_MAX / 2 && Tq >= 0 && Tq <= INT32_MAX / 2 && Tk >= 0 &&
          Tk <= INT32_MAX / 2 && heads_ok(Hq, Hkv) && D >= 1 && mul_ok(Tq, Hq, &t) &&
          mul_ok(t, D, &t) && mul_ok(t, 4, &t);
 }

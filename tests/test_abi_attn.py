@@ -133,3 +133,14 @@ def test_binding_checks(P):
         P.KVCache(z.float(), z.float())
     with pytest.raises(ValueError, match="no scales"):
         P.KVCache(z, z, z, z)
+
+
+def test_more_sequences_than_can_be_counted_are_refused(P):
+    L = P.load()
+    c = ctypes.byref(_cache(P, kv_heads=1, head_dim=64))
+    assert L.ptq_attn_decode(P16, 64, c, P16, 4, P16, P16, None, 2 ** 30, 1, 0.1, P.PTQ_BF16, P16, 1 << 40,
+                             None) == 2
+    assert L.ptq_attn_prefill(P16, P16, P16, 64, 64, 64, P16, P16, P16, None, 2 ** 30, 8, 8, 1, 1, 64, 0.1, 0,
+                              P.PTQ_BF16, P16, 1 << 40, None) == 2
+    assert L.ptq_attn_decode_workspace_bytes(2 ** 30, 1, 1, 64, P.PTQ_BF16) == 0
+    assert L.ptq_attn_prefill_workspace_bytes(2 ** 30, 8, 8, 1, 1, 64, P.PTQ_BF16) == 0
