@@ -423,7 +423,8 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_embed_ptq1(
 /* PTQ_KV_BF16: rows are rounded to nearest-even bf16.
  * PTQ_KV_I8: a row x (one token, one head) is stored as
  *     s = max_d |x_d| / 127   (fp32, rounded to nearest)
- *     c_d = x_d / s rounded to the nearest integer, ties to even
+ *     c_d = x_d / s rounded to the nearest integer, ties to even, and to +-127
+ *           beyond (only a subnormal s is rounded so far that x_d / s passes 127)
  * and stands for c_d s.  A row of zeros has s = 0; a row that holds a
  * non-finite value has s = NaN and c = 0, and reads back as NaN. */
 typedef enum ptq_kv_type { PTQ_KV_BF16 = 0, PTQ_KV_I8 = 1 } ptq_kv_type;
