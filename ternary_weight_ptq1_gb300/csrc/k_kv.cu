@@ -86,14 +86,13 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float (&x)[kVec
   }
 }
 
-// round_half_even(x / s), given r near 1 / s: x r is within 1e-4 of the quotient,
-// and where that leaves the rounding open (or r is NaN) the division decides.  A
-// subnormal s is rounded by up to half of itself, so a quotient may pass 127 there
-// alone: the code stops at 127.
+// round_half_even(x / s) for |x| <= 127 s, given r near 1 / s: x r is within
+// 1e-4 of the quotient, and where that leaves the rounding open (or r is not
+// finite) the division decides.
 __device__ __forceinline__ int code_of(float x, float s, float r) {
   const float t = x * r;
   float n = rintf(t);
-  if (!(fabsf(t - n) < 0.4999f)) n = fminf(fmaxf(rintf(x / s), -127.0f), 127.0f);
+  if (!(fabsf(t - n) < 0.4999f)) n = rintf(x / s);
   return (int)n;
 }
 
@@ -138,7 +137,18 @@ __global__ void __launch_bounds__(kThreads)
       const float s = finite ? m / 127.0f : __int_as_float(0x7fc00000);
       uint32_t w[2] = {0, 0};
       if (s > 0.0f) {  // a row of zeros (or of values whose scale underflows) keeps zero codes
-        const float inv = s < FLT_MIN ? __int_as_float(0x7fc00000) : 1.0f / s;
+        // A scale of few bits is rounded by up to half of itself, and the row's
+        // largest values may pass 127 s: their codes are 127.  (The smallest bf16
+        // value, 2^16 units, gives a scale of 516: at most 127.2 of it.)
+        if constexpr (T == Act::F32) {
+          if (__builtin_expect(s < FLT_MIN, 0)) {
+            asm volatile("");  // a branch: as selections they take 3% of the write's time
+            const float lim = 127.0f * s;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[n][i] = fminf(fmaxf(x[n][i], -lim), lim);
+          }
+        }
+        const float inv = 1.0f / s;
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
           w[i >> 2] |= ((uint32_t)code_of(x[n][i], s, inv) & 0xffu) << (8 * (i & 3));
