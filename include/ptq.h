@@ -496,8 +496,11 @@ PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64
  *   out    B x q_heads x head_dim of dtype, contiguous
  *   lse    B x q_heads fp32, or NULL
  * softmax_scale is finite and positive.  With PTQ_F32 the arithmetic keeps
- * fp32 accuracy over both cache types (over a bf16 cache an infinite key or
- * value that is seen makes the row NaN: the factors are split).  The work is
+ * fp32 accuracy over both cache types: over int8 a weight times its value's
+ * scale has 22 bits, or 2^-35 of the row's largest such product.  Factors are
+ * split into 16-bit terms, so an infinite query (or a fp32 one past the largest
+ * bf16 value) makes its row NaN, except in bf16 over bf16, and over a bf16 cache
+ * with PTQ_F32 so does an infinite key or value that is seen.  The work is
  * split by a rule on the shapes and the lengths alone, and the parts are joined
  * in a fixed order:
  * results are bitwise reproducible.  B = 0 is a no-op; B is under 2^30.

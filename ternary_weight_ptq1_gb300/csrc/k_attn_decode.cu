@@ -42,7 +42,9 @@
 // the second, and the two rows' results are added (a kv head has rarely more
 // than eight query heads, so the second terms cost no instruction):
 //   int8 cache: two fp16 terms, 22 bits (q scaled by a power of two to its
-//     row's largest value, p by the largest value scale so far);
+//     row's largest value, p times its value's scale by the largest such product
+//     of the row so far: a value of great scale and no weight costs the others no
+//     bits);
 //   bf16 cache, bf16 q: q is exact, p has two bf16 terms, 16 bits;
 //   bf16 cache, fp32 q: three bf16 terms, the third in a second instruction.
 // More than eight heads take two row blocks a warp (kBlocks) up to head_dim
@@ -66,7 +68,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kWarps = 4;
 constexpr int kLead = 16;
-constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100, the smallest reference value scale
+constexpr float kTiny = 1.2037062152420224e-35f;  // 2^-116, the smallest reference weight
 constexpr float kPScale = 1024.0f;               // fp16 probabilities are stored times this
 
 template <Act T, int D, bool kI8, int kBlocks>
@@ -525,13 +527,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
 
     // head 8 h + g of the block: its maximum and sum so far, and its output
     // (first terms' rows, and without kFresh the second terms' rows apart)
-    float fac[kBlocks], m[kBlocks], l[kBlocks], vref = kTiny;
+    float fac[kBlocks], m[kBlocks], l[kBlocks];
+    float ref[kBlocks];  // (int8) power of two above every p times value scale so far, p as m is now
     float o[kBlocks][kNO][C::kFresh ? 2 : 4] = {};
 #pragma unroll
     for (int h = 0; h < kBlocks; ++h) {
       fac[h] = qfac[8 * h + g];
       m[h] = kNegInf;
       l[h] = 0.0f;
+      ref[h] = kTiny;
     }
 
     for (int tile = seg.t0 + warp; tile < seg.t1; tile += kWarps) {
@@ -586,17 +590,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
 
       // ---- softmax: column 2 t4 + i of group n is token 8 n + 2 t4 + i -------------
       const int left = seg.len - tile * kT;  // tokens of the tile that exist, if under kT
-      float inv = 1.0f, shrink = 1.0f;
-      if constexpr (kI8) {
-        // the power of two above the largest value scale so far (NaN stays)
-        const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(vs[lane]) & 0x7fffffffu);
-        const float ref = top < 0x7f000000u ? __uint_as_float((top & 0x7f800000u) + 0x00800000u)
-                                            : __uint_as_float(top);
-        const float nref = ref > vref || ref != ref ? ref : vref;
-        shrink = vref / nref;
-        vref = nref;
-        inv = kPScale / nref;
-      }
       // p as the second product's A: tokens 16 k .. + 15 are groups 2 k, 2 k + 1
       uint32_t ph[kBlocks][kNS][2], p3[kBlocks][C::kThree ? kNS : 1];
       float fade[kBlocks];
@@ -629,15 +622,35 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
         const float f = exp2_fast(m[h] - z);
         m[h] = top;
         l[h] *= f;
-        fade[h] = f * shrink;
+        fade[h] = f;
+        float inv = 1.0f, most = 0.0f;
 #pragma unroll
         for (int n = 0; n < kNS; ++n) {
-          float e0 = exp2_fast(s[h][n][0] - z), e1 = exp2_fast(s[h][n][1] - z);
+          float &e0 = s[h][n][0], &e1 = s[h][n][1];
+          e0 = exp2_fast(e0 - z), e1 = exp2_fast(e1 - z);
           l[h] += e0 + e1;
           if constexpr (kI8) {
             const float2 w = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * t4);
-            e0 *= w.x * inv, e1 *= w.y * inv;
+            e0 *= w.x, e1 *= w.y;
+            most = fmaxf(most, fmaxf(e0, e1));
           }
+        }
+        if constexpr (kI8) {
+          // The reference moves with m, down too, and up to the tile's largest weight,
+          // to 2^126 at most (larger weights still fit fp16; NaN stays in the products).
+          most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+          const float up = fmaxf(fmaxf(most, 0.5f * kTiny), 0.5f * ref[h] * f);
+          const uint32_t bits = (min(__float_as_uint(up), 0x7e000000u) & 0x7f800000u) + 0x00800000u;
+          const float over = __uint_as_float(0x7f000000u - bits);  // one over it
+          fade[h] = f * (ref[h] * over);
+          ref[h] = __uint_as_float(bits);
+          inv = kPScale * over;
+        }
+#pragma unroll
+        for (int n = 0; n < kNS; ++n) {
+          float e0 = s[h][n][0], e1 = s[h][n][1];
+          if constexpr (kI8) e0 *= inv, e1 *= inv;
           ph[h][n][0] = round2<kI8>(e0, e1);
           ph[h][n][1] = round2<kI8>(e0, e1);
           if constexpr (C::kThree) p3[h][n] = round2<kI8>(e0, e1);
@@ -721,9 +734,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     // Handed over in each warp's free stage, rows of D floats, 16-byte pieces
     // exchanged by row so that neighbouring rows use other banks.
     float* mine_o = reinterpret_cast<float*>(ring + stage * C::kStage);
-    const float back = kI8 ? vref / kPScale : 1.0f;
 #pragma unroll
     for (int h = 0; h < kBlocks; ++h) {
+      const float back = kI8 ? ref[h] / kPScale : 1.0f;
       l[h] += __shfl_xor_sync(~0u, l[h], 1);
       l[h] += __shfl_xor_sync(~0u, l[h], 2);
       const int r = 8 * h + g;

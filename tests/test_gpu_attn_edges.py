@@ -52,3 +52,78 @@ def test_codes_of_subnormal_rows_stay_in_range(P, D):
     k, v = P.kv_read(cache, slots, dtype=torch.float32)
     np.testing.assert_array_equal(k.cpu().numpy(), c * s[..., None])
     np.testing.assert_array_equal(v.cpu().numpy(), -c * s[..., None])
+
+
+# ---- decode over int8: weights and value scales ------------------------------------
+
+def _weighted_bound(q, k, v, vs, scale, bf16_out):
+    """The definition's output in 64 bits and what it may be off by, for one query
+    row over keys k, values v (rows as stored, their scales vs).
+
+    A score's error is that of attn_ref, for each key by itself: eps_j = 2^-21
+    sqrt(D) scale sum_d |q_d k_jd| + 2^-20.  It changes the normalised weight p_j by
+    at most p_j (eps_j + sum_i p_i eps_i) to first order (a tenth more covers the
+    rest).  Weights and sums are fp32 or a pair of fp16 terms, 2^-21 of each
+    product and 2^-24 of the sum for each addition; a pair of terms under the 16-bit
+    range keeps 2^-35 of the largest weighted scale, doubled for the power of two
+    above it, times a code of at most 127: 2^-27 for each key."""
+    q, k, v, vs = (np.asarray(a, np.float64) for a in (q, k, v, vs))
+    s = scale * (k @ q)
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    out = p @ v
+    eps = 2.0 ** -21 * np.sqrt(len(q)) * scale * (np.abs(k) @ np.abs(q)) + 2.0 ** -20
+    bound = 1.1 * (p * (eps + p @ eps)) @ np.abs(v)
+    bound = bound + (2.0 ** -21 + len(k) * 2.0 ** -24) * (p @ np.abs(v)) + len(k) * 2.0 ** -27 * (p * vs).max()
+    return out, bound + (2.0 ** -8 * np.abs(out) if bf16_out else 0)
+
+
+def _decode_weighted(P, k, v, q, act, page, width, what):
+    import torch
+
+    n, D = len(k), k.shape[-1]
+    pages = -(-n // page)
+    cache = P.KVCache.empty(pages, 1, page, D, torch.int8)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda()
+    P.kv_write(cache, dev(k)[:, None], dev(v)[:, None], slots)
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :pages] = torch.arange(pages, dtype=torch.int32)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = R.bf16(q) if act == "bf16" else q.astype(np.float32)
+    qd = dev(q)[None].to(torch.bfloat16 if act == "bf16" else torch.float32)
+    out = _host(P.attn_decode(qd, cache, table, lens))[0]
+    (kc, ks), (vc, vs) = R.quantise(k), R.quantise(v)
+    kk, vv = (c.astype(np.float64) * s[:, None].astype(np.float64) for c, s in ((kc, ks), (vc, vs)))
+    for h in range(len(q)):
+        ref, bound = _weighted_bound(q[h], kk, vv, vs, D ** -0.5, act == "bf16")
+        err = np.abs(out[h] - ref)
+        assert (err <= bound).all(), f"{what} head {h}: off by {(err / bound).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 5), (128, 12), (256, 3)])
+@pytest.mark.parametrize("width", [40, 200])      # a cluster's call, and runs
+def test_a_loud_value_of_no_weight_costs_no_accuracy(P, act, D, G, width):
+    rng = np.random.default_rng([D, G])
+    n = 300
+    for r in (8, 16, 24, 32, 60):
+        for where in (0, 17, 150, n - 1):
+            base = rng.standard_normal(D)
+            q = base + 0.05 * rng.standard_normal((G, D))
+            k, v = 0.3 * rng.standard_normal((n, D)), rng.standard_normal((n, D))
+            # weight 2^-r e^-25 or so: a score that much under the others'
+            k[where] = -base * (r * np.log(2) + 25) * np.sqrt(D) / (base @ base)
+            v[where] *= 2.0 ** r
+            _decode_weighted(P, k.astype(np.float32), v.astype(np.float32), q, act, 16, width, f"2^{r} at {where}")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-35, 1e-30, 1e30])
+def test_values_of_any_size(P, act, size):
+    rng = np.random.default_rng(3)
+    n, D = 150, 128
+    k, v = 0.3 * rng.standard_normal((n, D)), size * rng.uniform(0.5, 2.0, (n, D))
+    q = rng.standard_normal((5, D))
+    for width in (40, 200):
+        _decode_weighted(P, k.astype(np.float32), v.astype(np.float32), q, act, 16, width, f"{size}")
