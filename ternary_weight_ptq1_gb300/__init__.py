@@ -160,6 +160,24 @@ def _stream(stream=None, device=None) -> int:
 _raw_stream = None
 
 
+def _new(like, shape, dtype, stream, returned=True):
+    """An uninitialised tensor beside `like` for a call queued on `stream`.  It
+    is allocated on that stream, whose work alone then gets its memory before
+    the call has run or after the tensor is dropped; one that is returned is
+    marked as used on the current stream too."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def _dev(t, dtype=None, name="tensor"):
     if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -204,7 +222,7 @@ def unpack(wq, K: int, stream=None):
     import torch
 
     N = wq.shape[0]
-    out = torch.empty((N, K), dtype=torch.int8, device=wq.device)
+    out = _new(wq, (N, K), torch.int8, stream)
     _check(load().ptq1_unpack(_dev(wq, torch.uint8, "wq"), _dev(out), N, K, _stream(stream)),
            "ptq1_unpack")
     return out
@@ -214,7 +232,7 @@ def fwht(x, signs, out=None, stream=None):
     """Signed 1024-wide rotation of the rows of x (in place when out is x)."""
     import torch
 
-    y = torch.empty_like(x) if out is None else out
+    y = _new(x, x.shape, x.dtype, stream) if out is None else out
     M, K = x.shape
     _check(load().ptq_fwht(_dev(x, None, "x"), _dev(y, x.dtype, "out"), _dev(signs, torch.int8, "signs"),
                            M, K, _act_dtype(x), _stream(stream)), "ptq_fwht")
@@ -234,10 +252,10 @@ def matmul(wq, scales, x, out=None, workspace=None, stream=None):
     M, K = x.shape
     N = wq.shape[0]
     dt = _act_dtype(x)
-    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x, (M, N), x.dtype, stream) if out is None else out
     need = matmul_workspace_bytes(M, N, K, dt)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new(x, need, torch.uint8, stream, returned=False)
     ws = _dev(workspace, None, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().ptq_matmul(_dev(wq, torch.uint8, "wq"), _dev(scales, torch.int16, "scales"),
@@ -254,9 +272,9 @@ def matmul_bf16_accumulator(wq, scales, x, stream=None):
 
     M, K = x.shape
     N = wq.shape[0]
-    y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    y = _new(x, (M, N), torch.float32, stream)
     need = matmul_workspace_bytes(M, N, K, PTQ_BF16)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
+    ws = _new(x, need, torch.uint8, stream, returned=False) if need > 0 else None
     _check(load().ptq_matmul_bf16_accumulator(
         _dev(wq, torch.uint8, "wq"), _dev(scales, torch.int16, "scales"),
         _dev(x, torch.bfloat16, "x"), _dev(y, torch.float32, "out"), M, N, K,
@@ -281,7 +299,7 @@ def pq2_unpack(wq, K: int, stream=None):
     import torch
 
     N = wq.shape[0]
-    out = torch.empty((N, K), dtype=torch.int8, device=wq.device)
+    out = _new(wq, (N, K), torch.int8, stream)
     _check(load().ptq2_unpack(_dev(wq, torch.uint8, "wq"), _dev(out), N, K, _stream(stream)),
            "ptq2_unpack")
     return out
@@ -298,10 +316,10 @@ def matmul_pq2(wq, scales, x, out=None, workspace=None, stream=None):
     M, K = x.shape
     N = wq.shape[0]
     dt = _act_dtype(x)
-    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x, (M, N), x.dtype, stream) if out is None else out
     need = matmul_pq2_workspace_bytes(M, N, K, dt)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new(x, need, torch.uint8, stream, returned=False)
     ws = _dev(workspace, None, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().ptq_matmul_pq2(_dev(wq, torch.uint8, "wq"), _dev(scales, torch.int16, "scales"),
@@ -350,10 +368,10 @@ def rotate_matmul(wq, scales, x, signs, out=None, workspace=None, stream=None):
     M, K = x.shape
     N = wq.shape[0]
     dt = _act_dtype(x)
-    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else out
+    y = _new(x, (M, N), x.dtype, stream) if out is None else out
     if workspace is None:
-        workspace = torch.empty(max(1, rotate_matmul_workspace_bytes(M, N, K, dt)),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _new(x, max(1, rotate_matmul_workspace_bytes(M, N, K, dt)), torch.uint8, stream,
+                         returned=False)
     _check(load().ptq_rotate_matmul(_dev(wq, torch.uint8, "wq"),
                                     _dev(scales, torch.int16, "scales"), _dev(x, None, "x"),
                                     _dev(signs, torch.int8, "signs"), _dev(y, x.dtype, "out"), M, N,
@@ -376,8 +394,8 @@ def ffn(wgu_q, wgu_s, wd_q, wd_s, signs_in, signs_mid, x, out=None, workspace=No
     dt = _act_dtype(x)
     need = ffn_workspace_bytes(M, H, I, dt)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
-    y = torch.empty_like(x) if out is None else out
+        workspace = _new(x, max(need, 1), torch.uint8, stream, returned=False)
+    y = _new(x, x.shape, x.dtype, stream) if out is None else out
     _check(load().ptq_ffn(_dev(wgu_q, torch.uint8, "wgu_q"), _dev(wgu_s, torch.int16, "wgu_s"),
                           _dev(wd_q, torch.uint8, "wd_q"), _dev(wd_s, torch.int16, "wd_s"),
                           _dev(signs_in, torch.int8, "signs_in"),
@@ -426,7 +444,7 @@ def ffn_stack(layers, norm_w, x, eps: float, act=None, workspace=None, stream=No
     dt = _act_dtype(torch.empty(0, dtype=act or torch.float32))
     need = ffn_stack_workspace_bytes(M, H, I, dt)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        workspace = _new(x, max(need, 1), torch.uint8, stream, returned=False)
     arr = (FfnLayer * max(L, 1))()
     names = ("wgu_q", "wgu_s", "wd_q", "wd_s", "signs_in", "signs_mid")
     types = (torch.uint8, torch.int16, torch.uint8, torch.int16, torch.int8, torch.int8)
@@ -454,7 +472,7 @@ def ffn_noalloc(wgu_q, wgu_s, wd_q, wd_s, signs_in, signs_mid, x, out=None, stre
 
     M, H = x.shape
     I = signs_mid.shape[0]
-    y = torch.empty_like(x) if out is None else out
+    y = _new(x, x.shape, x.dtype, stream) if out is None else out
     _check(load().ptq_ffn_noalloc(_dev(wgu_q, torch.uint8, "wgu_q"), _dev(wgu_s, torch.int16, "wgu_s"),
                                   _dev(wd_q, torch.uint8, "wd_q"), _dev(wd_s, torch.int16, "wd_s"),
                                   _dev(signs_in, torch.int8, "signs_in"),
@@ -473,7 +491,7 @@ def embed(table, ids, signs, out=None, stream=None):
     dt = _act_dtype(table)
     V, H = table.shape
     M = ids.numel()
-    y = torch.empty((M, H), dtype=table.dtype, device=table.device) if out is None else out
+    y = _new(table, (M, H), table.dtype, stream) if out is None else out
     _check(load().ptq_embed(_dev(table, None, "table"), _dev(ids, torch.int32, "ids"),
                             _dev(signs, torch.int8, "signs"), _dev(y, table.dtype, "out"), M, V, H,
                             dt, _stream(stream)), "ptq_embed")
@@ -492,7 +510,7 @@ def embed_ptq1(wq, scales, ids, signs, out_dtype=None, out=None, stream=None):
         raise TypeError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
     V, H = scales.shape[0], scales.shape[1] * 128
     M = ids.numel()
-    y = torch.empty((M, H), dtype=out_dtype, device=wq.device) if out is None else out
+    y = _new(wq, (M, H), out_dtype, stream) if out is None else out
     _check(load().ptq_embed_ptq1(_dev(wq, torch.uint8, "wq"), _dev(scales, None, "scales"),
                                  _dev(ids, torch.int32, "ids"), _dev(signs, torch.int8, "signs"),
                                  _dev(y, out_dtype, "out"), M, V, H, dt, _stream(stream)),
@@ -600,9 +618,9 @@ def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
         dtype = k.dtype if k is not None else cache._bfloat16
     sp = _dev(slots, cache._int32, "slots")
     if k is None:
-        k = slots.new_empty(shape, dtype=dtype)
+        k = _new(slots, shape, dtype, stream)
     if v is None:
-        v = slots.new_empty(shape, dtype=dtype)
+        v = _new(slots, shape, dtype, stream)
     kp, ks = _heads(k, "k", dtype, shape)
     vp, vs = _heads(v, "v", dtype, shape)
     _check(load().ptq_kv_read(cache._ref, sp, shape[0], kp, vp, ks, vs, _act_dtype(k),
@@ -614,10 +632,10 @@ def attn_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: i
     return int(load().ptq_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, dtype))
 
 
-def _attn_buffers(q, out, lse, workspace, need):
+def _attn_buffers(q, out, lse, workspace, need, stream):
     """The output, the addresses of out and lse, the workspace, its address and size."""
     if out is None:
-        out = q.new_empty(q.shape)
+        out = _new(q, q.shape, q.dtype, stream)
     elif out.shape != q.shape:
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
     op = _dev(out, q.dtype, "out")
@@ -629,10 +647,10 @@ def _attn_buffers(q, out, lse, workspace, need):
         if lse.shape != q.shape[:2]:
             raise ValueError(f"lse must be {tuple(q.shape[:2])}, got {tuple(lse.shape)}")
         lp = _dev(lse, torch.float32, "lse")
-    if workspace is None and need() > 0:
+    if workspace is None and (wb := need()) > 0:
         import torch
 
-        workspace = q.new_empty(need(), dtype=torch.uint8)
+        workspace = _new(q, wb, torch.uint8, stream, returned=False)
     if workspace is not None:
         wp, wb = _dev(workspace, None, "workspace"), workspace.nbytes
     return out, op, lp, wp, wb, workspace
@@ -654,7 +672,7 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
     if len(ts) != 2 or ts[0] != B or lens.shape != (B,):
         raise ValueError("table must be sequences x pages, lens one count for each sequence")
     out, op, lp, wp, wb, keep = _attn_buffers(
-        q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt))
+        q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt), stream)
     _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, int32, "table"), ts[1],
                                   _dev(lens, int32, "lens"), op, lp, B, Hq,
                                   D ** -0.5 if scale is None else scale, dt, wp, wb,
@@ -688,7 +706,8 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     if B < 0 or cu_q.shape != cu_k.shape:
         raise ValueError("cu_q and cu_k must have one offset more than there are sequences")
     out, op, lp, wp, wb, keep = _attn_buffers(
-        q, out, lse, workspace, lambda: attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt))
+        q, out, lse, workspace, lambda: attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt),
+        stream)
     _check(load().ptq_attn_prefill(qp, kp, vp, qs, ks, vs, _dev(cu_q, torch.int32, "cu_q"),
                                    _dev(cu_k, torch.int32, "cu_k"), op, lp, B, Tq, Tk, Hq, Hkv, D,
                                    D ** -0.5 if scale is None else scale,
@@ -710,7 +729,7 @@ def matmul_f32_peel(wq, scales, x, out=None, stream=None):
 
     M, K = x.shape
     N = wq.shape[0]
-    y = torch.empty((M, N), dtype=torch.float32, device=x.device) if out is None else out
+    y = _new(x, (M, N), torch.float32, stream) if out is None else out
     _check(load().ptq_matmul_f32_peel(
         _dev(wq, torch.uint8, "wq"), _dev(scales, torch.int16, "scales"),
         _dev(x, torch.float32, "x"), _dev(y, torch.float32, "out"), M, N, K, _stream(stream)),

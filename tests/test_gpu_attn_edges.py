@@ -127,3 +127,49 @@ def test_values_of_any_size(P, act, size):
     q = rng.standard_normal((5, D))
     for width in (40, 200):
         _decode_weighted(P, k.astype(np.float32), v.astype(np.float32), q, act, 16, width, f"{size}")
+
+
+# ---- streams -----------------------------------------------------------------------
+
+def test_default_buffers_on_another_stream(P):
+    """Calls queued on a stream behind other work, with the buffers they allocate
+    themselves, while the current stream fills new tensors of the same sizes."""
+    import torch
+
+    rng = np.random.default_rng(51)
+    B, Hkv, G, D, page = 5, 4, 5, 128, 16
+    lens = [3000, 1, 777, 2048, 90]
+    pages = -(-max(lens) // page)
+    cache = P.KVCache.empty(B * pages, Hkv, page, D, torch.int8)
+    table = torch.randperm(B * pages, device="cuda").to(torch.int32).view(B, pages)
+    slots = torch.arange(B * pages * page, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(len(slots), Hkv, D, device="cuda") for _ in range(2))
+    q = torch.randn(B, Hkv * G, D, device="cuda")
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    # few queries over many keys: the prompts' keys are cut into parts
+    nq, nk = 40, 9000
+    pq, pk, pv = (torch.randn(n, h, D, device="cuda").bfloat16() for n, h in ((nq, G), (nk, 1), (nk, 1)))
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (nq, nk))
+    assert P.attn_prefill_workspace_bytes(1, nq, nk, G, 1, D, P.PTQ_BF16) > 0
+
+    def calls(stream):
+        kr, vr = P.kv_read(cache, slots[:999], dtype=torch.float32, stream=stream)
+        return [kr, vr, P.attn_decode(q, cache, table, lens_d, stream=stream),
+                P.attn_prefill(pq, pk, pv, cu_q, cu_k, stream=stream)]
+
+    P.kv_write(cache, k, v, slots)
+    want = [t.clone() for t in calls(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)   # some 10 ms
+        got = calls(side)
+        sizes = [P.attn_decode_workspace_bytes(B, Hkv * G, Hkv, D, P.PTQ_F32),
+                 P.attn_prefill_workspace_bytes(1, nq, nk, G, 1, D, P.PTQ_BF16)] + [t.nbytes for t in got]
+        fill = [torch.full((n,), 0xAA, dtype=torch.uint8, device="cuda") for n in sizes * 2]
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert all((t == 0xAA).all() for t in fill)
+        del got, fill

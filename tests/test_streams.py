@@ -1,0 +1,133 @@
+"""Buffers that a call allocates for itself belong to the stream it is queued
+on.  On the host: a stand-in for a CUDA tensor notes the stream it was
+allocated on, and a stand-in library takes the call."""
+import contextlib
+import types
+
+import pytest
+
+
+class _Tensor:
+    is_cuda = True
+
+    def __init__(self, world, shape, dtype, stream="made by the caller"):
+        import torch
+
+        self.world, self.shape, self.dtype, self.stream = world, torch.Size(shape), dtype, stream
+        self.used = []
+        world.made.append(self)
+
+    device = "cuda:0"
+    data_ptr = lambda self: 4096 * (1 + self.world.made.index(self))
+    is_contiguous = lambda self: True
+    get_device = lambda self: 0
+    numel = lambda self: self.shape.numel()
+    element_size = lambda self: self.dtype.itemsize
+    nbytes = property(lambda self: self.numel() * self.element_size())
+    dim = lambda self: len(self.shape)
+
+    def new_empty(self, shape, dtype=None):
+        shape = (shape,) if isinstance(shape, int) else shape
+        return _Tensor(self.world, shape, dtype or self.dtype, self.world.current)
+
+    def record_stream(self, stream):
+        self.used.append(stream)
+
+
+@pytest.fixture
+def world(monkeypatch):
+    import torch
+
+    import ternary_weight_ptq1_gb300 as P
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    w = types.SimpleNamespace(P=P, made=[], calls=[], main=Stream(1), side=Stream(2))
+    w.current = w.main
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, w.current = w.current, stream
+        yield
+        w.current = before
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("workspace_bytes"):
+                    return 1 << 20
+                w.calls.append((name, args))
+                return 0
+            return call
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: w.current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", lambda *shape, dtype=None, device=None: _Tensor(
+        w, shape[0] if isinstance(shape[0], tuple) else shape, dtype, w.current))
+    monkeypatch.setattr(torch, "empty_like", lambda t: t.new_empty(t.shape))
+    monkeypatch.setattr(P, "load", lambda path=None: Library())
+    raw = lambda device: w.current.cuda_stream  # noqa: E731
+    monkeypatch.setattr(P, "_raw_stream", raw)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", raw, raising=False)
+    w.new = lambda shape, dtype: _Tensor(w, shape, dtype)
+    return w
+
+
+def _calls(w):
+    import torch
+
+    P, new = w.P, w.new
+    f32, bf16, i8, i16, i32, u8 = (torch.float32, torch.bfloat16, torch.int8, torch.int16, torch.int32, torch.uint8)
+    x, wq, sc, sg = new((4, 1024), f32), new((256, 208), u8), new((256, 8), i16), new((1024,), i8)
+    ids = new((4,), i32)
+    cache = types.SimpleNamespace(kv_heads=2, head_dim=64, _int32=i32, _bfloat16=bf16, _ref=64, k=new((1, 2, 4, 64), i8))
+    q, k, cu = new((4, 4, 64), bf16), new((4, 2, 64), bf16), new((2,), i32)
+    block = (new((2048, 208), u8), sc, wq, sc, sg, sg)
+    return {
+        "matmul_f32_peel": lambda **s: P.matmul_f32_peel(wq, sc, x, **s),
+        "unpack": lambda **s: P.unpack(wq, 1024, **s),
+        "fwht": lambda **s: P.fwht(x, sg, **s),
+        "matmul": lambda **s: P.matmul(wq, sc, x, **s),
+        "accumulator": lambda **s: P.matmul_bf16_accumulator(wq, sc, new((4, 1024), bf16), **s),
+        "pq2_unpack": lambda **s: P.pq2_unpack(wq, 1024, **s),
+        "matmul_pq2": lambda **s: P.matmul_pq2(wq, sc, x, **s),
+        "rotate_matmul": lambda **s: P.rotate_matmul(wq, sc, x, sg, **s),
+        "ffn": lambda **s: P.ffn(*block, x, **s),
+        "ffn_noalloc": lambda **s: P.ffn_noalloc(*block, x, **s),
+        "embed": lambda **s: P.embed(x, ids, sg, **s),
+        "embed_ptq1": lambda **s: P.embed_ptq1(wq, sc, ids, sg, **s),
+        "kv_read": lambda **s: P.kv_read(cache, ids, **s),
+        "attn_decode": lambda **s: P.attn_decode(q, cache, new((4, 3), i32), ids, **s),
+        "attn_prefill": lambda **s: P.attn_prefill(q, k, k, cu, cu, **s),
+    }
+
+
+NAMES = ("matmul_f32_peel", "unpack", "fwht", "matmul", "accumulator", "pq2_unpack", "matmul_pq2", "rotate_matmul",
+         "ffn", "ffn_noalloc", "embed", "embed_ptq1", "kv_read", "attn_decode", "attn_prefill")
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_buffers_belong_to_the_calls_stream(world, name):
+    call = _calls(world)[name]
+    n = len(world.made)
+    back = call(stream=world.side)
+    made = [t for t in world.made[n:] if t.stream != "made by the caller"]
+    assert made and all(t.stream is world.side for t in made), [t.shape for t in made if t.stream is not world.side]
+    # what the caller gets is used on its current stream too
+    for t in back if isinstance(back, tuple) else (back,):
+        assert t.used == [world.main]
+    (_, args), = world.calls
+    assert args[-1] == 2                    # queued on the side stream
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_a_stream_they_belong_to_the_current_one(world, name):
+    call = _calls(world)[name]
+    n = len(world.made)
+    call()
+    made = [t for t in world.made[n:] if t.stream != "made by the caller"]
+    assert made and all(t.stream is world.main and not t.used for t in made)
