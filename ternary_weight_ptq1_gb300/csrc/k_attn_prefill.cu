@@ -52,8 +52,9 @@
 // tile are unrolled: the MMAs of both halves of P issued by one loop, whose
 // operands are then no constants, took 583 us for 466 at 8192 tokens.
 //
-// Every wait is bounded; one that runs out raises the device status word and
-// the CTA drains what it has in flight and exits.
+// Every wait is bounded (to some 6 s, or to so long without progress of the CTA);
+// one that runs out raises the device status word and the CTA drains what it has in
+// flight and exits.
 #include <cuda_bf16.h>
 
 #include "async_util.cuh"
@@ -128,12 +129,22 @@ static_assert(sizeof(Item) <= 64, "its place in shared memory");
 
 __device__ __forceinline__ int clamped(int v, int hi) { return min(max(v, 0), hi); }
 
+// What the warps of a CTA tell one another beside the barriers.
+struct Pulse {
+  int abort;  // a wait ran out
+  int beat;   // moves on as K and V tiles are loaded, and in whatever else takes long
+};
+
 // A bounded wait, in few instructions: the warps' roles together are larger than
-// the instruction cache.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// the instruction cache.  It gives up after kWaitLimit polls of 1.5 us; kItem: a
+// wait that may last a whole item, which goes on while the CTA makes progress.
+// (As all of them it took 1 to 2% of the prompts' time.)
+template <bool kItem = false>
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile Pulse* pulse) {
   const uint32_t at = smem_addr(bar);
+  int beat = -1;
 #pragma unroll 1
-  for (uint32_t i = kWaitLimit; i > 0; --i) {
+  for (uint32_t i = kWaitLimit;;) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
@@ -142,9 +153,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
         : "r"(at), "r"(parity)
         : "memory");
     if (done) return true;
-    if (*abort) return false;
+    if (pulse->abort) return false;
+    if (--i == 0) {
+      const int now = kItem ? pulse->beat : beat;
+      if (now == beat) return false;
+      beat = now, i = kWaitLimit;
+    }
   }
-  return false;
 }
 
 struct Span {
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
            *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 2,
            *all_done = ml_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile Pulse* pulse = reinterpret_cast<volatile Pulse*>(smem + C::kOffMisc + 8);
 
   const PrefillArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -435,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(ml_free + i, 4);
     }
     mbar_init(all_done, kTiles);
-    *abort_flag = 0;
+    pulse->abort = pulse->beat = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   fence_before();
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
   int seen = 0;  // items read
   auto read_item = [&](Item& it, bool one_lane) {
-    const bool there = bar_wait(item_full + (seen & 1), (seen >> 1) & 1, abort_flag);
+    const bool there = bar_wait<true>(item_full + (seen & 1), (seen >> 1) & 1, pulse);
     ok = one_lane ? there : __all_sync(~0u, there);
     if (!ok) return false;
     const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -500,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
       }
       if (seen >= 2)
-        ok = __all_sync(~0u, bar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait<true>(item_free + (seen & 1), ((seen >> 1) - 1) & 1, pulse));
       if (!ok) break;
       if (lane == 0) {
         volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -517,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (it.n[s] == 0) continue;
         const int y = it.q0 + it.first + s * p.tpt;
         if (lane < D / 64) tma_3d_prefetch(&map_q, 64 * lane, it.hq0, y);
-        if (qn[s] > 0) ok = ok && __all_sync(~0u, bar_wait(q_free + s, (qn[s] - 1) & 1, abort_flag));
+        if (qn[s] > 0) ok = ok && __all_sync(~0u, bar_wait<true>(q_free + s, (qn[s] - 1) & 1, pulse));
         if (!ok) break;
         ++qn[s];
         if (lane == 0) {
@@ -546,10 +561,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll 1
         for (int k = 0; k < C::kUnits; ++k, ++u) {
           const int st = u % C::kRing, round = u / C::kRing, y = key0 + j * kKeys;
-          if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, abort_flag));
+          if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, pulse));
           if (!ok) break;
           if (elected()) {  // boxes of 64 columns: K by columns, V by keys
             const uint32_t to = ring + st * C::kUnit;
+            pulse->beat = u;
             mbar_expect_tx(full + st, C::kUnit);
             if (v) {
 #pragma unroll
@@ -578,7 +594,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // and one waits for barriers while the other's MMAs run -------------------------
     const int s = warp - kMma;
     auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, abort_flag));
+      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, pulse));
     };
     struct Place {  // in the ring
       int st;
@@ -725,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       for (int j = 0; j < tiles && ok; ++j) {
         const int g = done + j, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
         const uint32_t at = tmem + lanes + slot * kKeys;
-        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, abort_flag));
+        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, pulse));
         if (!ok) break;
         fence_after();
         const int left = sees - j * kKeys, left_lo = least - j * kKeys, left_hi = best - j * kKeys;
@@ -773,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           // O moves to the new maximum once the product with the tile before is
           // done (where S follows P, S says so)
           if constexpr (!kAfter) {
-            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, abort_flag));
+            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, pulse));
             if (!ok) break;
           }
           const float mn = t2 > m + kSlack ? t2 : m;
@@ -843,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       float lo, hi;
       unpair(add2(sum2[0], sum2[1]), lo, hi);
       if (outs > 0) {
-        ok = __all_sync(~0u, bar_wait(ml_free + s, (outs - 1) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait<true>(ml_free + s, (outs - 1) & 1, pulse));
         if (!ok) break;
       }
       ++outs;
@@ -867,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int tok = first + my_tok, hq = it.hq0 + my_head;
         const bool mine = row < p.hg * p.tpt && tok < it.nq;
         const int64_t out_row = (int64_t)(it.q0 + tok) * a.Hq + hq;
-        ok = __all_sync(~0u, bar_wait(ml_full + s, (told >> s) & 1, abort_flag));
+        ok = __all_sync(~0u, bar_wait<true>(ml_full + s, (told >> s) & 1, pulse));
         if (!ok) break;
         told ^= 1u << s;
         const float2 ml = sums[s * kRows + row];
@@ -881,7 +897,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             a.lse[out_row] = l == 0.0f ? kNegInf : (ml.x + __log2f(l)) * kLn2;
         }
         if (tiles > 0) {
-          ok = __all_sync(~0u, bar_wait(o_full + s, (outs >> s) & 1, abort_flag));
+          ok = __all_sync(~0u, bar_wait(o_full + s, (outs >> s) & 1, pulse));
           if (!ok) break;
           outs ^= 1u << s;
           fence_after();
@@ -949,10 +965,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
   }
   if (!ok) {
-    *abort_flag = 1;
+    pulse->abort = 1;
     if (lane == 0) atomicOr(status, kDevTimeout);
   }
-  if (*abort_flag && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
+  if (pulse->abort && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
   fence_before();
   __syncthreads();
   if (warp == kMma) {
