@@ -109,6 +109,7 @@ struct Args {
   int G, hg, tpt;  // query heads of a kv head; heads and tokens of a Q tile
   int heads;       // head blocks in all
   Divider by_per, by_heads, by_G, by_hg;  // by_per: head blocks times parts
+  Divider by_run;  // queries of an item: the Q tiles' tokens
   int splits;      // parts the keys of each item are cut into
   float* part;     // splits > 1: [splits][Tq Hq][D] output sums, and the (maximum,
   float2* ml;      // sum) they refer to, [splits][Tq Hq]
@@ -340,45 +341,69 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 // ---- the order of the work -----------------------------------------------------------
 // Sequences are cut into runs of `run` queries.  The runs that come late in
-// their sequence (under a causal mask those with the most keys) are first:
-// level by level downwards, and through the sequences in each level.  One warp
-// walks them, each time further on.
+// their sequence (under a causal mask those with the most keys) are first: band
+// by band of levels downwards, through the sequences in each band, and downwards
+// in each sequence's part of the band.  One warp walks them, each time further on,
+// 32 sequences a step; a band is one level, or as many as keep the walk to kSteps
+// steps (or to one way through the sequences).
+constexpr int kSteps = 4096;
+
 struct Walk {
-  int level, before;  // runs of higher levels
+  int base;      // the band's first level
+  int band;      // its levels
+  int b0;        // the next 32 sequences
+  int before;    // runs before them
 };
 
-__device__ __forceinline__ int queries_of(const PrefillArgs& a, int b) {
+// The runs of sequence b.
+__device__ __forceinline__ int runs_of(const Args& p, int b) {
+  const PrefillArgs& a = p.a;
   if (b >= (int)a.B) return 0;
   const int Tq = (int)a.Tq;
-  return max(0, clamped(__ldg(a.cu_q + b + 1), Tq) - clamped(__ldg(a.cu_q + b), Tq));
+  const int n = max(0, clamped(__ldg(a.cu_q + b + 1), Tq) - clamped(__ldg(a.cu_q + b), Tq));
+  return p.by_run(n + p.by_run.d - 1);
 }
 
-__device__ __forceinline__ Walk walk_from_top(const PrefillArgs& a, int run) {
+__device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pulse) {
   int most = 0;
 #pragma unroll 1
-  for (int b = threadIdx.x & 31; b < (int)a.B; b += 32) most = max(most, queries_of(a, b));
-  return {((int)__reduce_max_sync(~0u, most) + run - 1) / run - 1, 0};
+  for (int b = threadIdx.x & 31; b < (int)p.a.B; b += 32) {
+    most = max(most, runs_of(p, b));
+    pulse->beat = b;
+  }
+  most = (int)__reduce_max_sync(~0u, most);
+  // most / band ways of B / 32 steps
+  const int ways = max(1, kSteps / (((int)p.a.B + 31) / 32)), band = (most + ways - 1) / ways;
+  return {most > 0 ? (most - 1) / band * band : -1, band, 0, 0};
 }
 
 // The sequence and level of run i in that order; false: there are not so many.
-__device__ __forceinline__ bool walk_to(const PrefillArgs& a, int run, int i, Walk& w, int* seq) {
-  const int lane = threadIdx.x & 31, first = queries_of(a, lane);
+// i grows from call to call.
+__device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq, int* level,
+                                        volatile Pulse* pulse) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (; w.level >= 0; --w.level) {
-    int n = w.before;
+  for (; w.base >= 0; w.base -= w.band, w.b0 = 0) {
 #pragma unroll 1
-    for (int b0 = 0; b0 < (int)a.B; b0 += 32) {
-      const bool mine = (b0 ? queries_of(a, b0 + lane) : first) > w.level * run;
-      const unsigned has = __ballot_sync(~0u, mine);
-      const int rank = n + __popc(has & ((1u << lane) - 1));
-      const unsigned at = __ballot_sync(~0u, mine && rank == i);
+    for (; w.b0 < (int)p.a.B; w.b0 += 32) {
+      const int mine = min(max(runs_of(p, w.b0 + lane) - w.base, 0), w.band);
+      int end = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, end, d);
+        if (lane >= d) end += o;
+      }
+      const int in = i - w.before;
+      const unsigned at = __ballot_sync(~0u, in < end);
       if (at) {
-        *seq = b0 + __ffs(at) - 1;
+        const int who = __ffs(at) - 1;
+        *seq = w.b0 + who;
+        *level = w.base + __shfl_sync(~0u, end, who) - 1 - in;
         return true;
       }
-      n += __popc(has);
+      w.before += __shfl_sync(~0u, end, 31);
+      pulse->beat = w.before;
     }
-    w.before = n;
   }
   return false;
 }
@@ -481,8 +506,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // ---- the items of this CTA, one ahead of their use, and their Q tiles, into L2 at
     // once and into shared memory when the tile before has been read ------------------
     int qn[kTiles] = {};  // Q tiles loaded
-    const int run = kTiles * p.tpt;
-    Walk walk = walk_from_top(a, run);
+    Walk walk = walk_from_top(p, pulse);
     for (int round = 0; ok; ++round) {
       // long items first, dealt out there and back, so that the CTAs' sums are alike
       const int i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -490,8 +514,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       // heads fastest: the long items of all of them come first
       const int n = p.by_per(i), sub = i - n * p.by_per.d;
       it.b = -1;
-      if (walk_to(a, run, n, walk, &it.b)) {
-        const int t = walk.level;
+      int t;
+      if (walk_to(p, n, walk, &it.b, &t, pulse)) {
         const Span sp = span_of(a, it.b);
         it.split = p.by_heads(sub);
         it.q0 = sp.q0, it.nq = sp.nq, it.k0 = sp.k0, it.nk = sp.nk;
@@ -1081,7 +1105,7 @@ cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int G = (int)(a.Hq / a.Hkv);
   Args p{a, G, 0, 0, 0, Divider(plan.heads * plan.splits), Divider(plan.heads), Divider(G), Divider(plan.hg),
-         0, nullptr, nullptr};
+         Divider(C::kTiles * plan.tpt), 0, nullptr, nullptr};
   p.hg = plan.hg;
   p.tpt = plan.tpt;
   p.splits = plan.splits;

@@ -173,3 +173,65 @@ def test_default_buffers_on_another_stream(P):
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         assert all((t == 0xAA).all() for t in fill)
         del got, fill
+
+
+# ---- prompts: many sequences ---------------------------------------------------------
+
+def _prompts(P, rng, nqs, nks, Hkv, G, D, causal, pick):
+    """Packed prompts against the definition, the sequences `pick` of them."""
+    import torch
+
+    q, k, v = (R.bf16(rng.standard_normal((n, h, D)).astype(np.float32))
+               for n, h in ((sum(nqs), Hkv * G), (sum(nks), Hkv), (sum(nks), Hkv)))
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(n)]) for n in (nqs, nks))
+    dev = lambda x: torch.from_numpy(x).cuda()
+    lse = torch.full((sum(nqs), Hkv * G), 7.0, device="cuda")
+    out = P.attn_prefill(dev(q).bfloat16(), dev(k).bfloat16(), dev(v).bfloat16(), dev(cu_q.astype(np.int32)),
+                         dev(cu_k.astype(np.int32)), causal=causal, lse=lse)
+    P.device_check()
+    out, lse = _host(out), _host(lse)
+    assert np.isfinite(out).all()
+    for b in pick:
+        (q0, q1), (k0, k1) = cu_q[b:b + 2], cu_k[b:b + 2]
+        i, j = np.arange(q1 - q0)[:, None], np.arange(k1 - k0)[None]
+        seen = (j <= i + (k1 - k0) - (q1 - q0)) if causal else np.ones((q1 - q0, k1 - k0), bool)
+        rows = np.arange(q1 - q0) if q1 - q0 < 200 else np.unique(np.linspace(0, q1 - q0 - 1, 60).astype(int))
+        for hq in range(Hkv * G):
+            ref = R.attend(q[q0 + rows, hq], k[k0:k1, hq // G], v[k0:k1, hq // G], D ** -0.5, seen[rows])
+            R.check(out[q0 + rows, hq], lse[q0 + rows, hq], ref, True, True, f"seq {b} head {hq}")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B,long,D,Hkv,G", [(33, 200, 128, 1, 5), (65, 900, 256, 1, 2), (700, 900, 64, 2, 1),
+                                            (3001, 700, 64, 1, 2), (20000, 3000, 64, 1, 1), (140001, 3000, 64, 1, 1)])
+def test_many_prompts(P, B, long, D, Hkv, G, causal):
+    """More sequences than one step of the planning warp sees, most of them short;
+    in the large batches several runs of a long prompt are dealt out at once."""
+    rng = np.random.default_rng([B, D])
+    nqs = rng.integers(0, 4, B)
+    at = [0, B // 3, B // 2, B - 2]
+    nqs[at] = [long, long // 2, 130, long - 77]
+    nks = nqs + (rng.random(B) < 0.3) * rng.integers(0, 3, B)
+    pick = list(range(min(B, 40))) + at + list(range(max(0, B - 40), B)) + list(rng.integers(0, B, 60))
+    _prompts(P, rng, nqs.tolist(), nks.tolist(), Hkv, G, D, causal, sorted(set(pick)))
+
+
+def test_planning_grows_with_the_batch_alone(P):
+    """65,536 prompts of a token: the planning warp's walk once took a step for
+    every 32 sequences for every item (3.5 million of them a CTA, a third of a
+    second); 3,450 items a CTA take some milliseconds."""
+    import torch
+
+    n, H, D = 65536, 8, 64
+    q, k, v = (torch.randn(n, H, D, device="cuda").bfloat16() for _ in range(3))
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out = P.attn_prefill(q, k, v, cu, cu)
+    P.device_check()
+    assert torch.equal(out, v)              # one key has all the weight
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    P.attn_prefill(q, k, v, cu, cu, out=out)
+    b.record()
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) < 60
+    print(f"{a.elapsed_time(b):.2f} ms")
