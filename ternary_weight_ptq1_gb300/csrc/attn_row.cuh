@@ -1,7 +1,6 @@
-// attn_row.cuh -- attention of one query row, a warp at a time: lane l holds
-// the values [l D/32, (l + 1) D/32) of the query, a key, a value and the
-// output, a score is a shuffle sum, and the softmax is kept as a running
-// maximum m and sum l (base 2):
+// attn_row.cuh -- attention of one query row by a warp: lane l holds the columns
+// [l D/32, (l + 1) D/32) of the output, a key's score is one lane's, and the
+// softmax is kept as a running maximum m and sum l (base 2):
 //     m' = max(m, s),  a = 2^(m - m'),  p = 2^(s - m'),
 //     l = l a + p,  o = o a + p v.
 // fp32 throughout.
@@ -20,22 +19,19 @@ struct RowState {
   float m = kNegInf, l = 0.0f;
   float o[D / 32] = {};
 
-  // One more key and value; scale2 = softmax scale * log2(e).
-  __device__ __forceinline__ void add(const float (&q)[D / 32], const float (&k)[D / 32],
-                                      const float (&v)[D / 32], float scale2) {
-    float s = 0.0f;
+  // 32 more keys, a score in units of log2 a lane: the lane's weight, which is in l
+  // (the lane's share of the sum) but not yet in o.
+  __device__ __forceinline__ float weigh(float s) {
+    float mn = fmaxf(m, s);  // a NaN score leaves m and makes its weight NaN
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(~0u, s, i);
-    s *= scale2;
-    const float mn = fmaxf(m, s);  // a NaN score leaves m and makes p NaN
+    for (int i = 16; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(~0u, mn, i));
     const float a = mn == kNegInf ? 1.0f : exp2f(m - mn);
     const float p = s == kNegInf ? 0.0f : exp2f(s - mn);
     m = mn;
     l = fmaf(l, a, p);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], a, p * v[i]);
+    for (int i = 0; i < D / 32; ++i) o[i] *= a;
+    return p;
   }
 
   // The state of both of two disjoint sets of keys.

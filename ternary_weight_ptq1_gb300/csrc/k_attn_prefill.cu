@@ -41,9 +41,11 @@
 // the items are few and the keys long, the keys are cut into parts whose sums
 // a second kernel joins in order.
 //
-// A key that a row does not see has P = 0, and 0 times a non-finite value is
-// NaN: rows whose output is not finite though their sum is are computed again
-// one by one over the keys they see.
+// A key that a row does not see has P = 0, and 0 times a non-finite value is NaN.
+// The values past a sequence's end are cleared in shared memory; rows that a value
+// hidden from them by the causal mask has spoilt are computed again one by one over
+// the keys they see (8192 tokens, 8 x 5 heads of 128, 0.46 ms: with the last token's
+// value infinite 18 ms, with the first one's, which every row sees, 0.64).
 //
 // All roles' code together is larger than the instruction cache: what runs once
 // an item is kept short, in loops where that costs nothing (a fifth of the
@@ -91,8 +93,8 @@ struct Cfg {
   static constexpr int kOffRing = kTiles * kQ;
   static constexpr int kOffBar = kOffRing + kRing * kUnit;
   // full[kRing] empty[kRing] q[2] q free[2] s[2] p[2][2] o[2] o free[2] pv[2] turn[2]
-  // item full[2] item empty[2] sums full[2] sums empty[2] done
-  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+  // item full[2] item empty[2] sums full[2] sums empty[2] tail full done
+  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1;
   static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
   static constexpr int kOffSums = kOffItem + 2 * 64;  // (maximum, sum) of each row
   static constexpr int kOffMisc = kOffSums + kTiles * kRows * 8;
@@ -173,40 +175,172 @@ __device__ __forceinline__ Span span_of(const PrefillArgs& a, int b) {
   return {q0, max(0, q1 - q0), k0, max(0, k1 - k0)};
 }
 
+// N (2, 4 or 8) consecutive values, aligned to their size.
 template <int N>
 __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&x)[N]) {
+  uint32_t w[N / 2];
+  if constexpr (N == 2) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (N == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
+  for (int i = 0; i < N; i += 2) {
+    x[i] = __uint_as_float(w[i / 2] << 16);
+    x[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+  }
 }
 
-// One query row by a warp: query t (of all), head hq, over keys [k0, end).
+// Query rows by a warp, kGroup rows and 32 keys at a time (a lane's own key for the
+// scores, a lane's own columns for the outputs): those of the lanes `todo` (a lane a
+// row: query t, head hq, over keys [k0, end)).  (Groups of four need more registers
+// than kRegsStore.)
+constexpr int kGroup = 2;
 template <int D>
-__device__ __noinline__ void attend_row(const Args& p, int split, int t, int hq, int h, int k0, int end) {
+__device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned todo, int t, int hq, int h,
+                                            int k0, int end, volatile Pulse* pulse) {
+  constexpr int N = D / 32, kBatch = D == 256 ? 4 : 8;
+  const PrefillArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  while (todo) {
+    RowState<D> r[kGroup];
+    const uint16_t* q[kGroup];
+    int64_t row[kGroup];
+    int ends[kGroup], most = k0;
+    int who = 0;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {  // the last row again where there are no more
+      if (todo) who = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int64_t tg = __shfl_sync(~0u, t, who);
+      const int hg = __shfl_sync(~0u, hq, who);
+      q[g] = a.q + tg * a.q_stride + (int64_t)hg * D;
+      row[g] = tg * a.Hq + hg;
+      ends[g] = __shfl_sync(~0u, end, who);
+      most = max(most, ends[g]);
+    }
+#pragma unroll 1
+    for (int j0 = k0; j0 < most; j0 += 32) {
+      float s[kGroup] = {}, w[kGroup];
+      const uint16_t* key = a.k + (int64_t)min(j0 + lane, most - 1) * a.k_stride + (int64_t)h * D;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 8) {
+        float x[8];
+        load_bf16(key + d, x);
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+          float y[8];
+          load_bf16(q[g] + d, y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[g] = fmaf(x[i], y[i], s[g]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g)
+        w[g] = r[g].weigh(j0 + lane < ends[g] ? s[g] * (a.scale * kLog2e) : kNegInf);
+      const uint16_t* value = a.v + (int64_t)j0 * a.v_stride + (int64_t)h * D + lane * N;
+#pragma unroll 1
+      for (int j = 0; j < min(32, most - j0); j += kBatch) {
+        float v[kBatch][N];  // loaded together
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) load_bf16(value + (int64_t)min(j + e, most - 1 - j0) * a.v_stride, v[e]);
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) {
+            const float wj = __shfl_sync(~0u, w[g], j + e);
+            if (j0 + j + e < ends[g]) {  // (0 times a hidden value may be NaN)
+#pragma unroll
+              for (int i = 0; i < N; ++i) r[g].o[i] = fmaf(wj, v[e][i], r[g].o[i]);
+            }
+          }
+      }
+      pulse->beat = j0;
+    }
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      float l = r[g].l;
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+      if (p.splits > 1) {
+        const int64_t at = (int64_t)split * a.Tq * a.Hq + row[g];
+        if (lane == 0) p.ml[at] = make_float2(r[g].m, l);
+#pragma unroll
+        for (int i = 0; i < N; ++i) p.part[at * D + lane * N + i] = r[g].o[i];
+        continue;
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        a.out[row[g] * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(r[g].o[i] * inv));
+    }
+  }
+}
+
+// The rows `again` of a warp (a lane a row: query t, head hq, which sees `sees` of
+// the part's `end` keys from key0 on) whose output is not finite though their sum
+// is.  A value that a row sees and that is not finite leaves its column so, rightly.
+// The row is computed again where a column has none of those, but one among the
+// hidden keys of the tiles (0 times it is NaN), and where no value explains it
+// (P may be 2^8 times a probability, and the sums of large values overflow).
+template <int D>
+__device__ __noinline__ void repair(const Args& p, int split, unsigned again, int t, int hq, int sees, int h,
+                                    int key0, int end, volatile Pulse* pulse) {
   constexpr int N = D / 32;
   const PrefillArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  float q[N];
-  load_bf16(a.q + (int64_t)t * a.q_stride + (int64_t)hq * D + lane * N, q);
-  RowState<D> r;
+  const bool mine = again >> lane & 1;
+  const int least = __reduce_min_sync(~0u, mine ? sees : end), most = __reduce_max_sync(~0u, mine ? sees : 0);
+  const uint16_t* value = a.v + (int64_t)key0 * a.v_stride + (int64_t)h * D + lane * N;
+  // of this lane's columns: the last hidden key and the first seen one that are not finite
+  int last[N], first[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) last[i] = -1, first[i] = end;
+#pragma unroll 4
+  for (int j = least; j < end; ++j) {
+    float v[N];
+    load_bf16(value + (int64_t)j * a.v_stride, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(fabsf(v[i]) < -kNegInf)) last[i] = j;
+  }
 #pragma unroll 1
-  for (int j = k0; j < end; ++j) {
-    float k[N], v[N];
-    load_bf16(a.k + (int64_t)j * a.k_stride + (int64_t)h * D + lane * N, k);
-    load_bf16(a.v + (int64_t)j * a.v_stride + (int64_t)h * D + lane * N, v);
-    r.add(q, k, v, a.scale * kLog2e);
-  }
-  const int64_t row = (int64_t)t * a.Hq + hq;
-  if (p.splits > 1) {
-    const int64_t at = (int64_t)split * a.Tq * a.Hq + row;
-    if (lane == 0) p.ml[at] = make_float2(r.m, r.l);
+  for (int j0 = 0; j0 < most; j0 += 16) {
+#pragma unroll 4
+    for (int j = j0; j < min(j0 + 16, most); ++j) {
+      float v[N];
+      load_bf16(value + (int64_t)j * a.v_stride, v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) p.part[at * D + lane * N + i] = r.o[i];
-    return;
-  }
-  const float inv = r.l == 0.0f ? 0.0f : 1.0f / r.l;
+      for (int i = 0; i < N; ++i)
+        if (!(fabsf(v[i]) < -kNegInf)) first[i] = min(first[i], j);
+    }
+    bool some = false, open = false;  // found one; a column that a hidden key spoils has none yet
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    a.out[row * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(r.o[i] * inv));
+    for (int i = 0; i < N; ++i) {
+      some |= first[i] < end;
+      open |= first[i] == end && last[i] >= 0;
+    }
+    pulse->beat = j0;
+    if (__any_sync(~0u, some) && !__any_sync(~0u, open)) break;
+  }
+  unsigned todo = 0;
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int who = __ffs(again) - 1, n = __shfl_sync(~0u, sees, who);
+    bool known = false, spoiled = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      known |= first[i] < n;
+      spoiled |= first[i] >= n && last[i] >= n;
+    }
+    if (__any_sync(~0u, spoiled) || !__any_sync(~0u, known)) todo |= 1u << who;
+  }
+  attend_rows<D>(p, split, todo, t, hq, h, key0, key0 + sees, pulse);
 }
 
 // ---- tensor core -------------------------------------------------------------------
@@ -339,6 +473,21 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Zeros over the keys from `from` on of a ring unit of values, by a warp, for the
+// tensor core to see.
+template <int D>
+__device__ __noinline__ void clear_values(uint32_t unit, int from) {
+  using C = Cfg<D>;
+#pragma unroll 1
+  for (uint32_t i = from * 128 + (threadIdx.x & 31) * 16; i < C::kVKeys * 128; i += 512)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(unit + c * C::kVKeys * 128 + i), "r"(0)
+                   : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // ---- the order of the work -----------------------------------------------------------
 // Sequences are cut into runs of `run` queries.  The runs that come late in
 // their sequence (under a causal mask those with the most keys) are first: band
@@ -434,12 +583,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   // ring units; of a Q tile: Q there, Q read; of a slot: S written, the first and
   // second half of P written; of a Q tile: O final, O read, a product with V
   // done (not where S's arrival says it), its turn to issue; items there, read; rows'
-  // maxima and sums there, read
+  // maxima and sums there, read; a unit of values with a sequence's end there
   uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing, *q_free = q_full + 2;
   uint64_t *s_full = q_free + 2, *p_full = s_full + 2, *o_full = p_full + 4,
            *o_free = o_full + 2, *pv_done = o_free + 2, *turn = pv_done + 2, *item_full = turn + 2,
            *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 2,
-           *all_done = ml_free + 2;
+           *tail_full = ml_free + 2, *all_done = tail_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile Pulse* pulse = reinterpret_cast<volatile Pulse*>(smem + C::kOffMisc + 8);
 
@@ -474,6 +623,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(ml_full + i, 4);
       mbar_init(ml_free + i, 4);
     }
+    mbar_init(tail_full, 1);
     mbar_init(all_done, kTiles);
     pulse->abort = pulse->beat = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -573,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else if (warp == kLoad) {
     // ---- loads: K and V tiles through the ring in the order of their use:
     // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
-    int u = 0;  // units issued
+    int u = 0, tails = 0;  // units issued; those with an end of a sequence
     Item it;
     while (read_item(it, false)) {
       const int most = max(it.n[0], it.n[1]), key0 = it.k0 + it.lo * kKeys;
@@ -587,21 +737,37 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           const int st = u % C::kRing, round = u / C::kRing, y = key0 + j * kKeys;
           if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, pulse));
           if (!ok) break;
-          if (elected()) {  // boxes of 64 columns: K by columns, V by keys
-            const uint32_t to = ring + st * C::kUnit;
+          const uint32_t to = ring + st * C::kUnit;
+          // keys of the sequence from this unit of values on
+          const int left = v ? it.k0 + it.nk - y - k * C::kVKeys : C::kVKeys;
+          const bool tail = left < C::kVKeys;
+          uint64_t* const bar = tail ? tail_full : full + st;
+          if (left > 0 && elected()) {  // boxes of 64 columns: K by columns, V by keys
             pulse->beat = u;
-            mbar_expect_tx(full + st, C::kUnit);
+            mbar_expect_tx(bar, C::kUnit);
             if (v) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_3d(to + c * C::kVKeys * 128, &map_v, 64 * c, it.h, y + k * C::kVKeys, full + st);
+                tma_3d(to + c * C::kVKeys * 128, &map_v, 64 * c, it.h, y + k * C::kVKeys, bar);
             } else {
 #pragma unroll
               for (int c = 0; c < C::kCols / 64; ++c)
-                tma_3d(to + c * kKeys * 128, &map_k, k * C::kCols + 64 * c, it.h, y, full + st);
+                tma_3d(to + c * kKeys * 128, &map_k, k * C::kCols + 64 * c, it.h, y, bar);
             }
           }
           __syncwarp();
+          if (__builtin_expect(tail, 0)) {
+            // The values past the sequence's end, of another one, are cleared before the
+            // unit is handed over.
+            if (left > 0) {
+              ok = __all_sync(~0u, bar_wait(tail_full, tails & 1, pulse));
+              if (!ok) static_cast<void>(mbar_wait(tail_full, tails & 1, nullptr));  // the copy lands
+              if (!ok) break;
+              ++tails;
+            }
+            clear_values<D>(to, max(0, left));
+            if (lane == 0) mbar_arrive(full + st);
+          }
         }
       }
       if (!ok) break;
@@ -974,15 +1140,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         // rows whose sum is finite and whose output is not
         float lo, hi;
         unpair(checked, lo, hi);
-        unsigned again = __ballot_sync(~0u, mine && !(lo + hi == 0.0f) && l == l);
-        while (again) {
-          const int who = __ffs(again) - 1;
-          again &= again - 1;
+        const unsigned again = __ballot_sync(~0u, mine && !(lo + hi == 0.0f) && l == l);
+        if (again) {
+          const int key0 = it.lo * kKeys, end = min(tiles * kKeys, it.nk - key0);
+          const int sees = (a.causal ? min(it.nk, it.nk - it.nq + tok + 1) : it.nk) - key0;
           __syncwarp();
-          const int sees = (a.causal ? min(it.nk, it.nk - it.nq + tok + 1) : it.nk) - it.lo * kKeys;
-          const int key0 = it.k0 + it.lo * kKeys;
-          attend_row<D>(p, it.split, it.q0 + __shfl_sync(~0u, tok, who), __shfl_sync(~0u, hq, who), it.h,
-                        key0, key0 + __shfl_sync(~0u, min(sees, tiles * kKeys), who));
+          repair<D>(p, it.split, again, it.q0 + tok, hq, min(sees, end), it.h, it.k0 + key0, end, pulse);
         }
       }
       if (!ok) break;

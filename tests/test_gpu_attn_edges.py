@@ -235,3 +235,142 @@ def test_planning_grows_with_the_batch_alone(P):
     torch.cuda.synchronize()
     assert a.elapsed_time(b) < 60
     print(f"{a.elapsed_time(b):.2f} ms")
+
+
+# ---- prompts: values that are not finite -----------------------------------------------
+
+def _timed(call):
+    import torch
+
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    call()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+class Long:
+    """Random queries, keys and values of some prompts, their clean outputs, and the
+    outputs and time with other values."""
+
+    def __init__(self, P, seed, nqs, nks, Hkv, G, D, causal=True):
+        import torch
+
+        torch.manual_seed(seed)
+        self.P, self.D, self.G, self.causal = P, D, G, causal
+        self.q, self.k, self.v = (torch.randn(n, h, D, device="cuda").bfloat16()
+                                  for n, h in ((sum(nqs), Hkv * G), (sum(nks), Hkv), (sum(nks), Hkv)))
+        self.cu = [torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
+                   for n in (nqs, nks)]
+        self.run(self.v)
+        self.clean, self.lse, self.ms = self.run(self.v)
+
+    def run(self, v):
+        import torch
+
+        out, lse = torch.empty_like(self.q), torch.empty(self.q.shape[:2], device="cuda")
+        ms = _timed(lambda: self.P.attn_prefill(self.q, self.k, v, *self.cu, causal=self.causal, out=out, lse=lse))
+        self.P.device_check()
+        return out, lse, ms
+
+    def check_row(self, out, lse, i, hq, v, keys):
+        """Query i of all, head hq, over `keys`."""
+        h = hq // self.G
+        ref = R.attend(_host(self.q[i, hq])[None], _host(self.k[keys, h]), _host(v[keys, h]), self.D ** -0.5)
+        R.check(_host(out[i, hq])[None], _host(lse[i, hq])[None], ref, True, True, f"query {i} head {hq}")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("D,Hkv,G", [(128, 2, 5), (64, 2, 4), (256, 1, 6)])
+def test_a_value_seen_by_all_spoils_its_column_alone(P, D, Hkv, G, bad):
+    """The first token's value not finite: the long prompt's rows are as without it
+    but for one column, and none is computed again one by one (which took
+    hundreds of times the prompt's own time)."""
+    import torch
+
+    s = Long(P, D, [8192], [8192], Hkv, G, D)
+    v = s.v.clone()
+    v[0, 0, 7] = bad
+    out, lse, ms = s.run(v)
+    assert torch.equal(lse, s.lse)
+    assert (torch.isnan(out[:, :G, 7]) if bad != bad else torch.isposinf(out[:, :G, 7])).all()
+    out[:, :G, 7] = s.clean[:, :G, 7]
+    assert torch.equal(out, s.clean)
+    assert ms < 5 * s.ms + 0.5, (ms, s.ms)
+
+
+@pytest.mark.parametrize("where", [8191, 8000, 4100])
+@pytest.mark.parametrize("D,Hkv,G", [(128, 2, 5), (64, 2, 4), (256, 1, 6)])
+def test_a_hidden_value_reaches_no_row(P, D, Hkv, G, where):
+    """Rows before the token are as without it, to the last bit or (those whose tile
+    it spoils) to the definition; the time stays near the prompt's."""
+    import torch
+
+    s = Long(P, D, [8192], [8192], Hkv, G, D)
+    v = s.v.clone()
+    v[where, 0] = float("nan")
+    out, lse, ms = s.run(v)
+    assert torch.equal(lse, s.lse) and torch.equal(out[:, G:], s.clean[:, G:])
+    assert torch.isnan(out[where:, :G]).all()
+    moved = (out[:where, :G] != s.clean[:where, :G]).any(-1).nonzero().cpu().numpy()
+    print(f"{len(moved)} rows differ, {ms:.2f} ms for {s.ms:.2f}")
+    assert len(moved) == 0 or moved[:, 0].min() >= where - 512
+    for i, hq in moved[:: max(1, len(moved) // 40)]:
+        s.check_row(out, lse, i, hq, v, slice(0, i + 1))
+    assert ms < 60
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,Hkv,G", [(128, 2, 5), (64, 2, 4), (256, 1, 6)])
+def test_the_next_prompts_values_reach_no_row(P, D, Hkv, G, causal):
+    """A prompt of NaN values after one whose last tile they share."""
+    import torch
+
+    for n in (4001, 4032, 4095):
+        s = Long(P, D, [n, 300], [n, 300], Hkv, G, D, causal)
+        v = s.v.clone()
+        v[n:] = float("nan")
+        out, lse, ms = s.run(v)
+        assert torch.equal(out[:n], s.clean[:n]) and torch.equal(lse, s.lse)
+        assert torch.isnan(out[n:]).all()
+        assert ms < 3 * s.ms + 0.5, (ms, s.ms)
+
+
+@pytest.mark.parametrize("D,G,nq,nk", [(128, 5, 40, 9000), (64, 1, 70, 12345), (256, 6, 9, 5000)])
+def test_non_finite_values_where_the_keys_are_cut_into_parts(P, D, G, nq, nk):
+    import torch
+
+    assert P.attn_prefill_workspace_bytes(1, nq, nk, G, 1, D, P.PTQ_BF16) > 0
+    s = Long(P, D, [nq], [nk], 1, G, D)
+    v = s.v.clone()
+    v[nk - 2, 0, 3] = float("nan")          # hidden from all but two queries
+    v[100, 0, 5] = float("inf")             # seen by all
+    out, lse, ms = s.run(v)
+    assert torch.equal(lse[nq - 2:], s.lse[nq - 2:]) and torch.isposinf(out[..., 5]).all()
+    assert torch.isnan(out[nq - 2:, :, 3]).all()
+    keep = [d for d in range(D) if d != 5]
+    assert torch.isfinite(out[:nq - 2, :, keep]).all()
+    out[..., 5], v[100, 0, 5] = s.clean[..., 5], s.v[100, 0, 5]
+    for i in range(0, nq - 2, max(1, nq // 5)):
+        for hq in range(G):
+            s.check_row(out, lse, i, hq, v, slice(0, i + nk - nq + 1))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_values_under_a_maximum_that_grows_a_little(P, D):
+    """Weights may be 2^8 times the largest key's while they are summed, and the sums
+    of values near 1e36 then overflow (147 x 132 x 1e36); relative to the largest key
+    (132 x 1e36) they do not."""
+    import torch
+
+    n, nq = 260, 5
+    q = torch.zeros(nq, 1, D, device="cuda", dtype=torch.bfloat16)
+    k = torch.zeros(n, 1, D, device="cuda", dtype=torch.bfloat16)
+    q[:, 0, 0], k[128:, 0, 0] = 1.0, 5.0     # scores of 0, then of 5 (7.2 in units of log2)
+    v = (torch.rand(n, 1, D, device="cuda") + 0.5).mul(1e36).bfloat16()
+    cu_q, cu_k = (torch.tensor([0, m], dtype=torch.int32, device="cuda") for m in (nq, n))
+    out = P.attn_prefill(q, k, v, cu_q, cu_k, scale=1.0)
+    for i in range(nq):
+        ref = R.attend(_host(q[i]), _host(k[:n - nq + i + 1, 0]), _host(v[:n - nq + i + 1, 0]), 1.0)
+        R.check(_host(out[i]), None, ref, True, True)
