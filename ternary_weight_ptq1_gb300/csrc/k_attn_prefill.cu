@@ -112,6 +112,7 @@ struct Args {
   int heads;       // head blocks in all
   Divider by_per, by_heads, by_G, by_hg;  // by_per: head blocks times parts
   Divider by_run;  // queries of an item: the Q tiles' tokens
+  int ways;        // through the sequences, that the planning warp may go
   int splits;      // parts the keys of each item are cut into
   float* part;     // splits > 1: [splits][Tq Hq][D] output sums, and the (maximum,
   float2* ml;      // sum) they refer to, [splits][Tq Hq]
@@ -521,9 +522,10 @@ __device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pul
     pulse->beat = b;
   }
   most = (int)__reduce_max_sync(~0u, most);
-  // most / band ways of B / 32 steps
-  const int ways = max(1, kSteps / (((int)p.a.B + 31) / 32)), band = (most + ways - 1) / ways;
-  return {most > 0 ? (most - 1) / band * band : -1, band, 0, 0};
+  // most / band ways through the sequences (no division where a band is a level)
+  if (most <= p.ways) return {most - 1, 1, 0, 0};
+  const int band = (most + p.ways - 1) / p.ways;
+  return {(most - 1) / band * band, band, 0, 0};
 }
 
 // The sequence and level of run i in that order; false: there are not so many.
@@ -536,11 +538,15 @@ __device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq,
 #pragma unroll 1
     for (; w.b0 < (int)p.a.B; w.b0 += 32) {
       const int mine = min(max(runs_of(p, w.b0 + lane) - w.base, 0), w.band);
-      int end = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(~0u, end, d);
-        if (lane >= d) end += o;
+      int end = mine;  // the sum up to this lane
+      if (w.band == 1) {
+        end = __popc(__ballot_sync(~0u, mine) & (~0u >> (31 - lane)));
+      } else {
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(~0u, end, d);
+          if (lane >= d) end += o;
+        }
       }
       const int in = i - w.before;
       const unsigned at = __ballot_sync(~0u, in < end);
@@ -1268,7 +1274,7 @@ cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int G = (int)(a.Hq / a.Hkv);
   Args p{a, G, 0, 0, 0, Divider(plan.heads * plan.splits), Divider(plan.heads), Divider(G), Divider(plan.hg),
-         Divider(C::kTiles * plan.tpt), 0, nullptr, nullptr};
+         Divider(C::kTiles * plan.tpt), 1, 0, nullptr, nullptr};
   p.hg = plan.hg;
   p.tpt = plan.tpt;
   p.splits = plan.splits;
@@ -1289,6 +1295,8 @@ cudaError_t launch(const PrefillArgs& a, void* ws, cudaStream_t st) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   p.heads = (int)plan.heads;
+  const int64_t steps = (a.B + 31) / 32;  // of one way
+  p.ways = steps < kSteps ? (int)(kSteps / steps) : 1;
   e = launch_pdl(kern, dim3((unsigned)(work < kSms ? work : kSms)), dim3(C::kThreads), C::kSmem, st,
                  mq, mk, mv, p, status);
   if (e != cudaSuccess || plan.splits == 1) return e;
