@@ -611,11 +611,12 @@ def kv_write(cache, k, v, slots, stream=None):
 
 def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     """The values that the int32 `slots` of the cache stand for, as (k, v) of
-    float32 or bfloat16 (default); into the given k and v (as for kv_write)
-    or new tensors.  A slot outside the cache gives NaN."""
+    float32 or bfloat16 (default, where neither k nor v is given); into the
+    given k and v (as for kv_write) or new tensors.  A slot outside the cache gives NaN."""
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
     if dtype is None:
-        dtype = k.dtype if k is not None else cache._bfloat16
+        given = v if k is None else k
+        dtype = cache._bfloat16 if given is None else given.dtype
     sp = _dev(slots, cache._int32, "slots")
     if k is None:
         k = _new(slots, shape, dtype, stream)

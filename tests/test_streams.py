@@ -131,3 +131,23 @@ def test_without_a_stream_they_belong_to_the_current_one(world, name):
     call()
     made = [t for t in world.made[n:] if t.stream != "made by the caller"]
     assert made and all(t.stream is world.main and not t.used for t in made)
+
+
+# ---- kv_read's results -------------------------------------------------------------
+
+def _cache(w, dtype=None):
+    import torch
+
+    dtype = dtype or torch.bfloat16
+    k, v = (w.new((3, 2, 4, 64), dtype) for _ in range(2))
+    scales = [w.new((3, 2, 4), torch.float32) for _ in range(2)] if dtype == torch.int8 else []
+    return w.P.KVCache(k, v, *scales)
+
+
+@pytest.mark.parametrize("given", ["k", "v"])
+def test_the_result_beside_a_given_one_is_of_its_type(world, given):
+    import torch
+
+    ids, mine = world.new((4,), torch.int32), world.new((4, 2, 64), torch.float32)
+    k, v = world.P.kv_read(_cache(world), ids, **{given: mine})
+    assert (k if given == "k" else v) is mine and k.dtype == v.dtype == torch.float32
