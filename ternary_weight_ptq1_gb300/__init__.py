@@ -536,7 +536,7 @@ class KVCache:
     """A paged key-value cache over the caller's tensors: k and v are pages x
     kv_heads x page_tokens x head_dim, bfloat16, or int8 with k_scale and
     v_scale (pages x kv_heads x page_tokens float32).  Keeps the tensors alive;
-    copies nothing."""
+    copies nothing, and hands their addresses to the library: none is replaced."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
@@ -562,6 +562,11 @@ class KVCache:
         self._struct = _KvCacheStruct(_dev(k, None, "k"), _dev(v, None, "v"), *scales, self.pages,
                                       self.page_tokens, self.kv_heads, self.head_dim, self.type)
         self._ref = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name} of a KVCache is not replaced: make a new one")
+        self.__dict__[name] = value
 
     @classmethod
     def empty(cls, pages, kv_heads, page_tokens, head_dim, dtype, device="cuda"):

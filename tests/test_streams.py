@@ -151,3 +151,17 @@ def test_the_result_beside_a_given_one_is_of_its_type(world, given):
     ids, mine = world.new((4,), torch.int32), world.new((4, 2, 64), torch.float32)
     k, v = world.P.kv_read(_cache(world), ids, **{given: mine})
     assert (k if given == "k" else v) is mine and k.dtype == v.dtype == torch.float32
+
+
+# ---- the cache object ----------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "pages", "page_tokens", "kv_heads", "head_dim"])
+def test_a_caches_tensors_are_not_replaced(world, name):
+    """The library has their addresses: another tensor would be ignored."""
+    import torch
+
+    cache = _cache(world, torch.int8)
+    was = getattr(cache, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(cache, name, was)
+    assert getattr(cache, name) is was
