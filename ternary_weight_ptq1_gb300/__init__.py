@@ -178,8 +178,23 @@ def _new(like, shape, dtype, stream, returned=True):
     return t
 
 
-def _dev(t, dtype=None, name="tensor"):
-    if not getattr(t, "is_cuda", False):
+def _device_of(t, name, on=None):
+    """The index of t's CUDA device, which is `on` where that is given."""
+    try:
+        d = t.get_device()
+    except AttributeError:
+        d = -1
+    if d < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if on is not None and d != on >= 0:
+        raise ValueError(f"{name} is on another device: cuda:{d}, not cuda:{on}")
+    return d
+
+
+def _dev(t, dtype=None, name="tensor", on=None):
+    if on is not None:
+        _device_of(t, name, on)
+    elif not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -543,12 +558,13 @@ class KVCache:
 
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v must be pages x kv_heads x page_tokens x head_dim, of one type")
+        on = k.get_device()
         if k.dtype == torch.int8:
             for s in (k_scale, v_scale):
                 if s is None or s.shape != k.shape[:3]:
                     raise ValueError("an int8 cache needs k_scale and v_scale, one scale for each row")
             self.type = PTQ_KV_I8
-            scales = (_dev(k_scale, torch.float32, "k_scale"), _dev(v_scale, torch.float32, "v_scale"))
+            scales = (_dev(k_scale, torch.float32, "k_scale", on), _dev(v_scale, torch.float32, "v_scale", on))
         elif k.dtype == torch.bfloat16:
             if k_scale is not None or v_scale is not None:
                 raise ValueError("a bfloat16 cache takes no scales")
@@ -556,10 +572,11 @@ class KVCache:
             scales = (None, None)
         else:
             raise TypeError(f"a cache is bfloat16 or int8, got {k.dtype}")
+        self._on = on
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self._int32, self._bfloat16 = torch.int32, torch.bfloat16
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
-        self._struct = _KvCacheStruct(_dev(k, None, "k"), _dev(v, None, "v"), *scales, self.pages,
+        self._struct = _KvCacheStruct(_dev(k, None, "k", on), _dev(v, None, "v", on), *scales, self.pages,
                                       self.page_tokens, self.kv_heads, self.head_dim, self.type)
         self._ref = ctypes.addressof(self._struct)
 
@@ -581,11 +598,10 @@ class KVCache:
                            for _ in range(2)))
 
 
-def _heads(t, name, dtype, shape=None):
+def _heads(t, name, dtype, on, shape=None):
     """The address and token stride of a tokens x heads x head_dim tensor whose
     heads are contiguous within a token (tokens may be any stride apart)."""
-    if not getattr(t, "is_cuda", False):
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _device_of(t, name, on)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     s = t.shape
@@ -608,10 +624,11 @@ def kv_write(cache, k, v, slots, stream=None):
     cache skips its token."""
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
     dtype = k.dtype
-    kp, ks = _heads(k, "k", dtype, shape)
-    vp, vs = _heads(v, "v", dtype, shape)
-    _check(load().ptq_kv_write(cache._ref, kp, vp, ks, vs, _dev(slots, cache._int32, "slots"), shape[0],
-                               _act_dtype(k), _stream(stream, k.get_device())), "ptq_kv_write")
+    on = cache._on
+    kp, ks = _heads(k, "k", dtype, on, shape)
+    vp, vs = _heads(v, "v", dtype, on, shape)
+    _check(load().ptq_kv_write(cache._ref, kp, vp, ks, vs, _dev(slots, cache._int32, "slots", on), shape[0],
+                               _act_dtype(k), _stream(stream, on)), "ptq_kv_write")
 
 
 def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
@@ -622,15 +639,16 @@ def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     if dtype is None:
         given = v if k is None else k
         dtype = cache._bfloat16 if given is None else given.dtype
-    sp = _dev(slots, cache._int32, "slots")
+    on = cache._on
+    sp = _dev(slots, cache._int32, "slots", on)
     if k is None:
         k = _new(slots, shape, dtype, stream)
     if v is None:
         v = _new(slots, shape, dtype, stream)
-    kp, ks = _heads(k, "k", dtype, shape)
-    vp, vs = _heads(v, "v", dtype, shape)
+    kp, ks = _heads(k, "k", dtype, on, shape)
+    vp, vs = _heads(v, "v", dtype, on, shape)
     _check(load().ptq_kv_read(cache._ref, sp, shape[0], kp, vp, ks, vs, _act_dtype(k),
-                              _stream(stream, k.get_device())), "ptq_kv_read")
+                              _stream(stream, on)), "ptq_kv_read")
     return k, v
 
 
@@ -638,13 +656,13 @@ def attn_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: i
     return int(load().ptq_attn_decode_workspace_bytes(B, q_heads, kv_heads, head_dim, dtype))
 
 
-def _attn_buffers(q, out, lse, workspace, need, stream):
+def _attn_buffers(q, out, lse, workspace, need, stream, on):
     """The output, the addresses of out and lse, the workspace, its address and size."""
     if out is None:
         out = _new(q, q.shape, q.dtype, stream)
     elif out.shape != q.shape:
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-    op = _dev(out, q.dtype, "out")
+    op = _dev(out, q.dtype, "out", on)
     lp = wp = None
     wb = 0
     if lse is not None:
@@ -652,13 +670,13 @@ def _attn_buffers(q, out, lse, workspace, need, stream):
 
         if lse.shape != q.shape[:2]:
             raise ValueError(f"lse must be {tuple(q.shape[:2])}, got {tuple(lse.shape)}")
-        lp = _dev(lse, torch.float32, "lse")
+        lp = _dev(lse, torch.float32, "lse", on)
     if workspace is None and (wb := need()) > 0:
         import torch
 
         workspace = _new(q, wb, torch.uint8, stream, returned=False)
     if workspace is not None:
-        wp, wb = _dev(workspace, None, "workspace"), workspace.nbytes
+        wp, wb = _dev(workspace, None, "workspace", on), workspace.nbytes
     return out, op, lp, wp, wb, workspace
 
 
@@ -670,7 +688,8 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
     the log-sum-exp of the scaled scores.  out and the workspace are allocated
     by PyTorch when not given."""
     dt = _act_dtype(q)
-    qp, qs = _heads(q, "q", q.dtype)
+    on = cache._on
+    qp, qs = _heads(q, "q", q.dtype, on)
     B, Hq, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q has head_dim {D}, the cache {cache.head_dim}")
@@ -678,11 +697,11 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
     if len(ts) != 2 or ts[0] != B or lens.shape != (B,):
         raise ValueError("table must be sequences x pages, lens one count for each sequence")
     out, op, lp, wp, wb, keep = _attn_buffers(
-        q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt), stream)
-    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, int32, "table"), ts[1],
-                                  _dev(lens, int32, "lens"), op, lp, B, Hq,
+        q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt), stream, on)
+    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, int32, "table", on), ts[1],
+                                  _dev(lens, int32, "lens", on), op, lp, B, Hq,
                                   D ** -0.5 if scale is None else scale, dt, wp, wb,
-                                  _stream(stream, q.get_device())), "ptq_attn_decode")
+                                  _stream(stream, on)), "ptq_attn_decode")
     return out
 
 
@@ -701,9 +720,10 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     import torch
 
     dt, dtype, shape = _act_dtype(q), q.dtype, k.shape
-    qp, qs = _heads(q, "q", dtype)
-    kp, ks = _heads(k, "k", dtype)
-    vp, vs = _heads(v, "v", dtype, shape)
+    on = _device_of(q, "q")
+    qp, qs = _heads(q, "q", dtype, on)
+    kp, ks = _heads(k, "k", dtype, on)
+    vp, vs = _heads(v, "v", dtype, on, shape)
     Tq, Hq, D = q.shape
     Tk, Hkv, Dk = shape
     if Dk != D:
@@ -713,12 +733,12 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
         raise ValueError("cu_q and cu_k must have one offset more than there are sequences")
     out, op, lp, wp, wb, keep = _attn_buffers(
         q, out, lse, workspace, lambda: attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dt),
-        stream)
-    _check(load().ptq_attn_prefill(qp, kp, vp, qs, ks, vs, _dev(cu_q, torch.int32, "cu_q"),
-                                   _dev(cu_k, torch.int32, "cu_k"), op, lp, B, Tq, Tk, Hq, Hkv, D,
+        stream, on)
+    _check(load().ptq_attn_prefill(qp, kp, vp, qs, ks, vs, _dev(cu_q, torch.int32, "cu_q", on),
+                                   _dev(cu_k, torch.int32, "cu_k", on), op, lp, B, Tq, Tk, Hq, Hkv, D,
                                    D ** -0.5 if scale is None else scale,
                                    PTQ_ATTN_CAUSAL if causal else 0, dt, wp, wb,
-                                   _stream(stream, q.get_device())), "ptq_attn_prefill")
+                                   _stream(stream, on)), "ptq_attn_prefill")
     return out
 
 

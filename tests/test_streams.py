@@ -1,5 +1,6 @@
-"""Buffers that a call allocates for itself belong to the stream it is queued
-on.  On the host: a stand-in for a CUDA tensor notes the stream it was
+"""The binding's own work on the host: the buffers that a call allocates belong
+to the stream it is queued on, a cache's tensors stay, the tensors of a call
+are on one device.  A stand-in for a CUDA tensor notes the stream it was
 allocated on, and a stand-in library takes the call."""
 import contextlib
 import types
@@ -20,7 +21,8 @@ class _Tensor:
     device = "cuda:0"
     data_ptr = lambda self: 4096 * (1 + self.world.made.index(self))
     is_contiguous = lambda self: True
-    get_device = lambda self: 0
+    index = 0
+    get_device = lambda self: self.index
     numel = lambda self: self.shape.numel()
     element_size = lambda self: self.dtype.itemsize
     nbytes = property(lambda self: self.numel() * self.element_size())
@@ -84,7 +86,7 @@ def _calls(w):
     f32, bf16, i8, i16, i32, u8 = (torch.float32, torch.bfloat16, torch.int8, torch.int16, torch.int32, torch.uint8)
     x, wq, sc, sg = new((4, 1024), f32), new((256, 208), u8), new((256, 8), i16), new((1024,), i8)
     ids = new((4,), i32)
-    cache = types.SimpleNamespace(kv_heads=2, head_dim=64, _int32=i32, _bfloat16=bf16, _ref=64, k=new((1, 2, 4, 64), i8))
+    cache = types.SimpleNamespace(kv_heads=2, head_dim=64, _int32=i32, _bfloat16=bf16, _ref=64, _on=0, k=new((1, 2, 4, 64), i8))
     q, k, cu = new((4, 4, 64), bf16), new((4, 2, 64), bf16), new((2,), i32)
     block = (new((2048, 208), u8), sc, wq, sc, sg, sg)
     return {
@@ -165,3 +167,46 @@ def test_a_caches_tensors_are_not_replaced(world, name):
     with pytest.raises(AttributeError, match=name):
         setattr(cache, name, was)
     assert getattr(cache, name) is was
+
+
+# ---- devices -------------------------------------------------------------------------
+
+def _attention(w):
+    """The attention calls by name, and the tensors of each."""
+    import torch
+
+    P, new = w.P, w.new
+    f32, bf16, i8, i32, u8 = torch.float32, torch.bfloat16, torch.int8, torch.int32, torch.uint8
+    cache = _cache(w)
+    t = dict(k=new((4, 2, 64), bf16), v=new((4, 2, 64), bf16), slots=new((4,), i32), q=new((4, 4, 64), bf16),
+             out=new((4, 4, 64), bf16), lse=new((4, 4), f32), workspace=new((1 << 20,), u8), table=new((4, 3), i32),
+             lens=new((4,), i32), cu_q=new((3,), i32), cu_k=new((3,), i32))
+    some = lambda *names: {n: t[n] for n in names}  # noqa: E731
+    rest = some("out", "lse", "workspace")
+    pools = {n: new((3, 2, 4, 64) if n in "kv" else (3, 2, 4), i8 if n in "kv" else f32)
+             for n in ("k", "v", "k_scale", "v_scale")}
+    return {
+        "KVCache": (lambda: P.KVCache(**pools), pools),
+        "kv_write": (lambda: P.kv_write(cache, t["k"], t["v"], t["slots"]), some("k", "v", "slots")),
+        "kv_read": (lambda: P.kv_read(cache, t["slots"], k=t["k"], v=t["v"]), some("k", "v", "slots")),
+        "attn_decode": (lambda: P.attn_decode(t["q"], cache, t["table"], t["lens"], **rest),
+                        some("q", "table", "lens", "out", "lse", "workspace")),
+        "attn_prefill": (lambda: P.attn_prefill(t["q"], t["k"], t["v"], t["cu_q"], t["cu_k"], **rest),
+                         some("q", "k", "v", "cu_q", "cu_k", "out", "lse", "workspace")),
+    }
+
+
+@pytest.mark.parametrize("name", ["KVCache", "kv_write", "kv_read", "attn_decode", "attn_prefill"])
+def test_tensors_of_one_call_are_on_one_device(world, name):
+    call, tensors = _attention(world)[name]
+    call()
+    done = len(world.calls)
+    for n, t in tensors.items():
+        t.index = 1
+        with pytest.raises(ValueError, match="device"):
+            call()
+        t.index = -1                        # the host
+        with pytest.raises(TypeError, match="CUDA"):
+            call()
+        t.index = 0
+    assert len(world.calls) == done
