@@ -178,24 +178,24 @@ def _new(like, shape, dtype, stream, returned=True):
     return t
 
 
-def _device_of(t, name, on=None):
-    """The index of t's CUDA device, which is `on` where that is given."""
-    try:
-        d = t.get_device()
-    except AttributeError:
-        d = -1
+def _nowhere():
+    return -1
+
+
+def _misplaced(t, name, on):
+    """Refuses a tensor that is not on the CUDA device of index `on`."""
+    d = getattr(t, "get_device", _nowhere)()
     if d < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if on is not None and d != on >= 0:
-        raise ValueError(f"{name} is on another device: cuda:{d}, not cuda:{on}")
-    return d
+    raise ValueError(f"{name} is on another device: cuda:{d}, not cuda:{on}")
 
 
 def _dev(t, dtype=None, name="tensor", on=None):
-    if on is not None:
-        _device_of(t, name, on)
-    elif not getattr(t, "is_cuda", False):
-        raise TypeError(f"{name} must be a CUDA tensor")
+    if on is None:
+        if not getattr(t, "is_cuda", False):
+            raise TypeError(f"{name} must be a CUDA tensor")
+    elif getattr(t, "get_device", _nowhere)() != on:
+        _misplaced(t, name, on)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
@@ -558,7 +558,7 @@ class KVCache:
 
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v must be pages x kv_heads x page_tokens x head_dim, of one type")
-        on = k.get_device()
+        on = k.get_device() if k.is_cuda else None
         if k.dtype == torch.int8:
             for s in (k_scale, v_scale):
                 if s is None or s.shape != k.shape[:3]:
@@ -601,7 +601,8 @@ class KVCache:
 def _heads(t, name, dtype, on, shape=None):
     """The address and token stride of a tokens x heads x head_dim tensor whose
     heads are contiguous within a token (tokens may be any stride apart)."""
-    _device_of(t, name, on)
+    if getattr(t, "get_device", _nowhere)() != on:
+        _misplaced(t, name, on)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     s = t.shape
@@ -720,7 +721,7 @@ def attn_prefill(q, k, v, cu_q, cu_k, causal=True, scale=None, out=None, lse=Non
     import torch
 
     dt, dtype, shape = _act_dtype(q), q.dtype, k.shape
-    on = _device_of(q, "q")
+    on = q.get_device() if getattr(q, "is_cuda", False) else _misplaced(q, "q", 0)
     qp, qs = _heads(q, "q", dtype, on)
     kp, ks = _heads(k, "k", dtype, on)
     vp, vs = _heads(v, "v", dtype, on, shape)

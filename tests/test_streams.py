@@ -9,7 +9,7 @@ import pytest
 
 
 class _Tensor:
-    is_cuda = True
+    is_cuda = property(lambda self: self.index >= 0)
 
     def __init__(self, world, shape, dtype, stream="made by the caller"):
         import torch
@@ -210,3 +210,18 @@ def test_tensors_of_one_call_are_on_one_device(world, name):
             call()
         t.index = 0
     assert len(world.calls) == done
+
+
+def test_an_array_is_no_tensor(world):
+    import numpy as np
+    import torch
+
+    P, new = world.P, world.new
+    q, lens, cache = new((4, 4, 64), torch.bfloat16), new((4,), torch.int32), _cache(world)
+    with pytest.raises(TypeError, match="table must be a CUDA tensor"):
+        P.attn_decode(q, cache, np.zeros((4, 3), np.int32), lens)
+    with pytest.raises(TypeError, match="cu_q must be a CUDA tensor"):
+        k = new((4, 2, 64), torch.bfloat16)
+        cu = types.SimpleNamespace(numel=lambda: 3, shape=(3,))
+        P.attn_prefill(q, k, k, cu, cu)
+    assert not world.calls
