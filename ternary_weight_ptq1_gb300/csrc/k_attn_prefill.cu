@@ -503,6 +503,8 @@ struct Walk {
   int band;      // its levels
   int b0;        // the next 32 sequences
   int before;    // runs before them
+  int all;       // runs in all
+  int first;     // of this lane's sequence among the first 32
 };
 
 // The runs of sequence b.
@@ -515,17 +517,21 @@ __device__ __forceinline__ int runs_of(const Args& p, int b) {
 }
 
 __device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pulse) {
-  int most = 0;
+  const int lane = threadIdx.x & 31, first = runs_of(p, lane);
+  int most = first, all = first;
 #pragma unroll 1
-  for (int b = threadIdx.x & 31; b < (int)p.a.B; b += 32) {
-    most = max(most, runs_of(p, b));
+  for (int b = 32 + lane; b < (int)p.a.B; b += 32) {
+    const int n = runs_of(p, b);
+    most = max(most, n);
+    all += n;
     pulse->beat = b;
   }
   most = (int)__reduce_max_sync(~0u, most);
+  all = (int)__reduce_add_sync(~0u, all);
   // most / band ways through the sequences (no division where a band is a level)
-  if (most <= p.ways) return {most - 1, 1, 0, 0};
+  if (most <= p.ways) return {most - 1, 1, 0, 0, all, first};
   const int band = (most + p.ways - 1) / p.ways;
-  return {(most - 1) / band * band, band, 0, 0};
+  return {(most - 1) / band * band, band, 0, 0, all, first};
 }
 
 // The sequence and level of run i in that order; false: there are not so many.
@@ -533,11 +539,12 @@ __device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pul
 __device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq, int* level,
                                         volatile Pulse* pulse) {
   const int lane = threadIdx.x & 31;
+  if (i >= w.all) return false;
 #pragma unroll 1
   for (; w.base >= 0; w.base -= w.band, w.b0 = 0) {
 #pragma unroll 1
     for (; w.b0 < (int)p.a.B; w.b0 += 32) {
-      const int mine = min(max(runs_of(p, w.b0 + lane) - w.base, 0), w.band);
+      const int mine = min(max((w.b0 ? runs_of(p, w.b0 + lane) : w.first) - w.base, 0), w.band);
       int end = mine;  // the sum up to this lane
       if (w.band == 1) {
         end = __popc(__ballot_sync(~0u, mine) & (~0u >> (31 - lane)));
