@@ -539,9 +539,8 @@ PTQ_API size_t ptq_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t T
  * no effect on it, NaN and infinities included.
  * dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED (the fp32
  * route serves decode).  Probabilities enter the second product as bf16.
- * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; B, Tq and Tk
- * are under 2^30.  workspace
- * as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
+ * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; Tq and Tk are
+ * under 2^30, B under 2^26.  workspace as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
  * Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for unknown flags. */
 #define PTQ_ATTN_CAUSAL 1u
 PTQ_API PTQ_NODISCARD ptq_status ptq_attn_prefill(

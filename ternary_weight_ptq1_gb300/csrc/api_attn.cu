@@ -88,9 +88,13 @@ bool decode_shape_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
          t <= INT32_MAX && mul_ok(t, D, &t) && mul_ok(t, 4, &t);
 }
 
+// Every CTA reads the sequences' offsets twice, 32 at a time: 2^26 of them take less
+// than a second, well under the limit of the waits for what comes of it.
+constexpr int64_t kMostPrompts = (int64_t)1 << 26;
+
 bool prefill_shape_ok(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
   int64_t t;
-  return B >= 0 && B <= INT32_MAX / 2 && Tq >= 0 && Tq <= INT32_MAX / 2 && Tk >= 0 &&
+  return B >= 0 && B < kMostPrompts && Tq >= 0 && Tq <= INT32_MAX / 2 && Tk >= 0 &&
          Tk <= INT32_MAX / 2 && heads_ok(Hq, Hkv) && D >= 1 && mul_ok(Tq, Hq, &t) &&
          mul_ok(t, D, &t) && mul_ok(t, 4, &t);
 }
