@@ -42,10 +42,10 @@
 // a second kernel joins in order.
 //
 // A key that a row does not see has P = 0, and 0 times a non-finite value is NaN.
-// The values past a sequence's end are cleared in shared memory; rows that a value
-// hidden from them by the causal mask has spoilt are computed again one by one over
-// the keys they see (8192 tokens, 8 x 5 heads of 128, 0.46 ms: with the last token's
-// value infinite 18 ms, with the first one's, which every row sees, 0.64).
+// The values past a long sequence's end are cleared in shared memory; rows that a
+// value hidden from them has spoilt are computed again over the keys they see (8192
+// tokens, 8 x 5 heads of 128, 0.46 ms: with the last token's value infinite 18 ms,
+// with the first one's, which every row sees, 0.64).
 //
 // All roles' code together is larger than the instruction cache: what runs once
 // an item is kept short, in loops where that costs nothing (a fifth of the
@@ -54,9 +54,9 @@
 // tile are unrolled: the MMAs of both halves of P issued by one loop, whose
 // operands are then no constants, took 583 us for 466 at 8192 tokens.
 //
-// Every wait is bounded (to some 6 s, or to so long without progress of the CTA);
-// one that runs out raises the device status word and the CTA drains what it has in
-// flight and exits.
+// Every wait is bounded, to some 6 s in which no warp computes rows again; one that
+// runs out raises the device status word and the CTA drains what it has in flight and
+// exits.
 #include <cuda_bf16.h>
 
 #include "async_util.cuh"
@@ -133,22 +133,17 @@ static_assert(sizeof(Item) <= 64, "its place in shared memory");
 
 __device__ __forceinline__ int clamped(int v, int hi) { return min(max(v, 0), hi); }
 
-// What the warps of a CTA tell one another beside the barriers.
-struct Pulse {
-  int abort;  // a wait ran out
-  int beat;   // moves on as K and V tiles are loaded, and in whatever else takes long
-};
+// What the warps of a CTA tell one another beside the barriers, in one word: kAborted,
+// a wait ran out; kBusy for each warp at something that may take long.
+constexpr int kAborted = 1, kBusy = 2;
 
 // A bounded wait, in few instructions: the warps' roles together are larger than
-// the instruction cache.  It gives up after kWaitLimit polls of 1.5 us; kItem: a
-// wait that may last a whole item, which goes on while the CTA makes progress.
-// (As all of them it took 1 to 2% of the prompts' time.)
-template <bool kItem = false>
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile Pulse* pulse) {
+// the instruction cache.  It gives up after kWaitLimit polls (of 1.5 us) while no
+// warp is busy.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* state) {
   const uint32_t at = smem_addr(bar);
-  int beat = -1;
 #pragma unroll 1
-  for (uint32_t i = kWaitLimit;;) {
+  for (uint32_t i = kWaitLimit; i > 0; --i) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
@@ -157,14 +152,26 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
         : "r"(at), "r"(parity)
         : "memory");
     if (done) return true;
-    if (pulse->abort) return false;
-    if (--i == 0) {
-      const int now = kItem ? pulse->beat : beat;
-      if (now == beat) return false;
-      beat = now, i = kWaitLimit;
+    const int now = *state;
+    if (__builtin_expect(now != 0, 0)) {
+      if (now & kAborted) return false;
+      i = kWaitLimit;
     }
   }
+  return false;
 }
+
+// A warp's stretch of being busy.
+struct Busy {
+  int* state;
+  __device__ __forceinline__ explicit Busy(volatile int* at) : state(const_cast<int*>(at)) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(state, kBusy);
+  }
+  __device__ __forceinline__ ~Busy() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) atomicSub(state, kBusy);
+  }
+};
 
 struct Span {
   int q0, nq, k0, nk;
@@ -203,7 +210,7 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&x)[N]) {
 constexpr int kGroup = 2;
 template <int D>
 __device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned todo, int t, int hq, int h,
-                                            int k0, int end, volatile Pulse* pulse) {
+                                            int k0, int end) {
   constexpr int N = D / 32, kBatch = D == 256 ? 4 : 8;
   const PrefillArgs& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -261,7 +268,6 @@ __device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned t
             }
           }
       }
-      pulse->beat = j0;
     }
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) {
@@ -291,8 +297,9 @@ __device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned t
 // (P may be 2^8 times a probability, and the sums of large values overflow).
 template <int D>
 __device__ __noinline__ void repair(const Args& p, int split, unsigned again, int t, int hq, int sees, int h,
-                                    int key0, int end, volatile Pulse* pulse) {
+                                    int key0, int end, volatile int* state) {
   constexpr int N = D / 32;
+  const Busy busy(state);
   const PrefillArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const bool mine = again >> lane & 1;
@@ -326,7 +333,6 @@ __device__ __noinline__ void repair(const Args& p, int split, unsigned again, in
       some |= first[i] < end;
       open |= first[i] == end && last[i] >= 0;
     }
-    pulse->beat = j0;
     if (__any_sync(~0u, some) && !__any_sync(~0u, open)) break;
   }
   unsigned todo = 0;
@@ -341,7 +347,7 @@ __device__ __noinline__ void repair(const Args& p, int split, unsigned again, in
     }
     if (__any_sync(~0u, spoiled) || !__any_sync(~0u, known)) todo |= 1u << who;
   }
-  attend_rows<D>(p, split, todo, t, hq, h, key0, key0 + sees, pulse);
+  attend_rows<D>(p, split, todo, t, hq, h, key0, key0 + sees);
 }
 
 // ---- tensor core -------------------------------------------------------------------
@@ -474,19 +480,41 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Zeros over the keys from `from` on of a ring unit of values, by a warp, for the
-// tensor core to see.
+// A ring unit of values with a sequence's end in it, for the tensor core to see zeros
+// past the `left` keys (64 or 128 from y on) that are the sequence's: it arrives at
+// `bar`, is cleared there and handed over at `full`.  False: the wait ran out.
+//
+// Sequences of more than kClear keys alone are given that: without it their rows (under
+// a causal mask the last ones, else all) are computed again when the next sequence's
+// values are not finite.  For short ones that is little, and the wait takes each item
+// 0.5 us (40 prompts of up to 300 tokens, 4 x 7 of 64, all keys: 29.6 us for 28.1).
+constexpr int kClear = 1024;
 template <int D>
-__device__ __noinline__ void clear_values(uint32_t unit, int from) {
+__device__ __noinline__ bool load_tail(const CUtensorMap* map, uint32_t unit, uint64_t* bar, uint32_t parity,
+                                       uint64_t* full, int h, int y, int left, volatile int* state) {
   using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  if (left > 0) {
+    if (lane == 0) {
+      mbar_expect_tx(bar, C::kUnit);
 #pragma unroll 1
-  for (uint32_t i = from * 128 + (threadIdx.x & 31) * 16; i < C::kVKeys * 128; i += 512)
+      for (int c = 0; c < D / 64; ++c) tma_3d(unit + c * C::kVKeys * 128, map, 64 * c, h, y, bar);
+    }
+    if (!__all_sync(~0u, bar_wait(bar, parity, state))) {
+      static_cast<void>(mbar_wait(bar, parity, nullptr));  // the copy lands
+      return false;
+    }
+  }
+#pragma unroll 1
+  for (uint32_t i = max(0, left) * 128 + lane * 16; i < C::kVKeys * 128; i += 512)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(unit + c * C::kVKeys * 128 + i), "r"(0)
                    : "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
 }
 
 // ---- the order of the work -----------------------------------------------------------
@@ -516,7 +544,7 @@ __device__ __forceinline__ int runs_of(const Args& p, int b) {
   return p.by_run(n + p.by_run.d - 1);
 }
 
-__device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pulse) {
+__device__ __forceinline__ Walk walk_from_top(const Args& p) {
   const int lane = threadIdx.x & 31, first = runs_of(p, lane);
   int most = first, all = first;
 #pragma unroll 1
@@ -524,7 +552,6 @@ __device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pul
     const int n = runs_of(p, b);
     most = max(most, n);
     all += n;
-    pulse->beat = b;
   }
   most = (int)__reduce_max_sync(~0u, most);
   all = (int)__reduce_add_sync(~0u, all);
@@ -536,8 +563,7 @@ __device__ __forceinline__ Walk walk_from_top(const Args& p, volatile Pulse* pul
 
 // The sequence and level of run i in that order; false: there are not so many.
 // i grows from call to call.
-__device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq, int* level,
-                                        volatile Pulse* pulse) {
+__device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq, int* level) {
   const int lane = threadIdx.x & 31;
   if (i >= w.all) return false;
 #pragma unroll 1
@@ -564,7 +590,6 @@ __device__ __forceinline__ bool walk_to(const Args& p, int i, Walk& w, int* seq,
         return true;
       }
       w.before += __shfl_sync(~0u, end, 31);
-      pulse->beat = w.before;
     }
   }
   return false;
@@ -603,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
            *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 2,
            *tail_full = ml_free + 2, *all_done = tail_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile Pulse* pulse = reinterpret_cast<volatile Pulse*>(smem + C::kOffMisc + 8);
+  volatile int* state = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
 
   const PrefillArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -638,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     mbar_init(tail_full, 1);
     mbar_init(all_done, kTiles);
-    pulse->abort = pulse->beat = 0;
+    *state = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   fence_before();
@@ -652,7 +677,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
   int seen = 0;  // items read
   auto read_item = [&](Item& it, bool one_lane) {
-    const bool there = bar_wait<true>(item_full + (seen & 1), (seen >> 1) & 1, pulse);
+    const bool there = bar_wait(item_full + (seen & 1), (seen >> 1) & 1, state);
     ok = one_lane ? there : __all_sync(~0u, there);
     if (!ok) return false;
     const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -669,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // ---- the items of this CTA, one ahead of their use, and their Q tiles, into L2 at
     // once and into shared memory when the tile before has been read ------------------
     int qn[kTiles] = {};  // Q tiles loaded
-    Walk walk = walk_from_top(p, pulse);
+    Walk walk = walk_from_top(p);
     for (int round = 0; ok; ++round) {
       // long items first, dealt out there and back, so that the CTAs' sums are alike
       const int i = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -678,7 +703,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int n = p.by_per(i), sub = i - n * p.by_per.d;
       it.b = -1;
       int t;
-      if (walk_to(p, n, walk, &it.b, &t, pulse)) {
+      if (walk_to(p, n, walk, &it.b, &t)) {
         const Span sp = span_of(a, it.b);
         it.split = p.by_heads(sub);
         it.q0 = sp.q0, it.nq = sp.nq, it.k0 = sp.k0, it.nk = sp.nk;
@@ -702,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
       }
       if (seen >= 2)
-        ok = __all_sync(~0u, bar_wait<true>(item_free + (seen & 1), ((seen >> 1) - 1) & 1, pulse));
+        ok = __all_sync(~0u, bar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, state));
       if (!ok) break;
       if (lane == 0) {
         volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
@@ -719,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (it.n[s] == 0) continue;
         const int y = it.q0 + it.first + s * p.tpt;
         if (lane < D / 64) tma_3d_prefetch(&map_q, 64 * lane, it.hq0, y);
-        if (qn[s] > 0) ok = ok && __all_sync(~0u, bar_wait<true>(q_free + s, (qn[s] - 1) & 1, pulse));
+        if (qn[s] > 0) ok = ok && __all_sync(~0u, bar_wait(q_free + s, (qn[s] - 1) & 1, state));
         if (!ok) break;
         ++qn[s];
         if (lane == 0) {
@@ -736,10 +761,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else if (warp == kLoad) {
     // ---- loads: K and V tiles through the ring in the order of their use:
     // K_0 V_0 K_1 V_1 ..., or with one Q tile K_0 K_1 V_0 K_2 V_1 ... --------------
-    int u = 0, tails = 0;  // units issued; those with an end of a sequence
+    int u = 0, tails = 0;  // units issued; those that waited for a sequence's end
     Item it;
     while (read_item(it, false)) {
       const int most = max(it.n[0], it.n[1]), key0 = it.k0 + it.lo * kKeys;
+      const int clear_from = it.nk > kClear ? it.k0 + it.nk : 0x7fffffff;
 #pragma unroll 1
       for (int i = 0; i < 2 * most && ok; ++i) {
         bool v = i & 1;
@@ -748,39 +774,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll 1
         for (int k = 0; k < C::kUnits; ++k, ++u) {
           const int st = u % C::kRing, round = u / C::kRing, y = key0 + j * kKeys;
-          if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, pulse));
+          if (round > 0) ok = __all_sync(~0u, bar_wait(empty + st, (round - 1) & 1, state));
           if (!ok) break;
           const uint32_t to = ring + st * C::kUnit;
-          // keys of the sequence from this unit of values on
-          const int left = v ? it.k0 + it.nk - y - k * C::kVKeys : C::kVKeys;
-          const bool tail = left < C::kVKeys;
-          uint64_t* const bar = tail ? tail_full : full + st;
-          if (left > 0 && elected()) {  // boxes of 64 columns: K by columns, V by keys
-            pulse->beat = u;
-            mbar_expect_tx(bar, C::kUnit);
+          if (__builtin_expect(v && y + (k + 1) * C::kVKeys > clear_from, 0)) {
+            const int at = y + k * C::kVKeys, left = it.k0 + it.nk - at;
+            ok = load_tail<D>(&map_v, to, tail_full, tails & 1, full + st, it.h, at, left, state);
+            if (!ok) break;
+            tails += left > 0;
+            continue;
+          }
+          if (elected()) {  // boxes of 64 columns: K by columns, V by keys
+            mbar_expect_tx(full + st, C::kUnit);
             if (v) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_3d(to + c * C::kVKeys * 128, &map_v, 64 * c, it.h, y + k * C::kVKeys, bar);
+                tma_3d(to + c * C::kVKeys * 128, &map_v, 64 * c, it.h, y + k * C::kVKeys, full + st);
             } else {
 #pragma unroll
               for (int c = 0; c < C::kCols / 64; ++c)
-                tma_3d(to + c * kKeys * 128, &map_k, k * C::kCols + 64 * c, it.h, y, bar);
+                tma_3d(to + c * kKeys * 128, &map_k, k * C::kCols + 64 * c, it.h, y, full + st);
             }
           }
           __syncwarp();
-          if (__builtin_expect(tail, 0)) {
-            // The values past the sequence's end, of another one, are cleared before the
-            // unit is handed over.
-            if (left > 0) {
-              ok = __all_sync(~0u, bar_wait(tail_full, tails & 1, pulse));
-              if (!ok) static_cast<void>(mbar_wait(tail_full, tails & 1, nullptr));  // the copy lands
-              if (!ok) break;
-              ++tails;
-            }
-            clear_values<D>(to, max(0, left));
-            if (lane == 0) mbar_arrive(full + st);
-          }
         }
       }
       if (!ok) break;
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // and one waits for barriers while the other's MMAs run -------------------------
     const int s = warp - kMma;
     auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, pulse));
+      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, state));
     };
     struct Place {  // in the ring
       int st;
@@ -944,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       for (int j = 0; j < tiles && ok; ++j) {
         const int g = done + j, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
         const uint32_t at = tmem + lanes + slot * kKeys;
-        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, pulse));
+        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, state));
         if (!ok) break;
         fence_after();
         const int left = sees - j * kKeys, left_lo = least - j * kKeys, left_hi = best - j * kKeys;
@@ -992,7 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           // O moves to the new maximum once the product with the tile before is
           // done (where S follows P, S says so)
           if constexpr (!kAfter) {
-            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, pulse));
+            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, state));
             if (!ok) break;
           }
           const float mn = t2 > m + kSlack ? t2 : m;
@@ -1062,7 +1078,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       float lo, hi;
       unpair(add2(sum2[0], sum2[1]), lo, hi);
       if (outs > 0) {
-        ok = __all_sync(~0u, bar_wait<true>(ml_free + s, (outs - 1) & 1, pulse));
+        ok = __all_sync(~0u, bar_wait(ml_free + s, (outs - 1) & 1, state));
         if (!ok) break;
       }
       ++outs;
@@ -1086,7 +1102,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int tok = first + my_tok, hq = it.hq0 + my_head;
         const bool mine = row < p.hg * p.tpt && tok < it.nq;
         const int64_t out_row = (int64_t)(it.q0 + tok) * a.Hq + hq;
-        ok = __all_sync(~0u, bar_wait<true>(ml_full + s, (told >> s) & 1, pulse));
+        ok = __all_sync(~0u, bar_wait(ml_full + s, (told >> s) & 1, state));
         if (!ok) break;
         told ^= 1u << s;
         const float2 ml = sums[s * kRows + row];
@@ -1100,7 +1116,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             a.lse[out_row] = l == 0.0f ? kNegInf : (ml.x + __log2f(l)) * kLn2;
         }
         if (tiles > 0) {
-          ok = __all_sync(~0u, bar_wait(o_full + s, (outs >> s) & 1, pulse));
+          ok = __all_sync(~0u, bar_wait(o_full + s, (outs >> s) & 1, state));
           if (!ok) break;
           outs ^= 1u << s;
           fence_after();
@@ -1155,20 +1171,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         unpair(checked, lo, hi);
         const unsigned again = __ballot_sync(~0u, mine && !(lo + hi == 0.0f) && l == l);
         if (again) {
-          const int key0 = it.lo * kKeys, end = min(tiles * kKeys, it.nk - key0);
+          // the part's keys in the tiles, those past the sequence's end too unless they
+          // were cleared
+          const int key0 = it.lo * kKeys,
+                    end = min(tiles * kKeys, (it.nk > kClear ? it.nk : (int)a.Tk - it.k0) - key0);
           const int sees = (a.causal ? min(it.nk, it.nk - it.nq + tok + 1) : it.nk) - key0;
           __syncwarp();
-          repair<D>(p, it.split, again, it.q0 + tok, hq, min(sees, end), it.h, it.k0 + key0, end, pulse);
+          repair<D>(p, it.split, again, it.q0 + tok, hq, min(sees, end), it.h, it.k0 + key0, end, state);
         }
       }
       if (!ok) break;
     }
   }
   if (!ok) {
-    pulse->abort = 1;
+    if (lane == 0) atomicOr(const_cast<int*>(state), kAborted);
     if (lane == 0) atomicOr(status, kDevTimeout);
   }
-  if (pulse->abort && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
+  if ((*state & kAborted) && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
   fence_before();
   __syncthreads();
   if (warp == kMma) {

@@ -337,6 +337,25 @@ def test_the_next_prompts_values_reach_no_row(P, D, Hkv, G, causal):
         assert ms < 3 * s.ms + 0.5, (ms, s.ms)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,Hkv,G", [(128, 2, 5), (64, 2, 4), (256, 1, 6)])
+def test_a_short_prompts_neighbours_values_reach_no_row(P, D, Hkv, G, causal):
+    import torch
+
+    for n in (3, 130, 700, 1024, 1025, 1100):
+        s = Long(P, D, [50, n, 40], [50, n, 40], Hkv, G, D, causal)
+        v = s.v.clone()
+        v[:50], v[50 + n:] = float("inf"), float("nan")
+        out, lse, ms = s.run(v)
+        assert torch.equal(lse, s.lse) and torch.isnan(out[50 + n:]).all()
+        mine, clean = out[50:50 + n], s.clean[50:50 + n]
+        moved = (mine != clean).any(-1).nonzero().cpu().numpy()
+        for i, hq in moved[:: max(1, len(moved) // 25)]:
+            s.check_row(out, lse, 50 + i, hq, s.v, slice(50, 50 + (i + 1 if causal else n)))
+        assert torch.isfinite(mine).all() and (mine - clean).abs().max() < 0.1
+        assert ms < 30
+
+
 @pytest.mark.parametrize("D,G,nq,nk", [(128, 5, 40, 9000), (64, 1, 70, 12345), (256, 6, 9, 5000)])
 def test_non_finite_values_where_the_keys_are_cut_into_parts(P, D, G, nq, nk):
     import torch
