@@ -498,12 +498,12 @@ PTQ_API size_t ptq_attn_decode_workspace_bytes(int64_t B, int64_t q_heads, int64
  * softmax_scale is finite and positive.  With PTQ_F32 the arithmetic keeps
  * fp32 accuracy over both cache types: over int8 a weight times its value's
  * scale has 22 bits, or 2^-35 of the row's largest such product.  Factors are
- * split into 16-bit terms, so an infinite query (or a fp32 one past the largest
- * bf16 value) makes its row NaN, except in bf16 over bf16, and over a bf16 cache
- * with PTQ_F32 so does an infinite key or value that is seen.  The work is
- * split by a rule on the shapes and the lengths alone, and the parts are joined
- * in a fixed order:
- * results are bitwise reproducible.  B = 0 is a no-op; B is under 2^30.
+ * split into 16-bit terms.  So an infinite query makes its row NaN, except in
+ * bf16 over bf16; over a bf16 cache with PTQ_F32 so do a query past the largest
+ * bf16 value and an infinite key or value that is seen.  The work is split by a
+ * rule on the shapes, the lengths and the clusters that the device holds, and
+ * the parts are joined in a fixed order: results are bitwise reproducible on
+ * one device.  B = 0 is a no-op; B is under 2^30.
  * workspace: device scratch of ptq_attn_decode_workspace_bytes(...) bytes,
  * 16-byte aligned, caller-owned, any initial contents.  Calls whose kernels
  * overlap on the GPU need separate workspaces.
@@ -536,9 +536,11 @@ PTQ_API size_t ptq_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t T
  * flags: 0, every query sees all keys of its sequence; PTQ_ATTN_CAUSAL, query
  * i of nq sees the keys j <= i + nk - nq (the last query sees all, and with
  * nk < nq the first ones see none).  A key or value a query does not see has
- * no effect on it, NaN and infinities included.
+ * no effect on it, NaN and infinities included.  A seen value that is not finite
+ * leaves its dimension of the output not finite, and no other.
  * dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED (the fp32
- * route serves decode).  Probabilities enter the second product as bf16.
+ * route serves decode).  Probabilities enter the second product as bf16, the
+ * type of the values: a relative 2^-9 of each, their sum is taken in fp32.
  * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; Tq and Tk are
  * under 2^30, B under 2^26.  workspace as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
  * Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for unknown flags. */

@@ -643,9 +643,9 @@ def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     on = cache._on
     sp = _dev(slots, cache._int32, "slots", on)
     if k is None:
-        k = _new(slots, shape, dtype, stream)
+        k = slots.new_empty(shape, dtype=dtype) if stream is None else _new(slots, shape, dtype, stream)
     if v is None:
-        v = _new(slots, shape, dtype, stream)
+        v = slots.new_empty(shape, dtype=dtype) if stream is None else _new(slots, shape, dtype, stream)
     kp, ks = _heads(k, "k", dtype, on, shape)
     vp, vs = _heads(v, "v", dtype, on, shape)
     _check(load().ptq_kv_read(cache._ref, sp, shape[0], kp, vp, ks, vs, _act_dtype(k),

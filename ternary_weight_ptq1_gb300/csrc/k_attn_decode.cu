@@ -10,11 +10,11 @@
 // rate; few or short sequences are bound by a call's chain of latencies
 // (lengths, page numbers, rows, the joins).
 //
-// Measured: 64 sequences of up to 8192 tokens, 8 x 8 heads of 128, bf16 over
-// int8, in 105 us (5.5 TB/s, 81% of the copy rate); one of 131,001 tokens, 4 x 6
-// of 256, bf16 cache, in 87 us (6.1 TB/s, 91%); 96 of up to 700 tokens, 16 heads
-// of 64, bf16, in 30 us (60%: three starts a CTA); 8 of up to 4096, 8 x 5 of 128,
-// fp32 over int8, in 14.6 us; one of 777 tokens, fp32 over bf16, in 8.6 us.
+// Measured in CUDA graphs: 64 sequences of up to 8192 tokens, 8 x 8 heads of 128, bf16
+// over int8, in 104 us (5.5 TB/s, 82% of the copy rate); one of 131,001 tokens, 4 x 6
+// of 256, bf16 cache, in 89 us (6.0 TB/s, 89%); 96 of up to 700 tokens, 16 heads
+// of 64, bf16, in 31 us (59%: three starts a CTA); 8 of up to 4096, 8 x 5 of 128,
+// fp32 over int8, in 14.4 us; one of 777 tokens, fp32 over bf16, in 8.7 us.
 //
 // Split.  The tokens of one (sequence, kv head) are cut into tiles of kT; the
 // tiles of all of them, in order, are dealt to the CTAs in runs of equal cost,
@@ -48,7 +48,7 @@
 //   bf16 cache, bf16 q: q is exact, p has two bf16 terms, 16 bits;
 //   bf16 cache, fp32 q: three bf16 terms, the third in a second instruction.
 // More than eight heads take two row blocks a warp (kBlocks) up to head_dim
-// 128 (64 x 4096 tokens, 2 x 16 heads of 128: 52 us over int8 and 59 over bf16,
+// 128 (64 x 4096 tokens, 2 x 16 heads of 128: 52 us over int8 and 57 over bf16,
 // for 63 and 89 with a block each); where there are more blocks still, each
 // reads the cache again (the same moment, so mostly from L2).
 // The fp32 routes, those of two row blocks and 256-wide heads over int8 (64 x 4096

@@ -11,16 +11,18 @@
 // of 256 columns is 2048 clocks of products and 320 KB, 2500 clocks.  On short
 // ones the chain S, softmax, P, O of each item's few steps bounds it.
 //
-// Measured, causal, bf16: 8192 tokens of 8 x 5 heads of 128 in 450 to 483 us
-// (1420 to 1525 TFLOP/s, 76 to 82% of a library product's rate), of 4 x 6 heads
-// of 256 at 1480 TFLOP/s, of 4 x 7 of 64 in 270 us (890); 16 prompts of up to
-// 1100 tokens in 75 us (800); two of up to 515 over prefixes of up to 7000,
-// 4 x 6 of 256, in 79 us (830, on 1.2 items an SM); 77 tokens in 7.4 us.
+// Measured in CUDA graphs, causal, bf16: 8192 tokens of 8 x 5 heads of 128 in 453 us
+// (1520 TFLOP/s, 82% of a library product's rate) over some ms, 473 over longer runs; of
+// 4 x 6 heads of 256 in 546 (1510), of 4 x 7 of 64 in 261 (920); 16 prompts of up to
+// 1100 tokens in 76 us (790); two of 460 and 479 over prefixes, 3518 and 2667 keys,
+// 4 x 6 of 256, in 77 us (850, on 1.2 items an SM); 77 tokens in 7.5 us.
 //
 // Tile.  128 rows of Q are tpt tokens of hg query heads that share a kv head
 // (row = token * hg + head, one TMA box), against tiles of 128 keys.  S and O
 // live in TMEM; P goes back there as bf16 over S's columns and is the A
-// operand of the second product, so only K and V pass through shared memory.
+// operand of the second product, so only K and V pass through shared memory.  (A and
+// B have one type, and V is bf16: P keeps 8 bits.  A second bf16 term of it would add
+// half to the products.  Its sum is taken in fp32, before the rounding.)
 // A CTA holds two Q tiles (head_dim up to 128), neighbours in the sequence,
 // that share each K and V tile; at head_dim 256 one Q tile whose S has two
 // buffers.  Either way the tensor core has one S's products in work while the
@@ -49,8 +51,8 @@
 //
 // All roles' code together is larger than the instruction cache: what runs once
 // an item is kept short, in loops where that costs nothing (a fifth of the
-// fetches missed when the kernel had 74 KB; at 53 KB 3% do, and the packed
-// prompts went from 101 us to 75).  Only the products and the softmax of a
+// fetches missed when 74 KB were in use; of the 52 KB besides what spoilt rows and
+// ends of sequences take, 4% do, and the packed prompts went from 101 us to 76).  Only the products and the softmax of a
 // tile are unrolled: the MMAs of both halves of P issued by one loop, whose
 // operands are then no constants, took 583 us for 466 at 8192 tokens.
 //
@@ -1266,8 +1268,8 @@ struct Plan {
 // Where the items fill less than half the SMs and the keys are long, each
 // item's keys are cut into parts of at least eight tiles, for about one item an
 // SM: 64 queries over 8192 keys, 8 x 5 heads of 128, take 28 us so and 90 whole.
-// (An item costs about four tiles of its own: with 180 items of up to 55 tiles
-// two parts took 84 us and one 78.)  A function of the shapes alone, so
+// (An item costs about four tiles of its own: with 180 items of 18 to 28 tiles two
+// parts took 84 us and one 78.)  A function of the shapes alone, so
 // the workspace query and the launch agree.
 Plan plan_of(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D) {
   Plan r;

@@ -4,17 +4,19 @@
 // A row is the head_dim values of one token and head.  PTQ_KV_I8 stores
 //     s = max_d |x_d| / 127,  c_d = round_half_even(x_d / s)
 // with IEEE fp32 divisions, so a row's codes and scale are a function of its
-// values alone; the row stands for c_d s.  Both kernels move each byte once
-// and compute a few operations a value: HBM bounds them, the launch at a
-// decode step's sizes.  A thread holds eight consecutive values (16 or 32
+// values alone; the row stands for c_d s.  Both kernels move each byte once: HBM
+// bounds them over bf16, the launch at a decode step's sizes.  Over int8 the write is
+// bound by its instructions (420 of a warp, the SMs issue in 74% of their cycles;
+// rintf and the conversions are a quarter of the slow pipe's time), the read waits for
+// its loads.  A thread holds eight consecutive values (16 or 32
 // bytes in, 8 or 16 out) of a key and the same of its value, so head_dim / 8
 // neighbouring threads share a row and its maximum is three to five shuffles.
 // (With two pieces of each the write and read of 33,001 x 4 x 256 took 139 us
 // when this took 109.)
 //
-// Measured, a write and a read together: 33,001 x 4 x 256, bf16, 82 us (98% of
-// the copy rate); 8192 x 8 x 128, bf16 through int8, 23 us (65%: 4 us are the
-// two launches); 64 x 8 x 128, fp32 through int8, 4.0 us, the launches.
+// Measured, a write and a read together, in CUDA graphs: 33,001 x 4 x 256, bf16, 82 us
+// (98% of the copy rate); 8192 x 8 x 128, bf16 through int8, 25 us (61%); 64 x 8 x 128,
+// fp32 through int8, 4.0 us, the launches.
 #include <cuda_bf16.h>
 #include <float.h>
 

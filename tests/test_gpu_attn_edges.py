@@ -1,5 +1,6 @@
 """The edges of the paged cache and the attention operators: rows of the
-smallest subnormals, value scales that differ by orders of magnitude."""
+smallest subnormals, value scales that differ by orders of magnitude, buffers on
+other streams, thousands of prompts, values that are not finite."""
 import numpy as np
 import pytest
 
