@@ -641,10 +641,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
           // to 2^126 at most (larger weights still fit fp16; NaN stays in the products).
           most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
           most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-          const float up = fmaxf(fmaxf(most, 0.5f * kTiny), 0.5f * ref[h] * f);
+          const float old = ref[h] * f;  // (0 where the weights so far are nothing)
+          const float up = fmaxf(fmaxf(most, 0.5f * kTiny), 0.5f * old);
           const uint32_t bits = (min(__float_as_uint(up), 0x7e000000u) & 0x7f800000u) + 0x00800000u;
           const float over = __uint_as_float(0x7f000000u - bits);  // one over it
-          fade[h] = f * (ref[h] * over);
+          fade[h] = old * over;          // at most 2; the references alone may be 2^242 apart
           ref[h] = __uint_as_float(bits);
           inv = kPScale * over;
         }

@@ -79,7 +79,8 @@ def _weighted_bound(q, k, v, vs, scale, bf16_out):
     return out, bound + (2.0 ** -8 * np.abs(out) if bf16_out else 0)
 
 
-def _decode_weighted(P, k, v, q, act, page, width, what):
+def _decode_weighted(P, k, v, q, act, page, width, what, copies=1):
+    """One sequence, or `copies` of it over the same pages (a CTA then takes whole ones)."""
     import torch
 
     n, D = len(k), k.shape[-1]
@@ -93,12 +94,13 @@ def _decode_weighted(P, k, v, q, act, page, width, what):
     lens = torch.tensor([n], dtype=torch.int32, device="cuda")
     q = R.bf16(q) if act == "bf16" else q.astype(np.float32)
     qd = dev(q)[None].to(torch.bfloat16 if act == "bf16" else torch.float32)
-    out = _host(P.attn_decode(qd, cache, table, lens))[0]
+    out = P.attn_decode(qd.repeat(copies, 1, 1), cache, table.repeat(copies, 1), lens.repeat(copies))
+    out = _host(out[[0, copies // 2, copies - 1]])
     (kc, ks), (vc, vs) = R.quantise(k), R.quantise(v)
     kk, vv = (c.astype(np.float64) * s[:, None].astype(np.float64) for c, s in ((kc, ks), (vc, vs)))
     for h in range(len(q)):
         ref, bound = _weighted_bound(q[h], kk, vv, vs, D ** -0.5, act == "bf16")
-        err = np.abs(out[h] - ref)
+        err = np.abs(out[:, h] - ref)
         assert (err <= bound).all(), f"{what} head {h}: off by {(err / bound).max():.3g} of the bound"
 
 
@@ -128,6 +130,23 @@ def test_values_of_any_size(P, act, size):
     q = rng.standard_normal((5, D))
     for width in (40, 200):
         _decode_weighted(P, k.astype(np.float32), v.astype(np.float32), q, act, 16, width, f"{size}")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 5), (128, 12), (256, 3)])
+def test_a_great_value_before_scores_that_leave_it_no_weight(P, act, D, G):
+    """The weights so far underflow at once, and the values that follow are smaller
+    by more than fp32's exponents (2^140)."""
+    rng = np.random.default_rng([D, G, 1])
+    n = 300
+    base = rng.standard_normal(D)
+    q = base + 0.05 * rng.standard_normal((G, D))
+    k, v = 0.05 * rng.standard_normal((n, D)), rng.standard_normal((n, D)) * 2.0 ** -70
+    k[n // 2:] += base * 150 * np.sqrt(D) / (base @ base)
+    v[:n // 2] *= 2.0 ** 140
+    for width in (40, 200):
+        for copies in (1, 400):
+            _decode_weighted(P, k.astype(np.float32), v.astype(np.float32), q, act, 16, width, "2^140", copies)
 
 
 # ---- streams -----------------------------------------------------------------------
