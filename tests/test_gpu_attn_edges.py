@@ -195,6 +195,31 @@ def test_default_buffers_on_another_stream(P):
         del got, fill
 
 
+def test_default_buffers_in_a_graph_of_two_streams(P):
+    import torch
+
+    torch.manual_seed(5)
+    q, k, v = (torch.randn(n, h, 128, device="cuda").bfloat16() for n, h in ((40, 5), (9000, 1), (9000, 1)))
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (40, 9000))
+    want = P.attn_prefill(q, k, v, cu_q, cu_k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    P.attn_prefill(q, k, v, cu_q, cu_k, stream=side)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        one = P.attn_prefill(q, k, v, cu_q, cu_k)
+        side.wait_stream(torch.cuda.current_stream())
+        two = P.attn_prefill(q, k, v, cu_q, cu_k, stream=side)
+        three = P.attn_prefill(q, k, v, cu_q, cu_k)
+        torch.cuda.current_stream().wait_stream(side)
+    for t in (one, two, three):
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in (one, two, three))
+
+
 # ---- prompts: many sequences ---------------------------------------------------------
 
 def _prompts(P, rng, nqs, nks, Hkv, G, D, causal, pick):
@@ -413,3 +438,25 @@ def test_large_values_under_a_maximum_that_grows_a_little(P, D):
     for i in range(nq):
         ref = R.attend(_host(q[i]), _host(k[:n - nq + i + 1, 0]), _host(v[:n - nq + i + 1, 0]), 1.0)
         R.check(_host(out[i]), None, ref, True, True)
+
+
+@pytest.mark.parametrize("D,Hkv,G", [(128, 2, 5), (64, 2, 4), (256, 1, 6)])
+def test_strided_tensors_and_an_output_of_16_byte_alignment(P, D, Hkv, G):
+    """Columns of one projection's rows, hidden and seen values that are not finite,
+    an output 16 bytes off a 32-byte boundary: as with tensors of their own."""
+    import torch
+
+    nqs = [1300, 70, 5]
+    s = Long(P, 9, nqs, nqs, Hkv, G, D)
+    v = s.v.clone()
+    v[1250, 0], v[1299], v[1305, 0, 2], v[40, Hkv - 1, 1] = float("nan"), float("inf"), float("nan"), float("inf")
+    want, lse, _ = s.run(v)
+    row = torch.cat([s.q, s.k, v], 1)
+    n, Hq = s.q.shape[:2]
+    buf = torch.full((n * Hq * D + 24,), 9.0, device="cuda", dtype=torch.bfloat16)
+    out = buf[8:-16].view(n, Hq, D)
+    assert out.data_ptr() % 32 == 16
+    lse2 = torch.empty_like(lse)
+    P.attn_prefill(row[:, :Hq], row[:, Hq:Hq + Hkv], row[:, Hq + Hkv:], *s.cu, out=out, lse=lse2)
+    assert torch.equal(lse, lse2) and torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
+    assert torch.equal(out.isnan(), want.isnan()) and (buf[:8] == 9).all() and (buf[-16:] == 9).all()
