@@ -52,9 +52,10 @@
 // All roles' code together is larger than the instruction cache: what runs once
 // an item is kept short, in loops where that costs nothing (a fifth of the
 // fetches missed when 74 KB were in use; of the 52 KB besides what spoilt rows and
-// ends of sequences take, 4% do, and the packed prompts went from 101 us to 76).  Only the products and the softmax of a
-// tile are unrolled: the MMAs of both halves of P issued by one loop, whose
-// operands are then no constants, took 583 us for 466 at 8192 tokens.
+// ends of sequences take, 4% do, and the packed prompts went from 101 us to 76).
+// Only the products and the softmax of a tile are unrolled: the MMAs of both halves
+// of P issued by one loop, whose operands are then no constants, took 583 us for 466
+// at 8192 tokens.
 //
 // Every wait is bounded, to some 6 s in which no warp computes rows again; one that
 // runs out raises the device status word and the CTA drains what it has in flight and
@@ -207,8 +208,8 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&x)[N]) {
 
 // Query rows by a warp, kGroup rows and 32 keys at a time (a lane's own key for the
 // scores, a lane's own columns for the outputs): those of the lanes `todo` (a lane a
-// row: query t, head hq, over keys [k0, end)).  (Groups of four need more registers
-// than kRegsStore.)
+// row: query t, head hq, over keys [k0, end)).  (Groups of two need 64 registers, 100 at
+// head_dim 256, groups of four more than kRegsStore, which the function has to fit.)
 constexpr int kGroup = 2;
 template <int D>
 __device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned todo, int t, int hq, int h,
