@@ -209,7 +209,7 @@ def prepare(case, seed):
             c = s["cache"]
             s["handle"] = P.KVCache(c["k"], c["v"], c["k_scale"], c["v_scale"])
         if case["op"] in ("rope", "append"):
-            s["rope"] = P.Rope(s["inv_freq"], axis=s["axis"], near=case["pairs"] == "near",
+            s["rope"] = P.Rope(s["inv_freq"], axis=s["axis"], interleaved=case["pairs"] == "near",
                                q_gain=s["q_gain"], k_gain=s["k_gain"], eps=EPS)
             if case.get("kv") == "i8":
                 s["k_read"], s["v_read"] = (torch.empty(case["tokens"], H, D, dtype=torch.bfloat16, device="cuda")
