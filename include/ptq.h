@@ -552,6 +552,120 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_attn_prefill(
     float softmax_scale, unsigned flags, ptq_dtype dtype, void* workspace,
     size_t workspace_bytes, ptq_stream_t stream);
 
+/* ---- positions: head norms, rotation, and the way into the cache ------------- */
+
+/* How queries and keys are normed and rotated; a HOST struct, read during the
+ * call only, whose pointers are device memory.
+ *   inv_freq  rotary_dim / 2 fp32: pair i turns by pos * inv_freq[i] radians.
+ *             Its angles are right to 2^-31 of a turn at any position.
+ *   axis      rotary_dim / 2 int8: which axis of the positions pair i goes by
+ *             (text, or time, height and width of images and video); NULL: all
+ *             by axis 0.  A pair whose axis is not in [0, axes) is not turned.
+ *   pos       axes x T int32, an axis pos_stride elements after the one before
+ *   rotary_dim  the head's first values that are turned: a multiple of 8, 0 to
+ *             head_dim (0: none; inv_freq and pos may then be NULL)
+ *   interleaved  0: pair i is values i and i + rotary_dim / 2; else 2 i, 2 i + 1
+ *   q_gain, k_gain  head_dim fp32, 16-byte aligned: each head of q / k becomes
+ *             x / sqrt(mean(x^2) + eps) * gain before it is turned; NULL: it is
+ *             not normed
+ *   eps       finite and positive where there is a gain */
+typedef struct ptq_rope {
+  const float* inv_freq;
+  const int8_t* axis;
+  const int32_t* pos;
+  int64_t pos_stride;
+  int64_t axes;
+  int64_t rotary_dim;
+  int interleaved;
+  const float* q_gain;
+  const float* k_gain;
+  float eps;
+} ptq_rope;
+
+/* ptq_qk_rope -- queries and keys normed and rotated: what attention takes.
+ *   q, k   T x q_heads / kv_heads x head_dim of dtype, tokens q_stride /
+ *          k_stride elements apart (columns of a fused projection's output);
+ *          16-byte aligned, strides a multiple of 16 bytes
+ *   q_out, k_out  the same, q_out_stride / k_out_stride apart.  Each may be its
+ *          input (with its stride); other overlaps are not allowed.
+ * Either of q_heads and kv_heads may be 0 (its pointers are then not used).
+ * head_dim is 64, 128 or 256.  Arithmetic is fp32, with one rounding at the end.
+ * T = 0 is a no-op.  Errors: PTQ_ERR_NULL, PTQ_ERR_SHAPE (rotary_dim, axes and
+ * pos_stride among them), PTQ_ERR_ALIGN, PTQ_ERR_VALUE (dtype, eps),
+ * PTQ_ERR_UNSUPPORTED (head_dim), PTQ_ERR_CUDA. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_qk_rope(const ptq_rope* rope, const void* q, const void* k,
+                                             int64_t q_stride, int64_t k_stride, void* q_out,
+                                             void* k_out, int64_t q_out_stride,
+                                             int64_t k_out_stride, int64_t T, int64_t q_heads,
+                                             int64_t kv_heads, int64_t head_dim, ptq_dtype dtype,
+                                             ptq_stream_t stream);
+
+/* ptq_kv_append -- T tokens' keys, normed and rotated, and values, as they
+ * are, into the cache, and (q_heads > 0) their queries, normed and rotated,
+ * into q_out: what ptq_qk_rope and ptq_kv_write do, in one pass.  A key goes
+ * from fp32 to the cache's type, with no rounding to dtype between.
+ *   q, k, v, slots and q_out as for ptq_qk_rope and ptq_kv_write: a slot
+ *   outside the cache skips its token's key and value (not its query), and two
+ *   tokens with one slot leave either's values there.
+ * Errors as ptq_qk_rope and ptq_kv_write. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_kv_append(const ptq_kv_cache* cache, const ptq_rope* rope,
+                                               const void* q, const void* k, const void* v,
+                                               int64_t q_stride, int64_t k_stride,
+                                               int64_t v_stride, const int32_t* slots,
+                                               void* q_out, int64_t q_out_stride, int64_t T,
+                                               int64_t q_heads, ptq_dtype dtype,
+                                               ptq_stream_t stream);
+
+/* ---- attention over part of the cache: chunks and windows ---------------------- */
+
+/* ptq_attn_decode_window -- ptq_attn_decode where the new token sees its
+ * sequence's last `window` tokens, itself among them, and the first `sinks`.
+ * window = 0: all tokens (ptq_attn_decode; sinks then counts for nothing).  0 <=
+ * window, sinks < 2^31.  Entries of the table whose tokens are not seen are not
+ * used.  Workspace, arithmetic and errors as ptq_attn_decode, plus
+ * PTQ_ERR_VALUE for window and sinks. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_attn_decode_window(
+    const void* q, int64_t q_stride, const ptq_kv_cache* cache, const int32_t* table,
+    int64_t table_width, const int32_t* lens, void* out, float* lse, int64_t B, int64_t q_heads,
+    float softmax_scale, int64_t window, int64_t sinks, ptq_dtype dtype, void* workspace,
+    size_t workspace_bytes, ptq_stream_t stream);
+
+/* ptq_attn_chunk_workspace_bytes -- scratch of ptq_attn_chunk; 0 when it needs
+ * none or the arguments are invalid. */
+PTQ_API size_t ptq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              ptq_dtype dtype);
+
+/* ptq_attn_chunk -- attention of each sequence's newest tokens (a prompt's next
+ * chunk, the tokens a draft is checked with, a decode step's one) over its
+ * cached tokens, those new ones among them (ptq_kv_append has stored them).
+ *   q       Tq x q_heads x head_dim bf16, tokens q_stride elements apart;
+ *           16-byte aligned, stride a multiple of 16 bytes
+ *   cu_q    B + 1 int32 offsets (device), not decreasing: the queries of
+ *           sequence b are rows cu_q[b] .. cu_q[b+1] - 1, counted into [0, Tq]
+ *   table, table_width, lens  as for ptq_attn_decode: query i of nq is token
+ *           p = lens[b] - nq + i.  It sees the tokens j <= p, and with window > 0
+ *           of those the last `window` (p - window < j) and the first `sinks`
+ *           (j < sinks).  With lens[b] < nq the first queries see none.
+ *   out     Tq x q_heads x head_dim bf16, contiguous; lse: Tq x q_heads fp32, or
+ *           NULL.  Rows of no sequence are not written.
+ * A query that sees a token of a page outside the cache is NaN (nothing is read
+ * for it); entries that no query of the sequence sees are not used.  A key or
+ * value that a query does not see has no effect on it, NaN and infinities
+ * included; a seen value that is not finite leaves its dimension of the output
+ * not finite.  dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED
+ * (ptq_attn_decode serves it).  Over int8 the codes enter the products as they
+ * are and the scales stay fp32; probabilities (times their value's scale) enter
+ * the second product as bf16, and their sum is taken in fp32.  Results are bitwise
+ * reproducible.  B = 0 or Tq = 0 is a no-op; Tq is under 2^30, B under 2^26.
+ * workspace as for ptq_attn_decode (NULL when ptq_attn_chunk_workspace_bytes is
+ * 0).  Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for window and sinks. */
+PTQ_API PTQ_NODISCARD ptq_status ptq_attn_chunk(
+    const void* q, int64_t q_stride, const ptq_kv_cache* cache, const int32_t* table,
+    int64_t table_width, const int32_t* lens, const int32_t* cu_q, void* out, float* lse,
+    int64_t B, int64_t Tq, int64_t q_heads, float softmax_scale, int64_t window, int64_t sinks,
+    ptq_dtype dtype, void* workspace, size_t workspace_bytes, ptq_stream_t stream);
+
 /* ptq_route -- the kernel ptq_matmul would run for (M, dtype) when K/128 is
  * even: writes its name to *kernel_name (static storage) and returns PTQ_OK,
  * or returns PTQ_ERR_UNSUPPORTED / PTQ_ERR_VALUE.  Host only. */

@@ -34,7 +34,8 @@ EXPORTS = ("ptq1_pack", "ptq1_unpack", "ptq_fwht", "ptq_matmul_workspace_bytes",
            "ptq_ffn_stack_ex", "ptq_ffn_stack_route", "ptq2_pack", "ptq2_unpack",
            "ptq_matmul_pq2_workspace_bytes", "ptq_matmul_pq2", "ptq_embed", "ptq_embed_ptq1",
            "ptq_kv_write", "ptq_kv_read", "ptq_attn_decode_workspace_bytes", "ptq_attn_decode",
-           "ptq_attn_prefill_workspace_bytes", "ptq_attn_prefill",
+           "ptq_attn_prefill_workspace_bytes", "ptq_attn_prefill", "ptq_qk_rope", "ptq_kv_append",
+           "ptq_attn_decode_window", "ptq_attn_chunk_workspace_bytes", "ptq_attn_chunk",
            "ptq_route", "ptq_gemv_plan", "ptq_matmul_bf16_accumulator", "ptq_matmul_f32_peel",
            "ptq_selftest_timeout",
            "ptq_selftest_grid_timeout",
@@ -110,7 +111,16 @@ def load(path: str | None = None):
     L.ptq_attn_prefill_workspace_bytes.restype = S
     L.ptq_attn_prefill.argtypes = ([_P] * 3 + [_I64] * 3 + [_P] * 4 + [_I64] * 6 +
                                    [ctypes.c_float, ctypes.c_uint, _I32, _P, S, _P])
-    for name in ("ptq_kv_write", "ptq_kv_read", "ptq_attn_decode", "ptq_attn_prefill"):
+    L.ptq_qk_rope.argtypes = [_P] * 3 + [_I64] * 2 + [_P] * 2 + [_I64] * 6 + [_I32, _P]
+    L.ptq_kv_append.argtypes = [_P] * 5 + [_I64] * 3 + [_P] * 2 + [_I64] * 3 + [_I32, _P]
+    L.ptq_attn_decode_window.argtypes = ([_P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, ctypes.c_float,
+                                          _I64, _I64, _I32, _P, S, _P])
+    L.ptq_attn_chunk_workspace_bytes.argtypes = [_I64] * 5 + [_I32]
+    L.ptq_attn_chunk_workspace_bytes.restype = S
+    L.ptq_attn_chunk.argtypes = ([_P, _I64, _P, _P, _I64] + [_P] * 4 + [_I64] * 3 +
+                                 [ctypes.c_float, _I64, _I64, _I32, _P, S, _P])
+    for name in ("ptq_kv_write", "ptq_kv_read", "ptq_attn_decode", "ptq_attn_prefill", "ptq_qk_rope",
+                 "ptq_kv_append", "ptq_attn_decode_window", "ptq_attn_chunk"):
         getattr(L, name).restype = _I32
     L.ptq_route.argtypes = [_I64, _I32, ctypes.POINTER(ctypes.c_char_p)]
     L.ptq_gemv_plan.argtypes = [_I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_int32)]
@@ -632,6 +642,110 @@ def kv_write(cache, k, v, slots, stream=None):
                                _act_dtype(k), _stream(stream, on)), "ptq_kv_write")
 
 
+class _RopeStruct(ctypes.Structure):
+    """ptq_rope (include/ptq.h)."""
+    _fields_ = [("inv_freq", _P), ("axis", _P), ("pos", _P), ("pos_stride", _I64), ("axes", _I64), ("rotary_dim", _I64),
+                ("interleaved", _I32), ("q_gain", _P), ("k_gain", _P), ("eps", ctypes.c_float)]
+
+
+class Rope:
+    """How heads are normed and rotated, over the caller's tensors: inv_freq
+    (float32, one frequency for each pair of the rotated values, so the first 2
+    len(inv_freq) values of a head are rotated), axis (int8, the positions' axis
+    that each pair goes by; None: the first), q_gain and k_gain (head_dim float32;
+    None: no norm).  Pair i is values i and i + len(inv_freq), or with
+    `interleaved` 2 i and 2 i + 1.  Keeps the tensors alive; none is replaced."""
+
+    def __init__(self, inv_freq, axis=None, interleaved=False, q_gain=None, k_gain=None, eps=1e-6):
+        import torch
+
+        if inv_freq.dim() != 1 or (axis is not None and axis.shape != inv_freq.shape):
+            raise ValueError("inv_freq must have one frequency for each pair, axis one axis for each")
+        on = inv_freq.get_device() if getattr(inv_freq, "is_cuda", False) else None
+        for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+            if g is not None and g.dim() != 1:
+                raise ValueError(f"{name} must be head_dim values")
+        self._int32 = torch.int32
+        self._on = on
+        self.inv_freq, self.axis, self.q_gain, self.k_gain = inv_freq, axis, q_gain, k_gain
+        self._front = (_dev(inv_freq, torch.float32, "inv_freq", on),
+                       None if axis is None else _dev(axis, torch.int8, "axis", on))
+        self._back = (2 * inv_freq.numel(), int(bool(interleaved)),
+                      None if q_gain is None else _dev(q_gain, torch.float32, "q_gain", on),
+                      None if k_gain is None else _dev(k_gain, torch.float32, "k_gain", on), eps)
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name} of a Rope is not replaced: make a new one")
+        self.__dict__[name] = value
+
+    def _at(self, pos, T, D, on):
+        """The struct for T tokens of head width D at `pos`, on device `on`."""
+        if self._on != on:
+            raise ValueError(f"the tensors of the Rope are on another device: cuda:{self._on}, not cuda:{on}")
+        for g, name in ((self.q_gain, "q_gain"), (self.k_gain, "k_gain")):
+            if g is not None and g.shape[0] != D:
+                raise ValueError(f"{name} must be {D} values, got {g.shape[0]}")
+        s = pos.shape
+        if len(s) not in (1, 2) or s[-1] != T:
+            raise ValueError(f"pos must be axes x tokens ({T}), got {tuple(s)}")
+        return _RopeStruct(*self._front, _dev(pos, self._int32, "pos", on), T, 1 if len(s) == 1 else s[0], *self._back)
+
+
+def qk_rope(rope, q, k, pos, q_out=None, k_out=None, stream=None):
+    """The queries and keys (tokens x heads x head_dim, float32 or bfloat16;
+    heads contiguous, tokens any stride apart) normed and rotated as `rope` says,
+    at the int32 positions `pos` (tokens, or axes x tokens), as (q, k); into the
+    given q_out and k_out, which may be q and k themselves, or new tensors."""
+    dt, dtype = _act_dtype(q), q.dtype
+    on = q.get_device() if getattr(q, "is_cuda", False) else _misplaced(q, "q", 0)
+    qp, qs = _heads(q, "q", dtype, on)
+    kp, ks = _heads(k, "k", dtype, on)
+    T, Hq, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k must be {T} tokens of heads of {D}, got {tuple(k.shape)}")
+    at = rope._at(pos, T, D, on)
+    if q_out is None:
+        q_out = _new(q, q.shape, dtype, stream)
+    if k_out is None:
+        k_out = _new(k, k.shape, dtype, stream)
+    qo, qos = _heads(q_out, "q_out", dtype, on, q.shape)
+    ko, kos = _heads(k_out, "k_out", dtype, on, k.shape)
+    _check(load().ptq_qk_rope(ctypes.addressof(at), qp, kp, qs, ks, qo, ko, qos, kos, T, Hq, k.shape[1], D, dt,
+                              _stream(stream, on)), "ptq_qk_rope")
+    return q_out, k_out
+
+
+def kv_append(cache, rope, k, v, slots, pos, q=None, q_out=None, stream=None):
+    """Stores the keys k, normed and rotated as `rope` says at the int32
+    positions `pos`, and the values v at the `slots` of the cache (as kv_write),
+    in one pass; returns the queries q, normed and rotated likewise, in q_out or a
+    new tensor (None without q)."""
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    dt, dtype = _act_dtype(k), k.dtype
+    on = cache._on
+    kp, ks = _heads(k, "k", dtype, on, shape)
+    vp, vs = _heads(v, "v", dtype, on, shape)
+    T, _, D = shape
+    at = rope._at(pos, T, D, on)
+    qp = qo = None
+    qs = qos = Hq = 0
+    if q is not None:
+        qp, qs = _heads(q, "q", dtype, on)
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"q must be {T} tokens of heads of {D}, got {tuple(q.shape)}")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = _new(q, q.shape, dtype, stream)
+        qo, qos = _heads(q_out, "q_out", dtype, on, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(load().ptq_kv_append(cache._ref, ctypes.addressof(at), qp, kp, vp, qs, ks, vs,
+                                _dev(slots, cache._int32, "slots", on), qo, qos, T, Hq, dt, _stream(stream, on)),
+           "ptq_kv_append")
+    return q_out
+
+
 def kv_read(cache, slots, dtype=None, k=None, v=None, stream=None):
     """The values that the int32 `slots` of the cache stand for, as (k, v) of
     float32 or bfloat16 (default, where neither k nor v is given); into the
@@ -681,13 +795,15 @@ def _attn_buffers(q, out, lse, workspace, need, stream, on):
     return out, op, lp, wp, wb, workspace
 
 
-def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace=None, stream=None):
+def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace=None, stream=None, window=0,
+                sinks=0):
     """Attention of one new token of each sequence over its cached tokens.
     q: sequences x q_heads x head_dim, float32 or bfloat16; table: sequences x
     pages int32 page numbers; lens: int32 token counts.  `scale` defaults to
     head_dim ** -0.5; `lse` (sequences x q_heads float32), when given, receives
     the log-sum-exp of the scaled scores.  out and the workspace are allocated
-    by PyTorch when not given."""
+    by PyTorch when not given.  With `window` the token sees the last `window`
+    tokens of its sequence, itself among them, and the first `sinks`."""
     dt = _act_dtype(q)
     on = cache._on
     qp, qs = _heads(q, "q", q.dtype, on)
@@ -699,10 +815,45 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
         raise ValueError("table must be sequences x pages, lens one count for each sequence")
     out, op, lp, wp, wb, keep = _attn_buffers(
         q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt), stream, on)
-    _check(load().ptq_attn_decode(qp, qs, cache._ref, _dev(table, int32, "table", on), ts[1],
-                                  _dev(lens, int32, "lens", on), op, lp, B, Hq,
-                                  D ** -0.5 if scale is None else scale, dt, wp, wb,
-                                  _stream(stream, on)), "ptq_attn_decode")
+    tp, np_ = _dev(table, int32, "table", on), _dev(lens, int32, "lens", on)
+    scale = D ** -0.5 if scale is None else scale
+    if window == 0:
+        _check(load().ptq_attn_decode(qp, qs, cache._ref, tp, ts[1], np_, op, lp, B, Hq, scale, dt, wp, wb,
+                                      _stream(stream, on)), "ptq_attn_decode")
+    else:
+        _check(load().ptq_attn_decode_window(qp, qs, cache._ref, tp, ts[1], np_, op, lp, B, Hq, scale, window, sinks,
+                                             dt, wp, wb, _stream(stream, on)), "ptq_attn_decode_window")
+    return out
+
+
+def attn_chunk_workspace_bytes(B: int, Tq: int, q_heads: int, kv_heads: int, head_dim: int, dtype: int) -> int:
+    return int(load().ptq_attn_chunk_workspace_bytes(B, Tq, q_heads, kv_heads, head_dim, dtype))
+
+
+def attn_chunk(q, cache, table, lens, cu_q, window=0, sinks=0, scale=None, out=None, lse=None, workspace=None,
+               stream=None):
+    """Attention of each sequence's newest tokens, already in the cache, over
+    its cached tokens.  q: queries x q_heads x head_dim, bfloat16, the
+    sequences one after the other; cu_q: their int32 offsets (one more than there
+    are sequences); table and lens as for attn_decode.  A query sees its
+    token and those before it; with `window` the last `window` of these and the
+    first `sinks`.  scale, out, lse and workspace as for attn_decode."""
+    dt = _act_dtype(q)
+    on = cache._on
+    qp, qs = _heads(q, "q", q.dtype, on)
+    Tq, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q has head_dim {D}, the cache {cache.head_dim}")
+    ts, int32 = table.shape, cache._int32
+    B = cu_q.numel() - 1
+    if B < 0 or len(ts) != 2 or ts[0] != B or lens.shape != (B,):
+        raise ValueError("cu_q must have one offset more than there are sequences, table a row and lens a count for each")
+    out, op, lp, wp, wb, keep = _attn_buffers(
+        q, out, lse, workspace, lambda: attn_chunk_workspace_bytes(B, Tq, Hq, cache.kv_heads, D, dt), stream, on)
+    _check(load().ptq_attn_chunk(qp, qs, cache._ref, _dev(table, int32, "table", on), ts[1],
+                                 _dev(lens, int32, "lens", on), _dev(cu_q, int32, "cu_q", on), op, lp, B, Tq, Hq,
+                                 D ** -0.5 if scale is None else scale, window, sinks, dt, wp, wb,
+                                 _stream(stream, on)), "ptq_attn_chunk")
     return out
 
 

@@ -1,5 +1,5 @@
 // k_attn_decode.cu -- attention of one new token of each sequence over its
-// paged key-value cache.
+// paged key-value cache: all of its tokens, or the last ones and a few first.
 //
 //   s_j = scale q . k_j,  p_j = 2^(s_j log2(e) - m),  out = sum_j p_j v_j / sum_j p_j
 //
@@ -210,10 +210,23 @@ __device__ __forceinline__ float both(float first, float second) {
 // 1 / sum; a row whose scores are all -infinity is one that sees no key.
 __device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
-__device__ __forceinline__ int length(const DecodeArgs& a, int b) {
+// The tokens of a sequence of n that a window hides: those from the `sinks` first
+// on to the last `window`.
+__device__ __forceinline__ int hidden(const DecodeArgs& a, int n) {
+  return a.window ? max(0, max(0, n - a.window) - a.sinks) : 0;
+}
+
+__device__ __forceinline__ int cached(const DecodeArgs& a, int b) {
   const int64_t most = a.table_width * a.c.page_tokens;
   const int n = __ldg(a.lens + b);
   return n < 0 ? 0 : n > most ? (int)most : n;
+}
+
+// The tokens of sequence b that are seen: from here on the sequence is these
+// alone, one after the other.
+__device__ __forceinline__ int length(const DecodeArgs& a, int b) {
+  const int n = cached(a, b);
+  return n - hidden(a, n);
 }
 
 template <int kT>
@@ -230,6 +243,7 @@ __device__ __forceinline__ int units(int n) { return n ? n + kLead : 0; }
 struct Segment {
   int b, vh, t0, t1, n, len;
   int64_t u;  // its first unit's place among all
+  int skip;   // tokens hidden after the first ones
 };
 
 // The tiles of the segment's (sequence, row block) in units [u0, u1); false: none.
@@ -249,8 +263,11 @@ __device__ __forceinline__ void next_segment(Segment& s, const Args& p, int64_t 
   }
   if (++s.vh == p.VH) {
     s.vh = 0;
-    do s.len = length(p.a, ++s.b);
-    while (s.len == 0);
+    int all;
+    do all = cached(p.a, ++s.b);
+    while (all == 0);
+    s.skip = hidden(p.a, all);
+    s.len = all - s.skip;
     s.n = tiles_of<kT>(s.len);
   }
   if (!clip(s, s.u, u1)) s.b = -1;  // the run ends before its first tile
@@ -316,12 +333,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       if (a.lse)
         for (int64_t h = tid; h < a.Hq; h += kWarps * 32) a.lse[b * a.Hq + h] = kNegInf;
     }
-  Segment seg{-1, 0, 0, 0, 0, 0, 0};
+  Segment seg{-1, 0, 0, 0, 0, 0, 0, 0};
   int64_t u1 = 1, per = 1;
   if (p.cluster) {  // an equal part of this cluster's (sequence, row block)
     const int id = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
     seg.vh = id % p.VH;
-    seg.len = length(a, id / p.VH);
+    const int all = cached(a, id / p.VH);
+    seg.skip = hidden(a, all);
+    seg.len = all - seg.skip;
     seg.n = tiles_of<kT>(seg.len);
     seg.t0 = (int)((int64_t)seg.n * rank / p.cluster);
     seg.t1 = (int)((int64_t)seg.n * (rank + 1) / p.cluster);
@@ -378,7 +397,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
     {
       seg.b = *found;
       const int64_t in = u0 - scan[kWarps];
-      seg.len = length(a, seg.b);
+      const int all = cached(a, seg.b);
+      seg.skip = hidden(a, all);
+      seg.len = all - seg.skip;
       seg.n = tiles_of<kT>(seg.len);
       seg.vh = (int)(in / units(seg.n));
       seg.u = scan[kWarps] + (int64_t)seg.vh * units(seg.n);
@@ -414,11 +435,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
       const uint32_t dst = ring_at + stage * C::kStage;
       const int32_t* pages = a.table + ahead.b * a.table_width;
       const int j0 = at * kT, head = ahead.vh / p.HC;
-      if (p.whole && ahead.len - j0 >= kT) {  // a tile inside one page: one stretch of rows
-        const int page = __ldg(pages + (unsigned)j0 / (unsigned)ps);
+      // the tile's first token, and whether the tile is inside one page
+      const unsigned tok = (unsigned)j0 + (j0 >= a.sinks ? ahead.skip : 0);
+      const unsigned in_page = tok % (unsigned)ps;
+      const bool one = ahead.skip == 0 ? p.whole
+                                       : in_page + kT <= (unsigned)ps && (j0 >= a.sinks || a.sinks - j0 >= kT);
+      if (one && ahead.len - j0 >= kT) {  // one stretch of rows
+        const int page = __ldg(pages + tok / (unsigned)ps);
         const bool in = (unsigned)page < (unsigned)a.c.pages;
         if (lane == 0) bad[stage] = !in;
-        const int64_t row = ((int64_t)(in ? page : 0) * heads + head) * ps + (unsigned)j0 % (unsigned)ps;
+        const int64_t row = ((int64_t)(in ? page : 0) * heads + head) * ps + in_page;
         const char* k = static_cast<const char*>(a.c.k) + row * C::kRow + lane * 16;
         const char* v = static_cast<const char*>(a.c.v) + row * C::kRow + lane * 16;
 #pragma unroll
@@ -431,10 +457,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, D, kI8, kBlocks>::kPerSm)
           copy4(dst + 2 * C::kTile + 4 * kT + 4 * lane, a.c.v_scale + row + lane, true);
         }
       } else {
-        const unsigned j = (unsigned)j0 + lane % kT;
+        unsigned j = (unsigned)j0 + lane % kT;
+        j += j >= (unsigned)a.sinks ? ahead.skip : 0;
         int64_t row = -1;
         bool wrong = false;
-        if (lane % kT < ahead.len - j0) {
+        if (lane % kT < ahead.len - j0) {  // (else j may be past the table)
           const int page = __ldg(pages + j / (unsigned)ps);
           wrong = (unsigned)page >= (unsigned)a.c.pages;
           if (!wrong) row = ((int64_t)page * heads + head) * ps + j % (unsigned)ps;
@@ -967,7 +994,9 @@ cudaError_t launch(const DecodeArgs& a, void* ws, cudaStream_t st) {
   // 1000, but 11.1 for 10.2 at 2000; 4 x 7 heads of 64 in bf16 5.3 for 8.4 and 6.6
   // for 9.5.  And while all run at once: 56 clusters, which do not, took 14.1 for
   // 10.0.
-  p.cluster = a.table_width * a.c.page_tokens <= 2 * kCluster * kWarps * C::kT &&
+  int64_t most = a.table_width * a.c.page_tokens;  // tokens that are seen
+  if (a.window && most > (int64_t)a.window + a.sinks) most = (int64_t)a.window + a.sinks;
+  p.cluster = most <= 2 * kCluster * kWarps * C::kT &&
                       a.B * p.VH <= resident_clusters<T, D, kI8, kBlocks>()
                   ? kCluster
                   : 0;

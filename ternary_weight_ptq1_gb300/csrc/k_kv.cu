@@ -17,21 +17,13 @@
 // Measured, a write and a read together, in CUDA graphs: 33,001 x 4 x 256, bf16, 82 us
 // (98% of the copy rate); 8192 x 8 x 128, bf16 through int8, 25 us (61%); 64 x 8 x 128,
 // fp32 through int8, 4.0 us, the launches.
-#include <cuda_bf16.h>
-#include <float.h>
-
-#include "ptq_internal.cuh"
+#include "kv_row.cuh"
 
 namespace ptq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kVec = 8;  // values a thread holds of a row
-
-struct Geometry {
-  int pages_slots;  // pages * page_tokens
-  Divider page_tokens, heads;
-};
+using Geometry = CacheGeometry;
 
 // Row r of T heads rows: head fastest, then token.
 struct RowId {
@@ -45,12 +37,6 @@ __device__ __forceinline__ RowId row_id(int64_t r, const Geometry& g) {
   }
   const int64_t t = r / g.heads.d;
   return {t, (int)(r - t * g.heads.d)};
-}
-
-// The row of the cache that (slot, h) names, in units of rows.
-__device__ __forceinline__ int64_t cache_row(int slot, int h, const Geometry& g) {
-  const int page = g.page_tokens(slot), p = slot - page * g.page_tokens.d;
-  return ((int64_t)page * g.heads.d + h) * g.page_tokens.d + p;
 }
 
 template <Act T>
@@ -71,11 +57,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t e, float (&x)[kVec]
   }
 }
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 template <Act T>
 __device__ __forceinline__ void store8(void* p, int64_t e, const float (&x)[kVec]) {
   if constexpr (T == Act::F32) {
@@ -86,16 +67,6 @@ __device__ __forceinline__ void store8(void* p, int64_t e, const float (&x)[kVec
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) =
         make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
   }
-}
-
-// round_half_even(x / s) for |x| <= 127 s, given r near 1 / s: x r is within
-// 1e-4 of the quotient, and where that leaves the rounding open (or r is not
-// finite) the division decides.
-__device__ __forceinline__ int code_of(float x, float s, float r) {
-  const float t = x * r;
-  float n = rintf(t);
-  if (!(fabsf(t - n) < 0.4999f)) n = rintf(x / s);
-  return (int)n;
 }
 
 template <Act T, int D, bool kI8>
@@ -125,36 +96,8 @@ __global__ void __launch_bounds__(kThreads)
     if constexpr (!kI8) {
       if (ok) store8<Act::BF16>(to, row * D + e, x[n]);
     } else {
-      float m = 0.0f;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        m = fmaxf(m, fabsf(x[n][i]));
-        bad |= !(fabsf(x[n][i]) < __int_as_float(0x7f800000));
-      }
-      if (bad) m = __int_as_float(0x7f800000);  // fmaxf drops NaN: a non-finite row is infinite
-#pragma unroll
-      for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
-      const bool finite = m < __int_as_float(0x7f800000);
-      const float s = finite ? m / 127.0f : __int_as_float(0x7fc00000);
-      uint32_t w[2] = {0, 0};
-      if (s > 0.0f) {  // a row of zeros (or of values whose scale underflows) keeps zero codes
-        // A scale of few bits is rounded by up to half of itself, and the row's
-        // largest values may pass 127 s: their codes are 127.  (The smallest bf16
-        // value, 2^16 units, gives a scale of 516: at most 127.2 of it.)
-        if constexpr (T == Act::F32) {
-          if (__builtin_expect(s < FLT_MIN, 0)) {
-            asm volatile("");  // a branch: as selections they take 3% of the write's time
-            const float lim = 127.0f * s;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) x[n][i] = fminf(fmaxf(x[n][i], -lim), lim);
-          }
-        }
-        const float inv = 1.0f / s;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          w[i >> 2] |= ((uint32_t)code_of(x[n][i], s, inv) & 0xffu) << (8 * (i & 3));
-      }
+      uint32_t w[2];
+      const float s = quantise<kLanes, T == Act::F32>(x[n], w);  // (bf16 rows stay within 127 as they are)
       if (ok) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to) + row * D + e) = make_uint2(w[0], w[1]);
         if (e == 0) (n ? vs : ks)[row] = s;

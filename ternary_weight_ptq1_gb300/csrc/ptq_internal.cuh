@@ -247,7 +247,32 @@ struct KvRows {
 cudaError_t launch_kv_write(const ptq_kv_cache& c, const KvRows& r, cudaStream_t st);
 cudaError_t launch_kv_read(const ptq_kv_cache& c, const KvRows& r, cudaStream_t st);
 
-// Attention of one new token over a paged cache (k_attn_decode.cu).
+// Head norms and position rotation (k_rope.cu): q and k into q_out and k_out, or,
+// given a cache, k (and v as it is) into its slots.
+struct RopeArgs {
+  const void *q, *k, *v;                 // T x Hq, Hkv, Hkv heads
+  int64_t q_stride, k_stride, v_stride;  // elements from a token to the next
+  void *q_out, *k_out;
+  int64_t qo_stride, ko_stride;
+  const int32_t* slots;
+  void *ck, *cv;
+  float *ks, *vs;
+  const float* inv_freq;
+  const int8_t* axis;
+  const int32_t* pos;
+  int64_t pos_stride;
+  int axes, rotary;
+  bool near;
+  const float *q_gain, *k_gain;
+  float eps;
+  int64_t T;
+  int Hq, Hkv;
+  Act t;
+};
+cudaError_t launch_rope(const RopeArgs& a, const ptq_kv_cache* c, int64_t D, cudaStream_t st);
+
+// Attention of one new token over a paged cache (k_attn_decode.cu), over all its
+// tokens or (window > 0) the last `window` and the first `sinks` of them.
 struct DecodeArgs {
   const void* q;
   int64_t q_stride;
@@ -260,6 +285,7 @@ struct DecodeArgs {
   int64_t B, Hq;
   float scale;
   Act t;
+  int window, sinks;
 };
 cudaError_t launch_attn_decode(const DecodeArgs& a, void* ws, cudaStream_t st);
 size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
@@ -278,6 +304,23 @@ struct PrefillArgs {
 cudaError_t launch_attn_prefill(const PrefillArgs& a, void* ws, cudaStream_t st);
 size_t attn_prefill_workspace(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv,
                               int64_t D);
+
+// Attention of chunks of new tokens over their pages (k_attn_chunk.cu), bf16.
+struct ChunkArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  ptq_kv_cache c;
+  const int32_t* table;
+  int64_t table_width;
+  const int32_t *lens, *cu_q;
+  uint16_t* out;
+  float* lse;
+  int64_t B, Tq, Hq;
+  float scale;
+  int window, sinks;  // window 0: all tokens
+};
+cudaError_t launch_attn_chunk(const ChunkArgs& a, void* ws, cudaStream_t st);
+size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D);
 
 // 3-D TMA tensor map over a tokens x heads x D array of 16-bit values, tokens
 // `stride` elements apart: boxes of 64 columns x box_heads x box_tokens, rows
