@@ -1,112 +1,278 @@
 // k_attn_chunk.cu -- attention of chunks of new tokens over their paged
-// key-value cache, all of it or a sliding window and the first tokens.
+// key-value cache, all of it or a sliding window and the first tokens, on the
+// 5th-generation tensor cores.
 //
-//   s_j = scale q . k_j,  p_j = 2^(s_j log2(e) - m),  out = sum_j p_j v_j / sum_j p_j
+//   S = Q K^T,  P = 2^(S scale log2(e) - m),  O = P V,  out = O / sum P
 //
-// over the tokens j <= p of the query's position p, with a window those with
-// p - window < j or j < sinks.  A warp a query row: 32 keys at a time, a lane's
-// own key for the scores and its own columns for the output.
+// over the tokens j <= p of a query's position p, with a window those with
+// p - window < j or j < sinks.
+//
+// Keys.  The tokens that some query of a Q tile sees are counted through: the
+// first `sinks`, then those of the window, so first tokens share a tile of 128
+// keys with others and hidden ones cost nothing.  Four warps copy a tile's rows out of
+// the pages (cp.async, a lane finds the page of a row): any page size packs full
+// tiles, and rows that are not there are zeros.  Over int8 each copies codes to a
+// place of its own and spreads them to bf16 for the products, which is exact; a
+// score is then multiplied by its key's scale and a probability by its value's, in
+// fp32, before P is rounded to bf16.
+//
+// Tile.  128 rows of Q are tpt tokens of hg query heads that share a kv head.  S, P
+// and O live in TMEM as in the kernel of whole prompts: P goes back over S as bf16
+// and is the A operand of the second product; the maximum that it refers to moves
+// when a row's grows by more than 2^8.  A CTA works on two S at a time (head_dim up
+// to 128): of two Q tiles, neighbours in the sequence, that share each K and V
+// tile; or, where a sequence's queries fill one, of the one tile over every other
+// tile of keys, with an O each that are added at the end.  At head_dim 256 the
+// one tile's S has two buffers.
+//
+// Work.  Runs of queries (the CTA's Q tiles) times head blocks, in order, cost
+// their keys and a start of kLead; each CTA gets an equal stretch of that order,
+// cut at tiles of keys: one long context spreads over all SMs, ragged batches end
+// together.  The lengths are on the device: every CTA adds them up (in closed form
+// for a sequence) and one of its warps walks its stretch.  A run that is cut
+// leaves its sums, relative to their maxima, in the workspace, and a second kernel
+// joins them in order.
+//
+// A key that a row does not see has P = 0, and 0 times a non-finite value is NaN.
+// Over int8 a row is not finite by its scale: such scales enter as 0, and rows that
+// see one are made NaN.  Over bf16 rows whose sum is finite and whose output is not
+// are looked at, and computed again where no value that they see explains it.
+//
+// Every wait is bounded, to some 6 s in which no warp computes rows again; one that
+// runs out raises the device status word and the CTA drains what it has in flight and
+// exits.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "attn_row.cuh"
+#include "attn_tc.cuh"
 #include "ptq_internal.cuh"
 
 namespace ptq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kCtas = (int)kSms;
+constexpr int kLead = 256;   // cost of a run's start, in keys
+constexpr int kScales = 8;   // tiles whose scales are in shared memory
 
-__device__ __forceinline__ int clamped(int v, int hi) { return min(max(v, 0), hi); }
+template <int D, bool kI8>
+struct Cfg {
+  static constexpr int kTiles = D == 256 ? 1 : 2;    // Q tiles of a CTA
+  // A K or V tile passes through the ring in one unit, or two: K by columns,
+  // V by keys, as the products use them up.
+  static constexpr int kUnits = D == 256 ? 2 : 1;
+  static constexpr int kCols = D / kUnits;           // columns of a K unit
+  static constexpr int kVKeys = kKeys / kUnits;      // keys of a V unit
+  static constexpr int kUnit = kKeys * kCols * 2;    // bytes
+  static constexpr int kRing = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
+  // Units on their way: copies are waited for this many units later (bf16), or land in
+  // this many places (int8).
+  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 6 : 3);
+  static constexpr int kStage = kI8 ? kUnit / 2 : 0;
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
+  static constexpr int kThreads = 32 * (kSoftmax + 8);  // four to feed, four others
+  // Registers a thread.  Two Q tiles: 512 threads get 128 each at launch (65,536
+  // in all); 256 softmax threads take 168, 128 that feed keep 96 and 128 others
+  // 80 (65,536).  One: 384 get 168 (64,512); 128 take 232, 128 keep 128, 128 keep
+  // 104 (59,392).
+  static constexpr int kRegsSoftmax = kTiles == 2 ? 168 : 232;
+  static constexpr int kRegsFeed = kTiles == 2 ? 96 : 128;
+  static constexpr int kRegsOther = kTiles == 2 ? 80 : 104;
+  static constexpr int kOffRing = kTiles * kQ;
+  static constexpr int kOffStage = kOffRing + kRing * kUnit;
+  // int8: K and V scales of each tile, and a bit for each V scale that is not finite;
+  // and scales of 1
+  static constexpr int kOffScale = kOffStage + kAhead * kStage;
+  static constexpr int kOffOdd = kOffScale + (kI8 ? kScales * 2 * kKeys * 4 : 0);
+  static constexpr int kOffOnes = kOffOdd + (kI8 ? kScales * 16 : 0);
+  static constexpr int kOffBar = kOffOnes + (kI8 ? kKeys * 4 : 0);
+  // full[kRing] empty[kRing] q[2] q free[2] s[2] p[2][2] o[2] o free[2] pv[2] turn[2]
+  // item full[2] item empty[2] sums full, empty, scales[kScales], done
+  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + kScales + 1;
+  static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
+  static constexpr int kOffSums = kOffItem + 2 * 64;  // (maximum, sum) of the second half's rows
+  static constexpr int kOffBad = kOffSums + (kTiles == 2 ? kRows * 8 : 0);
+  static constexpr int kOffMisc = kOffBad + 4 * 16 * 4;
+  static constexpr int kSmem = kOffMisc + 16;
+};
+static_assert(Cfg<128, false>::kSmem <= 227 * 1024 && Cfg<256, false>::kSmem <= 227 * 1024 &&
+                  Cfg<128, true>::kSmem <= 227 * 1024 && Cfg<256, true>::kSmem <= 227 * 1024, "shared memory");
+// The scales of a tile stay until its P is written: its V is released after that.  When the
+// copies of K tile j are issued the units before the last kRing + kAhead are released: all up to
+// V tile j - kScales at least.
+static_assert(2 * (kScales - 1) >= Cfg<64, true>::kRing + Cfg<64, true>::kAhead + 1 &&
+                  4 * (kScales - 2) >= Cfg<256, true>::kRing + Cfg<256, true>::kAhead + 1, "scales");
+static_assert(Cfg<64, true>::kAhead <= 15 && Cfg<64, false>::kAhead <= 15, "kinds of 16 units");
 
-// Eight consecutive values of a cached row, in fp32 (int8: times its scale).
+// A run that is cut: what the second kernel joins.
+struct Note {
+  int64_t row;  // first query and head of the run, among Tq Hq rows
+  int tokens;   // 0: none
+  int slot;     // of its first part, in its CTA; the others' is 0
+  int last;     // CTA of its last part
+  int pad[3];
+};
+
+struct Args {
+  ChunkArgs a;
+  int G, hg, tpt;  // query heads of a kv head; heads and tokens of a Q tile
+  int heads;       // head blocks in all
+  int run;         // queries of an item: the Q tiles' tokens
+  int part_rows;   // rows of a part
+  Divider by_G, by_hg, by_run;
+  float* part;     // [CTA][2][part_rows][D] output sums
+  float2* ml;      // [CTA][2][part_rows], the maximum and sum they refer to
+  Note* note;      // [CTA]
+};
+
+// A CTA's next piece of work: the Q tiles of one run and head block, over tiles
+// of the keys that the run sees.  b < 0: no more.
+struct Item {
+  int b, q0, nq, first;  // the sequence, its first query's row, its queries, the run's first
+  int h, hq0;            // kv head, first query head
+  int nk;                // cached tokens of the sequence
+  int skip, nv;          // tokens hidden after the first `sinks`; tokens that the run sees
+  int t0, tiles;         // this part's tiles
+  int n[2];              // tiles of each Q tile, or (split) of each half
+  int split;             // one Q tile, its key tiles dealt out to both S
+  int slot;              // part of the workspace; -1: the whole run
+};
+static_assert(sizeof(Item) <= 64, "its place in shared memory");
+
+// ---- the order of the work -----------------------------------------------------------
+
+struct Seq {
+  int q0, nq, nk;
+};
+__device__ __forceinline__ Seq seq_of(const ChunkArgs& a, int b) {
+  const int Tq = (int)a.Tq;
+  const int64_t most = a.table_width * a.c.page_tokens;
+  const int n = __ldg(a.lens + b);
+  const int q0 = clamped(__ldg(a.cu_q + b), Tq), q1 = clamped(__ldg(a.cu_q + b + 1), Tq);
+  return {q0, max(0, q1 - q0), n < 0 ? 0 : n > most ? (int)most : n};
+}
+
+// The sum of max(0, at + i step) for i < n, where step n < 2^31.
+__device__ __forceinline__ int64_t ramp(const Args& p, int64_t at, int n) {
+  if (n <= 0 || at + (int64_t)p.run * (n - 1) <= 0) return 0;
+  const int i0 = at > 0 ? 0 : p.by_run((int)-at) + 1;
+  const int64_t k = n - i0, first = at + (int64_t)i0 * p.run;
+  return k * first + p.run * (k * (k - 1) / 2);
+}
+
+__device__ __forceinline__ int runs_of(const Args& p, int nq) { return p.by_run(nq + p.run - 1); }
+
+// The cost of the first r runs of a sequence.
+__device__ __forceinline__ int64_t cost_of(const Args& p, const Seq& s, int r) {
+  const int64_t base = (int64_t)s.nk - s.nq;
+  int64_t sum = (int64_t)kLead * r + ramp(p, base + p.run, r);
+  if (r > 0 && (int64_t)r * p.run > s.nq) sum -= (int64_t)r * p.run - s.nq;  // the last run is shorter
+  if (p.a.window) sum -= ramp(p, base + 1 - p.a.window - p.a.sinks, r);
+  return sum;
+}
+
+// Tokens that run r sees, and those hidden after the first ones.
+__device__ __forceinline__ int tokens_of(const Args& p, const Seq& s, int r, int* skip) {
+  const int end = max(0, s.nk - s.nq + min((r + 1) * p.run, s.nq));
+  const int from = max(0, s.nk - s.nq + r * p.run + 1);
+  *skip = p.a.window ? max(0, max(0, from - p.a.window) - p.a.sinks) : 0;
+  return end - *skip;
+}
+
+// The first tile of a run (of n, which begins at unit `start`) that is not before unit u.
+__device__ __forceinline__ int tile_at(int64_t u, int64_t start, int n) {
+  const int64_t k = u - start - kLead;
+  return k <= 0 ? 0 : (int)min((int64_t)n, (k + kKeys - 1) / kKeys);
+}
+
+// ---- rows again ------------------------------------------------------------------------
+
+// Eight consecutive values of a cached row, in fp32 (int8: codes).
 template <bool kI8>
-__device__ __forceinline__ void row8(const void* p, int64_t e, float scale, float (&x)[8]) {
+__device__ __forceinline__ void row8(const void* p, int64_t e, float (&x)[8]) {
   if constexpr (kI8) {
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + e));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3))) * scale;
+    for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
   } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    load_bf16(static_cast<const uint16_t*>(p) + e, x);
   }
 }
 
+// A lane's D / 32 columns of a cached row.
 template <int D, bool kI8>
-__global__ void __launch_bounds__(32 * kWarps) attn_chunk_kernel(ChunkArgs a) {
+__device__ __forceinline__ void columns(const void* p, int64_t row, int lane, float (&x)[D / 32]) {
   constexpr int N = D / 32;
-  pdl_release();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (r >= a.Tq * a.Hq) return;
-  const int t = (int)(r / a.Hq), hq = (int)(r - (int64_t)t * a.Hq);
-  const int Tq = (int)a.Tq, ps = (int)a.c.page_tokens, heads = (int)a.c.kv_heads;
-  const int h = hq / (int)(a.Hq / heads);
-  int lo = 0, hi = (int)a.B;  // the last sequence that begins at t or before
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (clamped(__ldg(a.cu_q + mid), Tq) <= t) lo = mid; else hi = mid;
+  if constexpr (kI8) {
+    const int8_t* q = static_cast<const int8_t*>(p) + row * D + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = (float)__ldg(q + i);
+  } else {
+    load_bf16(static_cast<const uint16_t*>(p) + row * D + lane * N, x);
   }
-  const int q0 = clamped(__ldg(a.cu_q + lo), Tq), q1 = clamped(__ldg(a.cu_q + lo + 1), Tq);
-  if (t < q0 || t >= q1) return;
-  const int64_t most = a.table_width * ps;
-  const int n = __ldg(a.lens + lo);
-  const int len = n < 0 ? 0 : n > most ? (int)most : n;
-  const int p = len - q1 + t, end = max(0, p + 1);
-  const int from = a.window ? max(0, end - a.window) : 0;
-  const int skip = max(0, from - a.sinks), seen = end - skip;
+}
+
+// What a row sees of its run's tokens v: v < end and (v >= from or v < sinks).
+struct Sight {
+  int end, from, sinks;
+  __device__ __forceinline__ bool sees(int v) const { return v < end && (v >= from || v < sinks); }
+};
+
+// The row of the cache of the run's token v; -1: its page is none.
+__device__ __forceinline__ int64_t cached_row(const ChunkArgs& a, const Item& it, int v) {
+  const unsigned ps = (unsigned)a.c.page_tokens, j = (unsigned)v + (v >= a.sinks ? it.skip : 0);
+  const int page = __ldg(a.table + it.b * a.table_width + j / ps);
+  if ((unsigned)page >= (unsigned)a.c.pages) return -1;
+  return ((int64_t)page * a.c.kv_heads + it.h) * ps + j % ps;
+}
+
+// One query row by a warp over the run's tokens [v0, v1): 32 keys at a time, a
+// lane's own key for the scores and its own columns for the output.  Where the
+// weights' sum is large the sums of values near the largest overflow although
+// their mean does not: then again with weights 2^-40 times as large.
+template <int D, bool kI8>
+__device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t row, Sight sight, int v0, int v1,
+                                        float* part, float2* ml) {
+  constexpr int N = D / 32;
+  const ChunkArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = row / a.Hq;
+  const uint16_t* q = a.q + t * a.q_stride + (row - t * a.Hq) * D;
   RowState<D> s;
   float l, small = 1.0f;
-  // The weights' sum may be large, and the sums of values near the largest overflow
-  // although their mean does not: then again with smaller weights.
-  for (int again = 0; again < 2; ++again) {
+#pragma unroll 1
+  for (;;) {
     s = RowState<D>();
-    for (int j0 = 0; j0 < seen; j0 += 32) {
-      int64_t row = -1;
-      bool bad = false;
-      int j = j0 + lane;
-      if (j < seen) {
-        j += j >= a.sinks ? skip : 0;
-        const int page = __ldg(a.table + (int64_t)lo * a.table_width + j / ps);
-        bad = (unsigned)page >= (unsigned)a.c.pages;
-        if (!bad) row = ((int64_t)page * heads + h) * ps + j % ps;
-      }
-      float x = kNegInf, vs = 0.0f;
-      if (row >= 0) {
+#pragma unroll 1
+    for (int v = v0; v < min(v1, sight.end); v += 32) {
+      const int mine = v + lane;
+      const bool in = mine < v1 && sight.sees(mine);
+      const int64_t at = in ? cached_row(a, it, mine) : -1;
+      float x = in ? __int_as_float(0x7fc00000) : kNegInf, vs = 1.0f;
+      if (at >= 0) {
         x = 0.0f;
+#pragma unroll 2
         for (int d = 0; d < D; d += 8) {
-          float kx[8], qx[8];
-          row8<kI8>(a.c.k, row * D + d, 1.0f, kx);
-          row8<false>(a.q, t * a.q_stride + (int64_t)hq * D + d, 1.0f, qx);
+          float k[8], y[8];
+          row8<kI8>(a.c.k, at * D + d, k);
+          row8<false>(q, d, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x = fmaf(kx[i], qx[i], x);
+          for (int i = 0; i < 8; ++i) x = fmaf(k[i], y[i], x);
         }
-        if constexpr (kI8) {
-          x *= __ldg(a.c.k_scale + row);
-          vs = __ldg(a.c.v_scale + row);
-        }
+        if constexpr (kI8) x *= __ldg(a.c.k_scale + at), vs = __ldg(a.c.v_scale + at);
         x *= a.scale * kLog2e;
       }
-      if (bad) x = __int_as_float(0x7fc00000);
-      const float w = s.weigh(x);
-      for (int i = 0; i < min(32, seen - j0); ++i) {
-        const float wi = __shfl_sync(~0u, w, i), si = __shfl_sync(~0u, vs, i);
-        const int64_t ri = __shfl_sync(~0u, row, i);
-        if (ri < 0) continue;
+      const float w = s.weigh(x) * (small * vs);
+#pragma unroll 1
+      for (unsigned left = __ballot_sync(~0u, at >= 0); left; left &= left - 1) {
+        const int e = __ffs(left) - 1;
+        const float we = __shfl_sync(~0u, w, e);
+        float y[N];
+        columns<D, kI8>(a.c.v, __shfl_sync(~0u, at, e), lane, y);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          float v;
-          if constexpr (kI8)
-            v = (float)static_cast<const int8_t*>(a.c.v)[ri * D + lane * N + e] * si;
-          else
-            v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.c.v)[ri * D + lane * N + e] << 16);
-          s.o[e] = fmaf(wi * small, v, s.o[e]);
-        }
+        for (int i = 0; i < N; ++i) s.o[i] = fmaf(we, y[i], s.o[i]);
       }
     }
     l = s.l;
@@ -114,35 +280,1130 @@ __global__ void __launch_bounds__(32 * kWarps) attn_chunk_kernel(ChunkArgs a) {
     for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
     bool fine = true;
 #pragma unroll
-    for (int e = 0; e < N; ++e) fine = fine && fabsf(s.o[e]) < -kNegInf;
-    if (!(l == l) || __all_sync(~0u, fine) || again) break;
+    for (int i = 0; i < N; ++i) fine = fine && fabsf(s.o[i]) < -kNegInf;
+    if (small != 1.0f || !(l == l) || __all_sync(~0u, fine)) break;
     small = 0x1p-40f;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / small / l;
+  if (part) {
+    if (lane == 0) *ml = make_float2(small == 1.0f ? s.m : s.m + 40.0f, l * small);
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    a.out[r * D + lane * N + e] = __bfloat16_as_ushort(__float2bfloat16_rn(l == l ? s.o[e] * inv : l));
-  if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? kNegInf : s.m * kLn2 + logf(l);
+    for (int i = 0; i < N; ++i) part[lane * N + i] = s.o[i];
+  } else {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * small);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      a.out[row * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(s.o[i] * inv));
+  }
+}
+
+// Whether a row whose sum is finite and whose output is not has to be computed
+// again.  A value that it sees and that is not finite leaves its column so, rightly;
+// not so a column that has none, but one among the hidden tokens of the row's tiles
+// [v0, v1) (0 times it is NaN), and an output that no value explains (P may be 2^8 times
+// a probability, and the sums of large values overflow).
+template <int D>
+__device__ __noinline__ bool spoilt(const Args& p, const Item& it, Sight sight, int v0, int v1) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  unsigned hid = 0, known = 0;  // of this lane's columns
+  auto look = [&](int v, unsigned& found) {
+    const int64_t at = cached_row(p.a, it, v);
+    float y[N];
+    if (at >= 0) {
+      columns<D, false>(p.a.c.v, at, lane, y);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(fabsf(y[i]) < -kNegInf)) found |= 1u << i;
+    }
+  };
+#pragma unroll 4
+  for (int v = max(v0, sight.end); v < v1; ++v) look(v, hid);
+#pragma unroll 4
+  for (int v = max(v0, min(sight.sinks, sight.end)); v < min(v1, min(sight.from, sight.end)); ++v) look(v, hid);
+  const bool any_hid = __any_sync(~0u, hid);
+#pragma unroll 1
+  for (int v = v0; v < min(v1, sight.end); v += 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (v + e < v1 && sight.sees(v + e)) look(v + e, known);
+    if (any_hid ? !__any_sync(~0u, hid & ~known) : __any_sync(~0u, known)) return false;
+  }
+  return true;
+}
+
+template <int D, bool kI8>
+__device__ __noinline__ void repair(const Args& p, const Item& it, unsigned again, int64_t row, Sight sight, int v0,
+                                    int v1, float* part, float2* ml, volatile int* state) {
+  const Busy busy(state);
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int who = __ffs(again) - 1;
+    const Sight s{__shfl_sync(~0u, sight.end, who), __shfl_sync(~0u, sight.from, who), sight.sinks};
+    const int64_t r = __shfl_sync(~0u, row, who);
+    float* to = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(part), who));
+    float2* mt = reinterpret_cast<float2*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(ml), who));
+    if constexpr (!kI8)
+      if (!spoilt<D>(p, it, s, v0, v1)) continue;
+    attend_row<D, kI8>(p, it, r, s, v0, v1, to, mt);
+  }
+}
+
+// ---- copies ------------------------------------------------------------------------------
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two of the four int8 codes of x as bf16: under the exponent of 128 a byte's low
+// seven bits are 128 + them and its top bit is 128 or 256, and their difference is the
+// code.
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t codes(uint32_t x) {
+  const uint32_t w = __byte_perm(x, 0x43434343u, kSel), a = w & 0xff7fff7fu, b = w & 0xff80ff80u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// The weight of sums with maximum m and sum l among sums of maximum top.
+// l = 0: no key.  m = -inf with l != 0: NaN scores.
+__device__ __forceinline__ float weight(float m, float l, float top) {
+  return l == 0.0f ? 0.0f : m == kNegInf ? 1.0f : exp2_fast(m - top);
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) {  // n below 0: none, above 32: all
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+}
+
+template <int D, bool kI8>
+__global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
+    attn_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ Args p, int* status) {
+  using C = Cfg<D, kI8>;
+  constexpr int kTiles = C::kTiles;
+  constexpr bool kAfter = kTiles == 2;  // the next S goes where P was
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  // ring units; of a Q tile: Q there, Q read; of a slot: S written, the first and
+  // second half of P written; of a Q tile: O final, O read, a product with V
+  // done (not where S's arrival says it), its turn to issue; items there, read; the
+  // second half's sums there, read; a tile's scales there
+  uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing, *q_free = q_full + 2;
+  uint64_t *s_full = q_free + 2, *p_full = s_full + 2, *o_full = p_full + 4,
+           *o_free = o_full + 2, *pv_done = o_free + 2, *turn = pv_done + 2, *item_full = turn + 2,
+           *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 1,
+           *scales = ml_free + 1, *all_done = scales + kScales;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* state = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+
+  const ChunkArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kFeed = C::kSoftmax, kMma = kFeed + 4, kPlan = kMma + kTiles, kWarps = C::kThreads / 32;
+
+  pdl_release();
+  pdl_wait();
+
+  // ---- this CTA's stretch of the work, [u0, u1), and the sequence that it begins in ------
+  int64_t u0, u1, per, seq_start = 0;
+  int seq = -1;
+  {
+    int64_t* scan = reinterpret_cast<int64_t*>(smem);  // (the places of Q, not yet used)
+    int64_t mine = 0;
+    auto cost = [&](int64_t b) {
+      if (b >= a.B) return (int64_t)0;
+      const Seq s = seq_of(a, (int)b);
+      return cost_of(p, s, runs_of(p, s.nq)) * p.heads;
+    };
+    for (int64_t b = threadIdx.x; b < a.B; b += C::kThreads) mine += cost(b);
+    int64_t incl = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t o = __shfl_up_sync(~0u, incl, i);
+      if (lane >= i) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    if (threadIdx.x == 0) p.note[blockIdx.x].tokens = 0;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    per = (total + gridDim.x - 1) / gridDim.x;
+    per = (per + kKeys - 1) / kKeys * kKeys;
+    u0 = blockIdx.x * per;
+    u1 = min(u0 + per, total);
+    if (u0 >= total) return;
+    int64_t* found = scan + kWarps;  // sequence, its start
+    if (a.B <= C::kThreads) {
+      const int64_t start = before + incl - mine;
+      if (u0 >= start && u0 < start + mine) found[0] = threadIdx.x, found[1] = start;
+    } else {
+      for (int64_t b0 = 0, base = 0;; b0 += C::kThreads) {
+        const int64_t one = cost(b0 + threadIdx.x);
+        int64_t upto = one;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+          const int64_t o = __shfl_up_sync(~0u, upto, i);
+          if (lane >= i) upto += o;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        int64_t start = base + upto - one;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) start += scan[w];
+          base += scan[w];
+        }
+        if (u0 >= start && u0 < start + one) found[0] = b0 + threadIdx.x, found[1] = start;
+        if (u0 < base) break;
+      }
+    }
+    __syncthreads();
+    seq = (int)found[0];
+    seq_start = found[1];
+    __syncthreads();
+  }
+
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == kFeed && lane == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(full + i, 4);  // the four warps that feed
+      mbar_init(empty + i, kTiles);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_free + i, kTiles);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + 2 * i, 4);  // the four softmax warps of a tile
+      mbar_init(p_full + 2 * i + 1, 4);
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, 4);
+      mbar_init(pv_done + i, 1);
+      mbar_init(turn + i, 1);
+      mbar_init(item_full + i, 1);
+      mbar_init(item_free + i, 4 + kTiles + C::kSoftmax);  // every warp that reads items
+    }
+    mbar_init(ml_full, 4);
+    mbar_init(ml_free, 4);
+    for (int i = 0; i < kScales; ++i) mbar_init(scales + i, 4);
+    mbar_init(all_done, kTiles);
+    *state = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if constexpr (kI8) {
+    if (threadIdx.x < kKeys) reinterpret_cast<float*>(smem + C::kOffOnes)[threadIdx.x] = 1.0f;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t ring = smem_addr(smem + C::kOffRing), qs = smem_addr(smem);
+  bool ok = true;
+
+  int seen = 0;  // items read
+  auto item_ready = [&] { return mbar_test(item_full + (seen & 1), (seen >> 1) & 1); };
+  auto read_item = [&](Item& it) {
+    ok = __all_sync(~0u, bar_wait(item_full + (seen & 1), (seen >> 1) & 1, state));
+    if (!ok) return false;
+    const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
+    int* to = reinterpret_cast<int*>(&it);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = from[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_free + (seen & 1));
+    ++seen;
+    return it.b >= 0;
+  };
+  if (warp >= kMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+  if (warp == kPlan) {
+    // ---- the items of this CTA, one ahead of their use, and their Q tiles -----------------
+    int qn[kTiles] = {};  // Q tiles loaded
+    Seq s = seq_of(a, seq);
+    int64_t each = cost_of(p, s, runs_of(p, s.nq));
+    int hb = (int)((u0 - seq_start) / each), r = 0;
+    int64_t start = seq_start + hb * each;  // of the run
+    {  // the last run that begins at u0 or before
+      int lo = 0, hi = runs_of(p, s.nq);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (start + cost_of(p, s, mid) <= u0) lo = mid; else hi = mid;
+      }
+      r = lo;
+      start += cost_of(p, s, r);
+    }
+    while (ok) {
+      Item it;
+      it.b = -1;
+      while (start < u1) {
+        if (r * (int64_t)p.run >= s.nq) {  // the next head block, or sequence with queries
+          r = 0;
+          if (++hb == p.heads) {
+            hb = 0;
+            for (++seq;; seq += 32) {
+              const bool some = seq + lane < a.B && seq_of(a, seq + lane).nq > 0;
+              const unsigned which = __ballot_sync(~0u, some);
+              if (which) {
+                seq += __ffs(which) - 1;
+                break;
+              }
+              if (seq + 32 >= a.B) break;  // (start is u1 before that)
+            }
+            s = seq_of(a, min(seq, (int)a.B - 1));
+          }
+        }
+        it.nv = tokens_of(p, s, r, &it.skip);
+        const int n = (it.nv + kKeys - 1) / kKeys;
+        it.t0 = tile_at(u0, start, n);
+        const int t1 = tile_at(u1, start, n);
+        const int64_t begin = start;
+        const int this_run = r++;
+        start += kLead + it.nv;
+        if (it.t0 >= t1 && !(n == 0 && begin >= u0)) continue;
+        it.b = seq;
+        it.q0 = s.q0, it.nq = s.nq, it.nk = s.nk;
+        it.first = this_run * p.run;
+        it.hq0 = hb * p.hg;
+        it.h = p.by_G(it.hq0);
+        it.tiles = t1 - it.t0;
+        it.split = kTiles == 2 && it.first + p.tpt >= it.nq;
+        it.slot = it.tiles == n ? -1 : begin < u0 ? 0 : 1;
+        if (kTiles == 1) {
+          it.n[0] = it.tiles, it.n[1] = 0;
+        } else if (it.split) {
+          it.n[0] = (it.tiles + 1) / 2, it.n[1] = it.tiles / 2;
+        } else {
+          const int v = it.nk - it.nq + it.first + p.tpt - it.skip;  // what the first tile's last query sees
+          const int n0 = v > 0 ? (v + kKeys - 1) / kKeys : 0;
+          it.n[0] = max(0, min(n0 - it.t0, it.tiles)), it.n[1] = it.tiles;
+        }
+        if (it.slot >= 0 && it.t0 == 0 && lane == 0) {
+          Note note;
+          note.row = (int64_t)(it.q0 + it.first) * a.Hq + it.hq0;
+          note.tokens = min(p.run, it.nq - it.first);
+          note.slot = it.slot;
+          note.last = (int)((begin + kLead + (int64_t)(n - 1) * kKeys) / per);
+          p.note[blockIdx.x] = note;
+        }
+        break;
+      }
+      if (seen >= 2)
+        ok = __all_sync(~0u, bar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, state));
+      if (!ok) break;
+      if (lane == 0) {
+        volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
+        const int* from = reinterpret_cast<const int*>(&it);
+#pragma unroll
+        for (int e = 0; e < (int)(sizeof(Item) / 4); ++e) to[e] = from[e];
+        mbar_arrive(item_full + (seen & 1));
+      }
+      __syncwarp();
+      ++seen;
+      if (it.b < 0) break;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        if (it.n[t] == 0 || (t == 1 && it.split)) continue;
+        const int y = it.q0 + it.first + t * p.tpt;
+        if (lane < D / 64) tma_3d_prefetch(&map_q, 64 * lane, it.hq0, y);
+        if (qn[t] > 0) ok = ok && __all_sync(~0u, bar_wait(q_free + t, (qn[t] - 1) & 1, state));
+        if (!ok) break;
+        ++qn[t];
+        if (lane == 0) {
+          mbar_expect_tx(q_full + t, (uint32_t)(p.hg * p.tpt * D * 2));
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c)
+            tma_3d(qs + t * C::kQ + c * kRows * 128, &map_q, 64 * c, it.hq0, y, q_full + t);
+        }
+        __syncwarp();
+      }
+    }
+    for (int t = 0; t < kTiles; ++t)  // the copies land before the CTA ends
+      if (qn[t] > 0) static_cast<void>(mbar_wait(q_full + t, (qn[t] - 1) & 1, nullptr));
+  } else if (warp >= kFeed && warp < kMma) {
+    // ---- K and V tiles through the ring in the order of their use: K_0 V_0 K_1 V_1 ..., or
+    // with one Q tile K_0 K_1 V_0 K_2 V_1 ...  A warp has 32 keys of each tile (lane l
+    // key 64 (l / 16) + 16 w + l % 16: 16 of each half), of a V unit of 64 keys 16 ------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFeed));
+    constexpr int kRowBytes = D * (kI8 ? 1 : 2);       // of a cached row
+    constexpr int kSrcCols = C::kCols * (kI8 ? 1 : 2);  // bytes of a row in a K unit
+    const int w = warp - kFeed;
+    const int key = 64 * (lane >> 4) + 16 * w + (lane & 15);
+    const uint32_t stage = smem_addr(smem + C::kOffStage) + w * (C::kStage / 4);
+    uint32_t* bads = reinterpret_cast<uint32_t*>(smem + C::kOffBad) + 16 * w;
+    int u = 0, f = 0;     // units issued, units handed over
+    uint32_t kinds = 0;   // of the last 16 units: 1 V, 2 its second unit
+    int tiles_in = 0, tiles_out = 0;  // K tiles issued, handed over
+    int64_t rows[2];      // this lane's row of the cache in tiles j and j - 1 (those whose V is to come)
+    // Of the unit's rows, idx / chunks is the row of this warp and idx % chunks the piece.
+    auto issue = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
+      const int at16 = u & 15;
+      kinds = (kinds & ~(3u << (2 * at16))) | ((v ? 1u : 0u) | (k ? 2u : 0u)) << (2 * at16);
+      const char* base = static_cast<const char*>(v ? a.c.v : a.c.k) + (v ? 0 : k * kSrcCols);
+      if constexpr (kI8) {
+        const uint32_t to = stage + (u % C::kAhead) * C::kStage;
+        if (!v && k == 0) {
+          const int slot = tiles_in & (kScales - 1);
+          const uint32_t sc = smem_addr(smem + C::kOffScale) + slot * (2 * kKeys * 4) + 4 * key;
+          copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
+          copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
+        }
+        auto go = [&](auto chunks_c, int row0) {
+          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
+#pragma unroll
+          for (int i = 0; i < kIts; ++i) {
+            const int64_t src = __shfl_sync(~0u, row, row0 + (i * 32 + lane) / kChunks);
+            copy16(to + (i * 32 + lane) * 16, base + (src < 0 ? 0 : src) * kRowBytes + (lane % kChunks) * 16, src >= 0);
+          }
+        };
+        if (D == 256 && v)
+          go(std::integral_constant<int, D / 16>(), 16 * k);
+        else
+          go(std::integral_constant<int, C::kCols / 16>(), 0);
+      } else {
+        const int st = u % C::kRing;
+        if (u >= C::kRing) ok = ok && __all_sync(~0u, bar_wait(empty + st, (u / C::kRing - 1) & 1, state));
+        if (!ok) return;
+        const uint32_t to = ring + st * C::kUnit;
+        auto go = [&](auto chunks_c, int row0, int unit_rows) {
+          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kUnit / 4 / 512;
+#pragma unroll
+          for (int i = 0; i < kIts; ++i) {
+            const int rl = row0 + (i * 32 + lane) / kChunks, c = lane % kChunks;
+            const int64_t src = __shfl_sync(~0u, row, rl);
+            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
+            copy16(to + (c >> 3) * unit_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   base + (src < 0 ? 0 : src) * kRowBytes + c * 16, src >= 0);
+          }
+        };
+        if (D == 256 && v)
+          go(std::integral_constant<int, D / 8>(), 16 * k, C::kVKeys);
+        else
+          go(std::integral_constant<int, C::kCols / 8>(), 0, kKeys);
+      }
+      if (!v && k == 0) {
+        const unsigned any = __ballot_sync(~0u, bad);
+        if (lane == 0) bads[at16] = any;
+        ++tiles_in;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++u;
+    };
+    // Unit f has landed (its group has been waited for): to the tensor core.
+    auto hand_over = [&] {
+      const int at16 = f & 15, st = f % C::kRing;
+      const bool v = kinds >> (2 * at16) & 1, second = kinds >> (2 * at16) & 2;
+      const uint32_t to = ring + st * C::kUnit;
+      __syncwarp();
+      if constexpr (kI8) {
+        if (f >= C::kRing) ok = ok && __all_sync(~0u, bar_wait(empty + st, (f / C::kRing - 1) & 1, state));
+        if (!ok) return;
+        const uint32_t from = stage + (f % C::kAhead) * C::kStage;
+        auto go = [&](auto chunks_c, int unit_rows) {
+          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
+#pragma unroll
+          for (int i = 0; i < kIts; ++i) {
+            const int rl = (i * 32 + lane) / kChunks, c = lane % kChunks;
+            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
+            uint32_t x[4], y[8];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(from + (i * 32 + lane) * 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[2 * e] = codes<0x4140>(x[e]), y[2 * e + 1] = codes<0x4342>(x[e]);
+            // Pieces 2 c and 2 c + 1 of the row; lanes of the upper half of 128 bytes write the second
+            // first, so that eight lanes together use all banks.
+            const bool swap = c & 4;
+            const int c0 = 2 * c + swap, c1 = 2 * c + !swap;
+            const uint32_t at = to + r * 128;
+            const uint32_t d0 = at + (c0 >> 3) * unit_rows * 128 + (((c0 & 7) ^ (r & 7)) << 4),
+                           d1 = at + (c1 >> 3) * unit_rows * 128 + (((c1 & 7) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d0), "r"(swap ? y[4] : y[0]),
+                         "r"(swap ? y[5] : y[1]), "r"(swap ? y[6] : y[2]), "r"(swap ? y[7] : y[3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d1), "r"(swap ? y[0] : y[4]),
+                         "r"(swap ? y[1] : y[5]), "r"(swap ? y[2] : y[6]), "r"(swap ? y[3] : y[7])
+                         : "memory");
+          }
+        };
+        if (D == 256 && v)
+          go(std::integral_constant<int, D / 16>(), C::kVKeys);
+        else
+          go(std::integral_constant<int, C::kCols / 16>(), kKeys);
+        if (!v && !second) {  // this lane's scales
+          const int slot = tiles_out & (kScales - 1);
+          float* sc = reinterpret_cast<float*>(smem + C::kOffScale) + slot * 2 * kKeys + key;
+          if (bads[at16] >> lane & 1) sc[0] = __int_as_float(0x7fc00000);
+          const bool odd = !(fabsf(sc[kKeys]) < -kNegInf);
+          if (odd) sc[kKeys] = 0.0f;
+          const unsigned odds = __ballot_sync(~0u, odd);
+          uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kOffOdd + slot * 16);
+          if ((lane & 15) == 0) mask[4 * (lane >> 4) + w] = (uint16_t)(odds >> lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scales + slot);
+        }
+      } else if (!v && !second && bads[at16]) {  // a key of no page: its scores are NaN
+        if (bads[at16] >> lane & 1)
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + key * 128 + ((key & 7) << 4)), "h"((short)0x7fc0) : "memory");
+      }
+      if (!v && !second) ++tiles_out;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + st);
+      ++f;
+    };
+    auto next = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
+      issue(v, k, row, bad, it);
+      if (ok && u - f == C::kAhead) {
+        copies_but<C::kAhead - 1>();
+        hand_over();
+      }
+    };
+    auto drain = [&] {
+      copies_but<0>();
+      while (ok && f < u) hand_over();
+    };
+    Item it;
+    for (;;) {
+      if (f < u && !__all_sync(~0u, item_ready())) drain();
+      if (!ok || !read_item(it)) break;
+      const int n = it.tiles;
+      bool bad = false;
+      auto find = [&](int j) {  // this lane's row of tile j
+        const int v = (it.t0 + j) * kKeys + key;
+        bad = false;
+        if (v >= it.nv) return (int64_t)-1;
+        const int64_t row = cached_row(a, it, v);
+        bad = row < 0;
+        return row;
+      };
+#pragma unroll 1
+      for (int j = 0; j < n + (kTiles == 1) && ok; ++j) {
+        if (j < n) {
+          rows[1] = rows[0];
+          rows[0] = find(j);
+#pragma unroll
+          for (int k = 0; k < C::kUnits; ++k)
+            if (ok) next(false, k, rows[0], bad, it);
+        } else {
+          rows[1] = rows[0];
+        }
+        if (kTiles == 1 && j == 0) continue;
+#pragma unroll
+        for (int k = 0; k < C::kUnits; ++k)
+          if (ok) next(true, k, rows[kTiles == 1], false, it);
+      }
+      if (!ok) break;
+    }
+    if (ok) drain();
+    copies_but<0>();  // whatever becomes of the MMAs, the copies land before the CTA ends
+  } else if (warp >= kMma && warp < kMma + kTiles) {
+    // ---- MMAs.  The warp stays converged and an elected lane issues each product
+    // in straight-line code; with two Q tiles each has an issuing warp of its own, and
+    // one waits for barriers while the other's MMAs run ----------------------------------
+    const int s = warp - kMma;
+    auto wait = [&](uint64_t* bar, int phase) {
+      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, state));
+    };
+    // of the items before: units in the ring, tiles of this S, rounds of turns, outputs of
+    // this S, Q tiles loaded
+    unsigned units = 0;
+    int done = 0, rounds = 0, outs = 0, qn[2] = {};
+    Item it;
+    while (read_item(it)) {
+      const int tiles = s ? it.n[1] : it.n[0], theirs = s ? it.n[0] : it.n[1];
+      if (it.tiles == 0) continue;
+      const bool split = kTiles == 2 && it.split;
+      const int most = split ? tiles : max(tiles, theirs), q_at = split ? 0 : s;
+      qn[0] += split || it.n[0] > 0;
+      qn[1] += !split && it.n[1] > 0;
+      auto slot_of = [&](int j) { return kTiles == 1 ? (done + j) & 1 : s; };
+      auto use_of = [&](int j) { return kTiles == 1 ? (done + j) >> 1 : done + j; };
+      // the first ring unit of this S's K or V tile j
+      auto k_unit = [&](int j) {
+        return units + (kTiles == 1 ? 2 * (j ? 2 * j - 1 : 0) : split ? 4 * j + 2 * s : 2 * j);
+      };
+      auto v_unit = [&](int j) {
+        return units + (kTiles == 1 ? 2 * (j + 1 < tiles ? 2 * j + 2 : 2 * j + 1) : split ? 4 * j + 2 * s + 1 : 2 * j + 1);
+      };
+      auto place = [&](unsigned x) { return (int)(x % C::kRing); };
+      auto landed = [&](unsigned x) { wait(full + place(x), (int)(x / C::kRing)); };
+      // A K or V tile that the other S does not use is released for both.
+      auto release = [&](int j, int st) {
+        mma_commit(empty + st);
+        if (kTiles == 2 && (split || j >= theirs)) mma_commit(empty + st);
+      };
+      // S of tile j into its slot
+      auto scores = [&](int j) {
+        const int slot = slot_of(j);
+        if (j == 0) wait(q_full + q_at, qn[q_at] - 1);
+#pragma unroll
+        for (int k = 0; k < C::kUnits; ++k) {  // by columns
+          const unsigned x = k_unit(j) + k;
+          landed(x);
+          fence_after();
+          if (ok && elected()) {
+            const uint32_t qd = tile_desc(qs + q_at * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
+            const uint32_t kd = tile_desc(ring + place(x) * C::kUnit, 16);
+#pragma unroll
+            for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int o = c * (kRows * 128 / 16) + 2 * e;
+                if (k == 0 && c == 0 && e == 0)
+                  mma_ss<false>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
+                else
+                  mma_ss<true>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
+              }
+            release(j, place(x));
+            if (k == C::kUnits - 1) {
+              mma_commit(s_full + slot);
+              if (j == tiles - 1) {
+                mma_commit(q_free + q_at);
+                if (kTiles == 2 && (!split || theirs == 0)) mma_commit(q_free + q_at);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      };
+      // A barrier tells one phase from the next, not from the one after: who does not use
+      // a Q tile or a unit waits for it all the same, at most kRing units apart.
+      if (split) wait(q_full, qn[0] - 1);
+      if (!kAfter) scores(0);
+#pragma unroll 1
+      for (int j = kAfter ? -1 : 0; j < most && ok; ++j) {
+        const bool mine = j >= 0 && j < tiles, more = j + 1 < tiles;
+        if (!kAfter && more) scores(j + 1);
+        // O += P V, over the first and second 64 keys
+        const int slot = slot_of(j), use = use_of(j);
+        const unsigned v = v_unit(j);
+        if (mine) {
+#pragma unroll
+          for (int k = 0; k < C::kUnits; ++k) landed(v + k);
+          if (j == 0 && outs > 0) wait(o_free + s, outs - 1);
+        }
+        // (not where S have each their own tiles: K may wait for V's release)
+        if (kAfter && !split && j >= 0 && more) landed(k_unit(j + 1));
+#pragma unroll
+        for (int half = 0; half < 2 && j >= 0; ++half) {
+          if (mine) wait(p_full + 2 * slot + half, use);
+          // Two Q tiles take turns: issued side by side their MMAs would alternate,
+          // both S would arrive together and the tensor core would stand still
+          // during both softmaxes.
+          if (kAfter && half == 0 && !split) {
+            const int t = rounds + j - (s == 0);
+            if (t >= 0) wait(turn + s, t);
+          }
+          if (!mine) break;
+          fence_after();
+          if (ok && elected()) {
+            const int st = place(v + (C::kUnits == 2 ? half : 0));
+            const uint32_t pa = tmem + slot * kKeys + 32 * half;
+            const uint32_t d = tmem + 2 * kKeys + s * D;
+            const uint32_t vd = tile_desc(ring + st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
+                                          C::kVKeys * 128);
+            if (half > 0 || j > 0)
+              mma_ts<true>(d, pa, vd, idesc<D, true>());
+            else
+              mma_ts<false>(d, pa, vd, idesc<D, true>());
+#pragma unroll
+            for (int e = 1; e < 4; ++e)  // 16 keys: 8 columns of P, 2048 bytes of V
+              mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
+            if (half == 1 || C::kUnits == 2) release(j, st);
+            if (half == 1) {
+              if (kTiles == 1) mma_commit(pv_done + s);
+              if (j == tiles - 1) mma_commit(o_full + s);
+            }
+          }
+          __syncwarp();
+        }
+        if (kAfter && more) scores(j + 1);
+        if (kAfter && !split && j >= 0 && ok && lane == 0) mbar_arrive(turn + 1 - s);
+      }
+      if (kTiles == 2) landed(units + 2 * it.tiles - 1);
+      if (!ok) break;
+      done += tiles;
+      if (!split) rounds += most;
+      outs += tiles > 0;
+      units += 2 * C::kUnits * it.tiles;
+    }
+    if (elected()) mma_commit(all_done);
+    __syncwarp();
+  } else if (warp < C::kSoftmax) {
+    // ---- softmax: thread = row of its S; then the output, O over its sum -----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    const int s = kTiles == 1 ? 0 : warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int row = 32 * quarter + lane;
+    const float scale2 = a.scale * kLog2e;
+    const uint32_t o_at = tmem + lanes + 2 * kKeys;
+    // this row's token of the tile, and those of the warp's first and last row
+    const int my_tok = p.by_hg(row), tok_lo = p.by_hg(32 * quarter), tok_hi = p.by_hg(32 * quarter + 31);
+    const int my_head = row - my_tok * p.hg;
+    const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    float2* sums = reinterpret_cast<float2*>(smem + C::kOffSums);
+    int done = 0, fed = 0, outs[2] = {}, joins = 0;  // of the items before: tiles of this S, all tiles, outputs, sums
+    Item it;
+    while (read_item(it)) {
+      const bool split = kTiles == 2 && it.split;
+      const int tiles = s ? it.n[1] : it.n[0], first = it.first + (split ? 0 : s * p.tpt);
+      // What the row of token t sees of the run's tokens.
+      auto sight_of = [&](int t) {
+        const int end = max(0, it.nk - it.nq + min(first + t, it.nq - 1) + 1);  // (no more than the last query)
+        Sight x;
+        x.sinks = a.sinks;
+        x.from = a.window ? max(0, end - a.window) - it.skip : 0;
+        x.end = end - it.skip;
+        return x;
+      };
+      const Sight sight = sight_of(my_tok), lowest = sight_of(tok_lo), highest = sight_of(tok_hi);
+      const bool mine = row < p.hg * p.tpt && first + my_tok < it.nq;
+      const bool idle = first + tok_lo >= it.nq || 32 * quarter >= p.hg * p.tpt;  // no row of the warp is one
+      float m = kNegInf;  // what P refers to, in units of log2
+      bool ready = false, odd = false;
+      uint64_t sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int g = done + i, slot = kTiles == 1 ? g & 1 : s, use = kTiles == 1 ? g >> 1 : g;
+        const int j = split ? 2 * i + s : i;  // of the part's tiles
+        const uint32_t at = tmem + lanes + slot * kKeys;
+        ok = __all_sync(~0u, ready || bar_wait(s_full + slot, use & 1, state));
+        if (!ok) break;
+        if (idle) {
+          if (lane == 0) {
+            mbar_arrive(p_full + 2 * slot);
+            mbar_arrive(p_full + 2 * slot + 1);
+          }
+          ready = false;
+          continue;
+        }
+        const int v0 = (it.t0 + j) * kKeys;
+        const float* ks = nullptr;
+        const float* vs = nullptr;
+        if constexpr (kI8) {
+          const int sc = (fed + j) & (kScales - 1);
+          ok = __all_sync(~0u, bar_wait(scales + sc, ((fed + j) / kScales) & 1, state));
+          if (!ok) break;
+          ks = reinterpret_cast<const float*>(smem + C::kOffScale) + sc * 2 * kKeys;
+          vs = ks + kKeys;
+          const uint4 om = *reinterpret_cast<const uint4*>(smem + C::kOffOdd + sc * 16);
+          if (__builtin_expect(om.x | om.y | om.z | om.w, 0)) {
+            const uint32_t o[4] = {om.x, om.y, om.z, om.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int x = v0 + 32 * c;
+              odd |= (o[c] & low_bits(sight.end - x) & (~low_bits(sight.from - x) | low_bits(sight.sinks - x))) != 0;
+            }
+          }
+        }
+        fence_after();
+        const int left_hi = highest.end - v0;
+        if (__builtin_expect(lowest.end - v0 < kKeys || (highest.from > v0 && sight.sinks - v0 < kKeys), 0)) {
+          // Keys that a row does not see, in TMEM: a loop that fits the instruction cache.
+#pragma unroll 1
+          for (int c = 0; c < (left_hi > 64 ? kKeys : 64); c += 32) {
+            const int x0 = v0 + c;
+            const uint32_t in = low_bits(sight.end - x0) & (~low_bits(sight.from - x0) | low_bits(sight.sinks - x0));
+            if (!kI8 && __all_sync(~0u, in == ~0u)) continue;
+            uint32_t x[32];
+            tmem_ld32(at + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if constexpr (kI8) x[e] = __float_as_uint(__uint_as_float(x[e]) * ks[c + e]);
+              if (!(in >> e & 1)) x[e] = 0xff800000u;
+            }
+            tmem_st32(at + c, x);
+          }
+          tmem_wait_st();
+          if constexpr (kI8) ks = reinterpret_cast<const float*>(smem + C::kOffOnes);
+        }
+        // The second 64 columns are read twice, for the maximum and again for their
+        // exponentials: 128 values held beside P's do not fit the registers.
+        uint32_t v[64];
+        auto read_s = [&](uint32_t* to, int c0) {
+          tmem_ld32(at + c0, to);
+          tmem_ld32(at + c0 + 32, to + 32);
+        };
+        auto scaled = [&](uint32_t* x, int c0) {  // scores of int8 codes
+          if constexpr (kI8) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(ks + c0 + e);
+              float y0, y1;
+              unpair(mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair(k.x, k.y)), y0, y1);
+              x[e] = __float_as_uint(y0), x[e + 1] = __float_as_uint(y1);
+              unpair(mul2(pair(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), pair(k.z, k.w)), y0, y1);
+              x[e + 2] = __float_as_uint(y0), x[e + 3] = __float_as_uint(y1);
+            }
+          }
+        };
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        auto take_max = [&](const uint32_t* x) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        };
+        {
+          uint32_t second[64];
+          read_s(v, 0);
+          read_s(second, 64);
+          tmem_wait_ld();
+          scaled(v, 0);
+          take_max(v);
+          if (left_hi > 64) {
+            scaled(second, 64);
+            take_max(second);
+          }
+        }
+        const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
+        if (i == 0) {
+          m = t2;
+        } else if (__builtin_expect(__any_sync(~0u, t2 > m + kSlack), 0)) {
+          // O moves to the new maximum once the product with the tile before is
+          // done (where S follows P, S says so)
+          if constexpr (!kAfter) {
+            ok = __all_sync(~0u, bar_wait(pv_done + s, (g - 1) & 1, state));
+            if (!ok) break;
+          }
+          const float mn = t2 > m + kSlack ? t2 : m;
+          const float f = m == kNegInf ? 0.0f : exp2_fast(m - mn);
+          m = mn;
+          fence_after();
+          float lo, hi;
+          unpair(sum2[0], lo, hi);
+          sum2[0] = pair(lo * f, hi * f);
+          unpair(sum2[1], lo, hi);
+          sum2[1] = pair(lo * f, hi * f);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + s * D + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(o_at + s * D + c, o);
+          }
+        }
+        const float z = m == kNegInf ? 0.0f : -m;
+        const uint64_t zz = pair(z, z), ss = pair(scale2, scale2);
+        auto half_p = [&](int half) {  // of v
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x0, x1;
+            unpair(fma2(pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ss, zz), x0, x1);
+            x0 = exp2_fast(x0);
+            x1 = exp2_fast(x1);
+            sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
+            if constexpr (kI8) {
+              const float2 w = *reinterpret_cast<const float2*>(vs + 64 * half + 2 * e);
+              unpair(mul2(pair(x0, x1), pair(w.x, w.y)), x0, x1);
+            }
+            x[e] = bf16x2(x0, x1);
+          }
+          tmem_st32(at + 32 * half, x);
+        };
+        auto publish = [&](int half) {
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 2 * slot + half);
+        };
+        // The product with V starts on the first half.
+        half_p(0);
+        publish(0);
+        {  // whether the next S has arrived: asked now, used at the top
+          const int ng = g + 1, nslot = kTiles == 1 ? ng & 1 : s, nuse = kTiles == 1 ? ng >> 1 : ng;
+          ready = i + 1 < tiles && mbar_test(s_full + nslot, nuse & 1);
+        }
+        if (left_hi > 64) {
+          read_s(v, 64);
+          tmem_wait_ld();
+          scaled(v, 64);
+          half_p(1);
+        } else {
+          const uint32_t none[32] = {};
+          tmem_st32(at + 32, none);
+        }
+        publish(1);
+      }
+      if (!ok) break;
+      done += tiles;
+      fed += it.tiles;
+
+      // ---- the output -------------------------------------------------------------------
+      float l;
+      {
+        float lo, hi;
+        unpair(add2(sum2[0], sum2[1]), lo, hi);
+        l = lo + hi;
+      }
+      const bool two = split && it.n[1] > 0;  // both O are one run's
+      if (two && s == 1) {
+        if (joins > 0) ok = __all_sync(~0u, bar_wait(ml_free, (joins - 1) & 1, state));
+        if (!ok) break;
+        sums[row] = make_float2(m, odd ? -l : l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full);
+      }
+      if ((split && s == 1) || (!split && first >= it.nq)) {
+        outs[0] += it.n[0] > 0, outs[1] += it.n[1] > 0, joins += two;
+        continue;
+      }
+      float w0 = 1.0f, w1 = 0.0f, l1 = 0.0f;
+      const float l0 = l;
+      if (two) {
+        ok = __all_sync(~0u, bar_wait(ml_full, joins & 1, state));
+        if (!ok) break;
+        const float2 other = sums[row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_free);
+        odd |= other.y < 0.0f;
+        l1 = fabsf(other.y);
+        const float top = fmaxf(m, other.x);
+        w0 = weight(m, l0, top), w1 = weight(other.x, l1, top);
+        l = l0 * w0 + l1 * w1;
+        m = top;
+      }
+      const int t = first + my_tok;
+      const int64_t out_row = (int64_t)(it.q0 + t) * a.Hq + it.hq0 + my_head;
+      const bool parts = it.slot >= 0;
+      const int64_t part_row = ((int64_t)blockIdx.x * 2 + max(0, it.slot)) * p.part_rows + (split ? 0 : s * kRows) + row;
+      if (mine) {
+        if (parts)
+          p.ml[part_row] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[out_row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * kLn2;
+      }
+      if (!parts) {
+        const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+        w0 *= inv, w1 *= inv;
+      }
+      if (l0 == 0.0f) w0 = 0.0f;
+      const int o_mine = split ? 0 : s;  // the O that this warp reads first
+      const bool has0 = (o_mine ? it.n[1] : it.n[0]) > 0;
+      if (has0) ok = __all_sync(~0u, bar_wait(o_full + o_mine, outs[o_mine] & 1, state));
+      if (two) ok = ok && __all_sync(~0u, bar_wait(o_full + 1, outs[1] & 1, state));
+      if (!ok) break;
+      fence_after();
+      uint64_t checked = pair(0.0f, 0.0f);
+      if (!idle) {
+        char* to = parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D);
+        const uint64_t ww0 = pair(w0, w0), ww1 = pair(w1, w1), zero2 = pair(0.0f, 0.0f);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16], o1[16];
+          if (has0) tmem_ld16(o_at + o_mine * D + c, o);
+          if (two) tmem_ld16(o_at + D + c, o1);
+          tmem_wait_ld();
+          if (w0 == 0.0f || !has0) {  // without a key O may be anything
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          }
+          if (w1 == 0.0f || !two) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o1[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            uint64_t y = mul2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ww0);
+            if (two) y = fma2(pair(__uint_as_float(o1[e]), __uint_as_float(o1[e + 1])), ww1, y);
+            checked = fma2(y, zero2, checked);  // 0 as long as every value is finite
+            float y0, y1;
+            unpair(y, y0, y1);
+            if (odd) y0 = y1 = __int_as_float(0x7fc00000);
+            o[e] = __float_as_uint(y0), o[e + 1] = __float_as_uint(y1);
+          }
+          if (!mine) continue;
+          if (parts) {
+            store32(to, o, true);
+            store32(to + 32, o + 8, true);
+            to += 64;
+          } else {
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            store32(to, y, aligned32);
+            to += 32;
+          }
+        }
+      }
+      // the next item's products may come
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (has0) mbar_arrive(o_free + o_mine);
+        if (two) mbar_arrive(o_free + 1);
+      }
+      outs[0] += it.n[0] > 0, outs[1] += it.n[1] > 0, joins += two;
+      // rows whose sum is finite and whose output is not
+      float lo, hi;
+      unpair(checked, lo, hi);
+      const unsigned again = __ballot_sync(~0u, mine && !odd && !(lo + hi == 0.0f) && l == l);
+      if (__builtin_expect(again, 0)) {
+        __syncwarp();
+        const int n = split ? it.tiles : s ? it.n[1] : it.n[0];
+        const Item copy = it;  // (its address is taken: `it` stays in registers)
+        repair<D, kI8>(p, copy, again, out_row, sight, it.t0 * kKeys, min(it.nv, (it.t0 + n) * kKeys),
+                       parts ? p.part + part_row * D : nullptr, p.ml + part_row, state);
+      }
+    }
+  }
+  if (!ok) {
+    if (lane == 0) atomicOr(const_cast<int*>(state), kAborted);
+    if (lane == 0) atomicOr(status, kDevTimeout);
+  }
+  if ((*state & kAborted) && warp == kMma && lane == 0) static_cast<void>(mbar_wait(all_done, 0, nullptr));
+  fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// Joins the parts of the run that begins in CTA blockIdx.x and goes on in the CTAs
+// after it, in their order: a warp a row.
+constexpr int kJoinCtas = 8;
+template <int D>
+__global__ void __launch_bounds__(256) attn_chunk_join_kernel(Args p) {
+  constexpr int N = D / 32;
+  pdl_release();
+  pdl_wait();
+  const ChunkArgs& a = p.a;
+  const Note note = p.note[blockIdx.x];
+  const int lane = threadIdx.x & 31, parts = note.last - (int)blockIdx.x + 1;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < note.tokens * p.hg; r += 8 * kJoinCtas) {
+    const int t = p.by_hg(r), head = r - t * p.hg;
+    const int tile = t / p.tpt, in_part = tile * kRows + (t - tile * p.tpt) * p.hg + head;
+    auto row_of = [&](int i) {
+      return ((int64_t)(blockIdx.x + i) * 2 + (i ? 0 : note.slot)) * p.part_rows + in_part;
+    };
+    float top = kNegInf;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.ml[row_of(i)].x);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+    float l = 0.0f;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 ml = p.ml[row_of(i)];
+      l += ml.y * weight(ml.x, ml.y, top);
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float o[N] = {};
+    for (int i0 = 0; i0 < parts; i0 += 32) {  // the weights of 32 parts, a lane each
+      float w = 0.0f;
+      if (i0 + lane < parts) {
+        const float2 ml = p.ml[row_of(i0 + lane)];
+        w = weight(ml.x, ml.y, top) * inv;
+        if (ml.y == 0.0f) w = -1.0f;  // no key: its sums were not written
+      }
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(~0u, w, i);
+        const float* from = p.part + row_of(i0 + i) * D + lane * N;
+        float x[N];
+        if constexpr (N == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(from);
+          x[0] = v.x, x[1] = v.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + e);
+            x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (wi != -1.0f) o[e] = fmaf(wi, x[e], o[e]);
+      }
+    }
+    const int64_t row = note.row + (int64_t)t * a.Hq + head;
+    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? kNegInf : top * kLn2 + logf(l);
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      *reinterpret_cast<uint32_t*>(a.out + row * D + lane * N + i) = bf16x2(o[i], o[i + 1]);
+  }
+}
+
+struct Plan {
+  int hg, tpt, part_rows;
+};
+
+Plan plan_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D) {
+  Plan r;
+  const int tiles = D == 256 ? 1 : 2;
+  r.hg = heads_of_tile(Hq / Hkv, B, Tq, tiles);
+  r.tpt = kRows / r.hg;
+  r.part_rows = Tq <= r.tpt ? (int)Tq * r.hg : tiles * kRows;  // one tile, as far as it is filled
+  return r;
+}
+
+size_t workspace_of(const Plan& r, int64_t D) {
+  return (size_t)kCtas * (2 * (size_t)r.part_rows * (size_t)(D * 4 + 8) + sizeof(Note)) + 768;
+}
+
+template <int D, bool kI8>
+cudaError_t launch(const ChunkArgs& a, void* ws, cudaStream_t st) {
+  using C = Cfg<D, kI8>;
+  const Plan plan = plan_of(a.B, a.Tq, a.Hq, a.c.kv_heads, D);
+  const int64_t G = a.Hq / a.c.kv_heads;
+  Args p{a, (int)G, plan.hg, plan.tpt, (int)(a.c.kv_heads * (G / plan.hg)), C::kTiles * plan.tpt, plan.part_rows,
+         Divider(G), Divider(plan.hg), Divider(C::kTiles * plan.tpt), nullptr, nullptr, nullptr};
+  auto up = [](void* q) { return (reinterpret_cast<uintptr_t>(q) + 255) & ~(uintptr_t)255; };
+  const size_t rows = (size_t)kCtas * 2 * plan.part_rows;
+  p.part = reinterpret_cast<float*>(up(ws));
+  p.ml = reinterpret_cast<float2*>(up(p.part + rows * D));
+  p.note = reinterpret_cast<Note*>(up(p.ml + rows));
+  CUtensorMap mq;
+  cudaError_t e = encode_tma_heads(&mq, a.q, D, a.Hq, a.Tq, a.q_stride, p.hg, p.tpt);
+  if (e != cudaSuccess) return e;
+  int* status = device_status_ptr();
+  if (!status) return cudaErrorInvalidDevice;
+  auto kern = attn_chunk_kernel<D, kI8>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(kCtas), dim3(C::kThreads), C::kSmem, st, mq, p, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_chunk_join_kernel<D>, dim3(kCtas, kJoinCtas), dim3(256), 0, st, p);
 }
 
 template <bool kI8>
-cudaError_t by_dim(const ChunkArgs& a, cudaStream_t st) {
-  const int64_t ctas = (a.Tq * a.Hq + kWarps - 1) / kWarps;
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)ctas), block(32 * kWarps);
+cudaError_t by_dim(const ChunkArgs& a, void* ws, cudaStream_t st) {
   switch (a.c.head_dim) {
-    case 64: return launch_pdl(attn_chunk_kernel<64, kI8>, grid, block, 0, st, a);
-    case 128: return launch_pdl(attn_chunk_kernel<128, kI8>, grid, block, 0, st, a);
-    default: return launch_pdl(attn_chunk_kernel<256, kI8>, grid, block, 0, st, a);
+    case 64: return launch<64, kI8>(a, ws, st);
+    case 128: return launch<128, kI8>(a, ws, st);
+    default: return launch<256, kI8>(a, ws, st);
   }
 }
 
 }  // namespace
 
-size_t attn_chunk_workspace(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (B == 0 || Tq == 0) return 0;
+  return workspace_of(plan_of(B, Tq, Hq, Hkv, D), D);
+}
 
-cudaError_t launch_attn_chunk(const ChunkArgs& a, void*, cudaStream_t st) {
-  return a.c.type == PTQ_KV_I8 ? by_dim<true>(a, st) : by_dim<false>(a, st);
+cudaError_t launch_attn_chunk(const ChunkArgs& a, void* ws, cudaStream_t st) {
+  return a.c.type == PTQ_KV_I8 ? by_dim<true>(a, ws, st) : by_dim<false>(a, ws, st);
 }
 
 }  // namespace ptq
