@@ -66,9 +66,8 @@ struct Cfg {
   static constexpr int kVKeys = kKeys / kUnits;      // keys of a V unit
   static constexpr int kUnit = kKeys * kCols * 2;    // bytes
   static constexpr int kRing = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
-  // Units on their way: copies are waited for this many units later (bf16), or land in
-  // this many places (int8).
-  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 6 : 3);
+  // Units on their way at most (int8: the places that they land in).
+  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : kRing;
   static constexpr int kStage = kI8 ? kUnit / 2 : 0;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
@@ -362,6 +361,16 @@ template <int N>
 __device__ __forceinline__ void copies_but() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// All groups of copies but the last n (or fewer) have landed.
+__device__ __forceinline__ void copies_but(int n) {
+  switch (n) {
+    case 0: return copies_but<0>();
+    case 1: return copies_but<1>();
+    case 2: return copies_but<2>();
+    case 3: return copies_but<3>();
+    default: return copies_but<4>();
+  }
+}
 
 // Two of the four int8 codes of x as bf16: under the exponent of 128 a byte's low
 // seven bits are 128 + them and its top bit is 128 or 256, and their difference is the
@@ -649,60 +658,6 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     uint32_t kinds = 0;   // of the last 16 units: 1 V, 2 its second unit
     int tiles_in = 0, tiles_out = 0;  // K tiles issued, handed over
     int64_t rows[2];      // this lane's row of the cache in tiles j and j - 1 (those whose V is to come)
-    // Of the unit's rows, idx / chunks is the row of this warp and idx % chunks the piece.
-    auto issue = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
-      const int at16 = u & 15;
-      kinds = (kinds & ~(3u << (2 * at16))) | ((v ? 1u : 0u) | (k ? 2u : 0u)) << (2 * at16);
-      const char* base = static_cast<const char*>(v ? a.c.v : a.c.k) + (v ? 0 : k * kSrcCols);
-      if constexpr (kI8) {
-        const uint32_t to = stage + (u % C::kAhead) * C::kStage;
-        if (!v && k == 0) {
-          const int slot = tiles_in & (kScales - 1);
-          const uint32_t sc = smem_addr(smem + C::kOffScale) + slot * (2 * kKeys * 4) + 4 * key;
-          copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
-          copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
-        }
-        auto go = [&](auto chunks_c, int row0) {
-          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
-#pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int64_t src = __shfl_sync(~0u, row, row0 + (i * 32 + lane) / kChunks);
-            copy16(to + (i * 32 + lane) * 16, base + (src < 0 ? 0 : src) * kRowBytes + (lane % kChunks) * 16, src >= 0);
-          }
-        };
-        if (D == 256 && v)
-          go(std::integral_constant<int, D / 16>(), 16 * k);
-        else
-          go(std::integral_constant<int, C::kCols / 16>(), 0);
-      } else {
-        const int st = u % C::kRing;
-        if (u >= C::kRing) ok = ok && __all_sync(~0u, bar_wait(empty + st, (u / C::kRing - 1) & 1, state));
-        if (!ok) return;
-        const uint32_t to = ring + st * C::kUnit;
-        auto go = [&](auto chunks_c, int row0, int unit_rows) {
-          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kUnit / 4 / 512;
-#pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int rl = row0 + (i * 32 + lane) / kChunks, c = lane % kChunks;
-            const int64_t src = __shfl_sync(~0u, row, rl);
-            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
-            copy16(to + (c >> 3) * unit_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                   base + (src < 0 ? 0 : src) * kRowBytes + c * 16, src >= 0);
-          }
-        };
-        if (D == 256 && v)
-          go(std::integral_constant<int, D / 8>(), 16 * k, C::kVKeys);
-        else
-          go(std::integral_constant<int, C::kCols / 8>(), 0, kKeys);
-      }
-      if (!v && k == 0) {
-        const unsigned any = __ballot_sync(~0u, bad);
-        if (lane == 0) bads[at16] = any;
-        ++tiles_in;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      ++u;
-    };
     // Unit f has landed (its group has been waited for): to the tensor core.
     auto hand_over = [&] {
       const int at16 = f & 15, st = f % C::kRing;
@@ -766,9 +721,69 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       if (lane == 0) mbar_arrive(full + st);
       ++f;
     };
+    // Of the unit's rows, idx / chunks is the row of this warp and idx % chunks the piece.
+    auto issue = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
+      const int at16 = u & 15;
+      kinds = (kinds & ~(3u << (2 * at16))) | ((v ? 1u : 0u) | (k ? 2u : 0u)) << (2 * at16);
+      const char* base = static_cast<const char*>(v ? a.c.v : a.c.k) + (v ? 0 : k * kSrcCols);
+      if constexpr (kI8) {
+        const uint32_t to = stage + (u % C::kAhead) * C::kStage;
+        if (!v && k == 0) {
+          const int slot = tiles_in & (kScales - 1);
+          const uint32_t sc = smem_addr(smem + C::kOffScale) + slot * (2 * kKeys * 4) + 4 * key;
+          copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
+          copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
+        }
+        auto go = [&](auto chunks_c, int row0) {
+          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
+#pragma unroll
+          for (int i = 0; i < kIts; ++i) {
+            const int64_t src = __shfl_sync(~0u, row, row0 + (i * 32 + lane) / kChunks);
+            copy16(to + (i * 32 + lane) * 16, base + (src < 0 ? 0 : src) * kRowBytes + (lane % kChunks) * 16, src >= 0);
+          }
+        };
+        if (D == 256 && v)
+          go(std::integral_constant<int, D / 16>(), 16 * k);
+        else
+          go(std::integral_constant<int, C::kCols / 16>(), 0);
+      } else {
+        const int st = u % C::kRing;
+        if (u >= C::kRing) {  // while no place is free, what has landed goes on
+          while (ok && f < u && !__all_sync(~0u, mbar_test(empty + st, (u / C::kRing - 1) & 1))) {
+            copies_but(u - f - 1);
+            hand_over();
+          }
+          ok = ok && __all_sync(~0u, bar_wait(empty + st, (u / C::kRing - 1) & 1, state));
+        }
+        if (!ok) return;
+        const uint32_t to = ring + st * C::kUnit;
+        auto go = [&](auto chunks_c, int row0, int unit_rows) {
+          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kUnit / 4 / 512;
+#pragma unroll
+          for (int i = 0; i < kIts; ++i) {
+            const int rl = row0 + (i * 32 + lane) / kChunks, c = lane % kChunks;
+            const int64_t src = __shfl_sync(~0u, row, rl);
+            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
+            copy16(to + (c >> 3) * unit_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   base + (src < 0 ? 0 : src) * kRowBytes + c * 16, src >= 0);
+          }
+        };
+        if (D == 256 && v)
+          go(std::integral_constant<int, D / 8>(), 16 * k, C::kVKeys);
+        else
+          go(std::integral_constant<int, C::kCols / 8>(), 0, kKeys);
+      }
+      if (!v && k == 0) {
+        const unsigned any = __ballot_sync(~0u, bad);
+        if (lane == 0) bads[at16] = any;
+        ++tiles_in;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++u;
+    };
     auto next = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
       issue(v, k, row, bad, it);
-      if (ok && u - f == C::kAhead) {
+      if (kI8 && ok && u - f == C::kAhead) {
         copies_but<C::kAhead - 1>();
         hand_over();
       }
@@ -842,10 +857,13 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       };
       auto place = [&](unsigned x) { return (int)(x % C::kRing); };
       auto landed = [&](unsigned x) { wait(full + place(x), (int)(x / C::kRing)); };
-      // A K or V tile that the other S does not use is released for both.
-      auto release = [&](int j, int st) {
+      // A K or V tile that the other S does not use is released for both, but for the item's
+      // last: its V both release, so that neither is more than kRing units behind the other or
+      // ahead (a barrier tells one phase from the next, not from the one after).
+      const bool owns_last = split ? ((it.tiles - 1) & 1) == s : tiles == most;
+      auto release = [&](int j, int st, bool v) {
         mma_commit(empty + st);
-        if (kTiles == 2 && (split || j >= theirs)) mma_commit(empty + st);
+        if (kTiles == 2 && (split || j >= theirs) && !(v && owns_last && j == tiles - 1)) mma_commit(empty + st);
       };
       // S of tile j into its slot
       auto scores = [&](int j) {
@@ -869,21 +887,23 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
                 else
                   mma_ss<true>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
               }
-            release(j, place(x));
+            release(j, place(x), false);
             if (k == C::kUnits - 1) {
               mma_commit(s_full + slot);
               if (j == tiles - 1) {
                 mma_commit(q_free + q_at);
-                if (kTiles == 2 && (!split || theirs == 0)) mma_commit(q_free + q_at);
+                if (kTiles == 2 && !split) mma_commit(q_free + q_at);
               }
             }
           }
           __syncwarp();
         }
       };
-      // A barrier tells one phase from the next, not from the one after: who does not use
-      // a Q tile or a unit waits for it all the same, at most kRing units apart.
-      if (split) wait(q_full, qn[0] - 1);
+      if (split && tiles == 0) {  // (it releases the Q tile too, as above)
+        wait(q_full, qn[0] - 1);
+        if (ok && lane == 0) mbar_arrive(q_free);
+        __syncwarp();
+      }
       if (!kAfter) scores(0);
 #pragma unroll 1
       for (int j = kAfter ? -1 : 0; j < most && ok; ++j) {
@@ -924,7 +944,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
 #pragma unroll
             for (int e = 1; e < 4; ++e)  // 16 keys: 8 columns of P, 2048 bytes of V
               mma_ts<true>(d, pa + 8 * e, vd + 128 * e, idesc<D, true>());
-            if (half == 1 || C::kUnits == 2) release(j, st);
+            if (half == 1 || C::kUnits == 2) release(j, st, true);
             if (half == 1) {
               if (kTiles == 1) mma_commit(pv_done + s);
               if (j == tiles - 1) mma_commit(o_full + s);
@@ -935,7 +955,12 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (kAfter && more) scores(j + 1);
         if (kAfter && !split && j >= 0 && ok && lane == 0) mbar_arrive(turn + 1 - s);
       }
-      if (kTiles == 2) landed(units + 2 * it.tiles - 1);
+      if (kTiles == 2 && !owns_last) {
+        const unsigned last = units + 2 * it.tiles - 1;
+        landed(last);
+        if (ok && lane == 0) mbar_arrive(empty + place(last));
+        __syncwarp();
+      }
       if (!ok) break;
       done += tiles;
       if (!split) rounds += most;

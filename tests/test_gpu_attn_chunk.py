@@ -128,6 +128,34 @@ def test_many_sequences_of_few_tokens(P, kv):
     _check(s, q, nq, out, lse, 100, 2)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 40, 8), (256, 24, 4), (64, 28, 4)])
+def test_many_runs_of_every_kind(P, D, Hq, Hkv, kv):
+    """Many runs a CTA, of one Q tile and two, with one tile of keys and several, in any order."""
+    rng = np.random.default_rng(23)
+    lens, nq = [], []
+    for _ in range(60):
+        n = int(rng.choice([1, 2, 20, 30, 55, 77, 130, 260, 300]))
+        nq.append(n)
+        lens.append(max(0, n + int(rng.choice([0, 0, -1, 1, 100, 127, 300, -n // 2]))))
+    s = Paged(P, rng, lens, Hkv, D, 16, kv)
+    q = _values(rng, (sum(nq), Hq, D), "bf16")
+    for window, sinks in ((0, 0), (90, 2)):
+        first = None
+        for _ in range(3):
+            out, lse = _run(P, s, q, nq, window=window, sinks=sinks)
+            assert first is None or ((out == first[0]).all() and (lse == first[1]).all())
+            first = out, lse
+        at = np.concatenate([[0], np.cumsum(nq)])
+        for b in rng.permutation(60)[:12]:
+            k, v = _stored(s.k[b], kv), _stored(s.v[b], kv)
+            hq = int(rng.integers(Hq))
+            i = rng.integers(nq[b], size=3)
+            seen = _sees(lens[b] - nq[b] + i, np.arange(lens[b]), window, sinks)
+            ref = R.attend(q[at[b] + i, hq], k[:, hq * Hkv // Hq], v[:, hq * Hkv // Hq], D ** -0.5, seen)
+            R.check(out[at[b] + i, hq], lse[at[b] + i, hq], ref, True, True, f"seq {b} head {hq}")
+
+
 def test_rows_of_no_sequence_are_left(P):
     rng = np.random.default_rng(6)
     s = Paged(P, rng, [100, 30], 1, 128, 16, "bf16")
