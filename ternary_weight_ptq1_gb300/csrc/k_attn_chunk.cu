@@ -668,37 +668,41 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (f >= C::kRing) ok = ok && __all_sync(~0u, bar_wait(empty + st, (f / C::kRing - 1) & 1, state));
         if (!ok) return;
         const uint32_t from = stage + (f % C::kAhead) * C::kStage;
-        auto go = [&](auto chunks_c, int unit_rows) {
-          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
+        // Eight rows and 64 codes of each at a time: four lanes a row write pieces 0, 2, 4, 6
+        // of 128 bytes, then 1, 3, 5, 7, the rows beside them the others (by the swizzle).
+        auto go = [&](auto quads_c, auto rows_c) {
+          constexpr int kQuads = decltype(quads_c)::value, kUnitRows = decltype(rows_c)::value;
+          constexpr int kIts = C::kStage / 4 / 512, kBatch = 4;
+          const uint32_t at = to + (16 * w + (lane >> 2)) * 128, p0 = ((2 * (lane & 3)) ^ (lane >> 2)) << 4;
 #pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int rl = (i * 32 + lane) / kChunks, c = lane % kChunks;
-            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
-            uint32_t x[4], y[8];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(from + (i * 32 + lane) * 16));
+          for (int i0 = 0; i0 < kIts; i0 += kBatch) {
+            uint32_t x[kBatch][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[2 * e] = codes<0x4140>(x[e]), y[2 * e + 1] = codes<0x4342>(x[e]);
-            // Pieces 2 c and 2 c + 1 of the row; lanes of the upper half of 128 bytes write the second
-            // first, so that eight lanes together use all banks.
-            const bool swap = c & 4;
-            const int c0 = 2 * c + swap, c1 = 2 * c + !swap;
-            const uint32_t at = to + r * 128;
-            const uint32_t d0 = at + (c0 >> 3) * unit_rows * 128 + (((c0 & 7) ^ (r & 7)) << 4),
-                           d1 = at + (c1 >> 3) * unit_rows * 128 + (((c1 & 7) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d0), "r"(swap ? y[4] : y[0]),
-                         "r"(swap ? y[5] : y[1]), "r"(swap ? y[6] : y[2]), "r"(swap ? y[7] : y[3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d1), "r"(swap ? y[0] : y[4]),
-                         "r"(swap ? y[1] : y[5]), "r"(swap ? y[2] : y[6]), "r"(swap ? y[3] : y[7])
-                         : "memory");
+            for (int i = 0; i < kBatch; ++i)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                           : "r"(from + ((i0 + i) * 32 + lane) * 16));
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int g = (i0 + i) / kQuads, block = (i0 + i) % kQuads;  // rows 8 g .. of the warp
+              const uint32_t d = at + block * kUnitRows * 128 + (kUnitRows == kKeys ? 64 * (g >> 1) + 8 * (g & 1) : 8 * g) * 128;
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[2 * e] = codes<0x4140>(x[i][e]), y[2 * e + 1] = codes<0x4342>(x[i][e]);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d + p0), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                           "r"(y[3])
+                           : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d + (p0 ^ 16)), "r"(y[4]), "r"(y[5]), "r"(y[6]),
+                           "r"(y[7])
+                           : "memory");
+            }
           }
         };
+        using std::integral_constant;
         if (D == 256 && v)
-          go(std::integral_constant<int, D / 16>(), C::kVKeys);
+          go(integral_constant<int, D / 64>(), integral_constant<int, C::kVKeys>());
         else
-          go(std::integral_constant<int, C::kCols / 16>(), kKeys);
+          go(integral_constant<int, C::kCols / 64>(), integral_constant<int, kKeys>());
         if (!v && !second) {  // this lane's scales
           const int slot = tiles_out & (kScales - 1);
           float* sc = reinterpret_cast<float*>(smem + C::kOffScale) + slot * 2 * kKeys + key;
@@ -734,18 +738,20 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
           copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
         }
-        auto go = [&](auto chunks_c, int row0) {
-          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kStage / 4 / 512;
+        auto go = [&](auto quads_c, int row0) {
+          constexpr int kQuads = decltype(quads_c)::value, kIts = C::kStage / 4 / 512;
 #pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int64_t src = __shfl_sync(~0u, row, row0 + (i * 32 + lane) / kChunks);
-            copy16(to + (i * 32 + lane) * 16, base + (src < 0 ? 0 : src) * kRowBytes + (lane % kChunks) * 16, src >= 0);
+          for (int g = 0; g < kIts / kQuads; ++g) {
+            const int64_t src = __shfl_sync(~0u, row, row0 + 8 * g + (lane >> 2));
+            const char* from = base + (src < 0 ? 0 : src) * kRowBytes + (lane & 3) * 16;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) copy16(to + ((g * kQuads + q) * 32 + lane) * 16, from + 64 * q, src >= 0);
           }
         };
         if (D == 256 && v)
-          go(std::integral_constant<int, D / 16>(), 16 * k);
+          go(std::integral_constant<int, D / 64>(), 16 * k);
         else
-          go(std::integral_constant<int, C::kCols / 16>(), 0);
+          go(std::integral_constant<int, C::kCols / 64>(), 0);
       } else {
         const int st = u % C::kRing;
         if (u >= C::kRing) {  // while no place is free, what has landed goes on
@@ -757,21 +763,25 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         }
         if (!ok) return;
         const uint32_t to = ring + st * C::kUnit;
-        auto go = [&](auto chunks_c, int row0, int unit_rows) {
-          constexpr int kChunks = decltype(chunks_c)::value, kIts = C::kUnit / 4 / 512;
+        // Four rows and 64 columns of each at a time.
+        auto go = [&](auto octs_c, auto rows_c, int row0) {
+          constexpr int kOcts = decltype(octs_c)::value, kUnitRows = decltype(rows_c)::value;
+          constexpr int kIts = C::kUnit / 4 / 512;
+          const uint32_t at = to + (16 * w + (lane >> 3)) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4;
 #pragma unroll
-          for (int i = 0; i < kIts; ++i) {
-            const int rl = row0 + (i * 32 + lane) / kChunks, c = lane % kChunks;
-            const int64_t src = __shfl_sync(~0u, row, rl);
-            const int r = (unit_rows == kKeys ? 64 * (rl >> 4) : 0) + 16 * w + (rl & 15);
-            copy16(to + (c >> 3) * unit_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                   base + (src < 0 ? 0 : src) * kRowBytes + c * 16, src >= 0);
+          for (int g = 0; g < kIts / kOcts; ++g) {
+            const int64_t src = __shfl_sync(~0u, row, row0 + 4 * g + (lane >> 3));
+            const char* from = base + (src < 0 ? 0 : src) * kRowBytes + (lane & 7) * 16;
+            const uint32_t d = at + (kUnitRows == kKeys ? 64 * (g >> 2) + 4 * (g & 3) : 4 * g) * 128 + (p0 ^ (64 * (g & 1)));
+#pragma unroll
+            for (int o = 0; o < kOcts; ++o) copy16(d + o * kUnitRows * 128, from + 128 * o, src >= 0);
           }
         };
+        using std::integral_constant;
         if (D == 256 && v)
-          go(std::integral_constant<int, D / 8>(), 16 * k, C::kVKeys);
+          go(integral_constant<int, D / 64>(), integral_constant<int, C::kVKeys>(), 16 * k);
         else
-          go(std::integral_constant<int, C::kCols / 8>(), 0, kKeys);
+          go(integral_constant<int, C::kCols / 64>(), integral_constant<int, kKeys>(), 0);
       }
       if (!v && k == 0) {
         const unsigned any = __ballot_sync(~0u, bad);
