@@ -55,6 +55,7 @@ namespace {
 constexpr int kCtas = (int)kSms;
 constexpr int kLead = 256;   // cost of a run's start, in keys
 constexpr int kScales = 8;   // tiles whose scales are in shared memory
+constexpr int kItems = 4;    // items on their way from the warp that plans to the others
 
 template <int D, bool kI8>
 struct Cfg {
@@ -67,7 +68,7 @@ struct Cfg {
   static constexpr int kUnit = kKeys * kCols * 2;    // bytes
   static constexpr int kRing = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
   // Units on their way at most (int8: the places that they land in).
-  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : kRing;
+  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : kRing - 1;
   static constexpr int kStage = kI8 ? kUnit / 2 : 0;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
@@ -88,10 +89,10 @@ struct Cfg {
   static constexpr int kOffOnes = kOffOdd + (kI8 ? kScales * 16 : 0);
   static constexpr int kOffBar = kOffOnes + (kI8 ? kKeys * 4 : 0);
   // full[kRing] empty[kRing] q[2] q free[2] s[2] p[2][2] o[2] o free[2] pv[2] turn[2]
-  // item full[2] item empty[2] sums full, empty, scales[kScales], done
-  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + kScales + 1;
+  // item full[kItems] item empty[kItems] sums full, empty, scales[kScales], done
+  static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 2 + 2 + 2 + 2 * kItems + 2 + kScales + 1;
   static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
-  static constexpr int kOffSums = kOffItem + 2 * 64;  // (maximum, sum) of the second half's rows
+  static constexpr int kOffSums = kOffItem + kItems * 64;  // (maximum, sum) of the second half's rows
   static constexpr int kOffBad = kOffSums + (kTiles == 2 ? kRows * 8 : 0);
   static constexpr int kOffMisc = kOffBad + 4 * 16 * 4;
   static constexpr int kSmem = kOffMisc + 16;
@@ -120,7 +121,7 @@ struct Args {
   int heads;       // head blocks in all
   int run;         // queries of an item: the Q tiles' tokens
   int part_rows;   // rows of a part
-  Divider by_G, by_hg, by_run;
+  Divider by_G, by_hg, by_run, by_page;
   float* part;     // [CTA][2][part_rows][D] output sums
   float2* ml;      // [CTA][2][part_rows], the maximum and sum they refer to
   Note* note;      // [CTA]
@@ -164,7 +165,7 @@ __device__ __forceinline__ int64_t ramp(const Args& p, int64_t at, int n) {
 __device__ __forceinline__ int runs_of(const Args& p, int nq) { return p.by_run(nq + p.run - 1); }
 
 // The cost of the first r runs of a sequence.
-__device__ __forceinline__ int64_t cost_of(const Args& p, const Seq& s, int r) {
+__device__ __noinline__ int64_t cost_of(const Args& p, const Seq& s, int r) {
   const int64_t base = (int64_t)s.nk - s.nq;
   int64_t sum = (int64_t)kLead * r + ramp(p, base + p.run, r);
   if (r > 0 && (int64_t)r * p.run > s.nq) sum -= (int64_t)r * p.run - s.nq;  // the last run is shorter
@@ -389,8 +390,65 @@ __device__ __forceinline__ float weight(float m, float l, float top) {
   return l == 0.0f ? 0.0f : m == kNegInf ? 1.0f : exp2_fast(m - top);
 }
 
+__device__ __forceinline__ void shared4(uint32_t at, float (&x)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at));
+}
+
 __device__ __forceinline__ uint32_t low_bits(int n) {  // n below 0: none, above 32: all
   return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+}
+
+// A row's output, w0 O0 + w1 O1 (a weight of 0: that O may be anything), from TMEM, as bf16 or
+// (a part) fp32; whether it is finite.  how: 1 both O, 2 the row is one, 4 a part, 8 NaN.
+// (Called: inlined its registers are kept from the scores', which then spill.)
+template <int D>
+__device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w1, char* to, unsigned how) {
+  uint64_t checked = pair(0.0f, 0.0f);
+  const uint64_t ww0 = pair(w0, w0), ww1 = pair(w1, w1), zero2 = pair(0.0f, 0.0f);
+  __syncwarp();
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16], x[16] = {};
+    tmem_ld16(o0 + c, o);
+    if (__any_sync(~0u, how & 1)) tmem_ld16(o1 + c, x);  // (of the whole warp)
+    tmem_wait_ld();
+    if (w0 == 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = 0u;
+    }
+    if (w1 == 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      uint64_t y = mul2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ww0);
+      y = fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ww1, y);
+      checked = fma2(y, zero2, checked);  // 0 as long as every value is finite
+      float y0, y1;
+      unpair(y, y0, y1);
+      if (how & 8) y0 = y1 = __int_as_float(0x7fc00000);
+      o[e] = __float_as_uint(y0), o[e + 1] = __float_as_uint(y1);
+    }
+    if (how & 2) {
+      if (how & 4) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {
+        uint32_t y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+    }
+    to += how & 4 ? 64 : 32;
+    __syncwarp();
+  }
+  float lo, hi;
+  unpair(checked, lo, hi);
+  return lo + hi == 0.0f;
 }
 
 template <int D, bool kI8>
@@ -408,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
   uint64_t *full = bars, *empty = bars + C::kRing, *q_full = bars + 2 * C::kRing, *q_free = q_full + 2;
   uint64_t *s_full = q_free + 2, *p_full = s_full + 2, *o_full = p_full + 4,
            *o_free = o_full + 2, *pv_done = o_free + 2, *turn = pv_done + 2, *item_full = turn + 2,
-           *item_free = item_full + 2, *ml_full = item_free + 2, *ml_free = ml_full + 1,
+           *item_free = item_full + kItems, *ml_full = item_free + kItems, *ml_free = ml_full + 1,
            *scales = ml_free + 1, *all_done = scales + kScales;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* state = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -505,6 +563,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       mbar_init(o_free + i, 4);
       mbar_init(pv_done + i, 1);
       mbar_init(turn + i, 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
       mbar_init(item_free + i, 4 + kTiles + C::kSoftmax);  // every warp that reads items
     }
@@ -526,17 +586,23 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
   bool ok = true;
 
   int seen = 0;  // items read
-  auto item_ready = [&] { return mbar_test(item_full + (seen & 1), (seen >> 1) & 1); };
+  auto item_ready = [&] { return mbar_test(item_full + seen % kItems, (seen / kItems) & 1); };
+  auto item_there = [&] {  // the next one's place
+    ok = __all_sync(~0u, bar_wait(item_full + seen % kItems, (seen / kItems) & 1, state));
+    return reinterpret_cast<const volatile Item*>(smem + C::kOffItem + seen % kItems * 64);
+  };
+  auto item_done = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_free + seen % kItems);
+    ++seen;
+  };
   auto read_item = [&](Item& it) {
-    ok = __all_sync(~0u, bar_wait(item_full + (seen & 1), (seen >> 1) & 1, state));
+    const volatile int* from = reinterpret_cast<const volatile int*>(item_there());
     if (!ok) return false;
-    const volatile int* from = reinterpret_cast<const volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
     int* to = reinterpret_cast<int*>(&it);
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = from[i];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(item_free + (seen & 1));
-    ++seen;
+    item_done();
     return it.b >= 0;
   };
   if (warp >= kMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
@@ -611,15 +677,15 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         }
         break;
       }
-      if (seen >= 2)
-        ok = __all_sync(~0u, bar_wait(item_free + (seen & 1), ((seen >> 1) - 1) & 1, state));
+      if (seen >= kItems)
+        ok = __all_sync(~0u, bar_wait(item_free + seen % kItems, (seen / kItems - 1) & 1, state));
       if (!ok) break;
       if (lane == 0) {
-        volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + (seen & 1) * 64);
+        volatile int* to = reinterpret_cast<volatile int*>(smem + C::kOffItem + seen % kItems * 64);
         const int* from = reinterpret_cast<const int*>(&it);
 #pragma unroll
         for (int e = 0; e < (int)(sizeof(Item) / 4); ++e) to[e] = from[e];
-        mbar_arrive(item_full + (seen & 1));
+        mbar_arrive(item_full + seen % kItems);
       }
       __syncwarp();
       ++seen;
@@ -657,7 +723,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     int u = 0, f = 0;     // units issued, units handed over
     uint32_t kinds = 0;   // of the last 16 units: 1 V, 2 its second unit
     int tiles_in = 0, tiles_out = 0;  // K tiles issued, handed over
-    int64_t rows[2];      // this lane's row of the cache in tiles j and j - 1 (those whose V is to come)
+    int64_t rows[2] = {};  // this lane's row of the cache in tiles j and j - 1 (those whose V is to come)
+    int page = 0;          // and its page of tile j + 1; -1: no token
     // Unit f has landed (its group has been waited for): to the tensor core.
     auto hand_over = [&] {
       const int at16 = f & 15, st = f % C::kRing;
@@ -726,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       ++f;
     };
     // Of the unit's rows, idx / chunks is the row of this warp and idx % chunks the piece.
-    auto issue = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
+    auto issue = [&](bool v, int k, int64_t row) {
       const int at16 = u & 15;
       kinds = (kinds & ~(3u << (2 * at16))) | ((v ? 1u : 0u) | (k ? 2u : 0u)) << (2 * at16);
       const char* base = static_cast<const char*>(v ? a.c.v : a.c.k) + (v ? 0 : k * kSrcCols);
@@ -753,16 +820,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         else
           go(std::integral_constant<int, C::kCols / 64>(), 0);
       } else {
-        const int st = u % C::kRing;
-        if (u >= C::kRing) {  // while no place is free, what has landed goes on
-          while (ok && f < u && !__all_sync(~0u, mbar_test(empty + st, (u / C::kRing - 1) & 1))) {
-            copies_but(u - f - 1);
-            hand_over();
-          }
-          ok = ok && __all_sync(~0u, bar_wait(empty + st, (u / C::kRing - 1) & 1, state));
-        }
-        if (!ok) return;
-        const uint32_t to = ring + st * C::kUnit;
+        const uint32_t to = ring + u % C::kRing * C::kUnit;
         // Four rows and 64 columns of each at a time.
         auto go = [&](auto octs_c, auto rows_c, int row0) {
           constexpr int kOcts = decltype(octs_c)::value, kUnitRows = decltype(rows_c)::value;
@@ -783,58 +841,61 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         else
           go(integral_constant<int, C::kCols / 64>(), integral_constant<int, kKeys>(), 0);
       }
-      if (!v && k == 0) {
-        const unsigned any = __ballot_sync(~0u, bad);
-        if (lane == 0) bads[at16] = any;
-        ++tiles_in;
-      }
+      tiles_in += !v && k == 0;
       asm volatile("cp.async.commit_group;" ::: "memory");
       ++u;
     };
-    auto next = [&](bool v, int k, int64_t row, bool bad, const Item& it) {
-      issue(v, k, row, bad, it);
-      if (kI8 && ok && u - f == C::kAhead) {
-        copies_but<C::kAhead - 1>();
-        hand_over();
+    // One place each for a copy and for a hand-over: their code is long.
+    Item it = {};
+    int x = 0, steps = 0;   // units of the item issued, all of them
+    bool ending = false;
+    auto token_of = [&](int j) {  // this lane's token of tile j; -1: none
+      const int v = (it.t0 + j) * kKeys + key;
+      return v < it.nv ? v + (v >= a.sinks ? it.skip : 0) : -1;
+    };
+    auto page_of = [&](int token) {
+      return token < 0 ? 0 : __ldg(a.table + it.b * a.table_width + p.by_page(token));
+    };
+    while (ok) {
+      if (x == steps && !ending && (f == u || __all_sync(~0u, item_ready()))) {
+        ending = !read_item(it);
+        x = 0, steps = ending ? 0 : 2 * C::kUnits * it.tiles;
+        if (steps) page = page_of(token_of(0));
+        continue;
       }
-    };
-    auto drain = [&] {
-      copies_but<0>();
-      while (ok && f < u) hand_over();
-    };
-    Item it;
-    for (;;) {
-      if (f < u && !__all_sync(~0u, item_ready())) drain();
-      if (!ok || !read_item(it)) break;
-      const int n = it.tiles;
-      bool bad = false;
-      auto find = [&](int j) {  // this lane's row of tile j
-        const int v = (it.t0 + j) * kKeys + key;
-        bad = false;
-        if (v >= it.nv) return (int64_t)-1;
-        const int64_t row = cached_row(a, it, v);
-        bad = row < 0;
-        return row;
-      };
-#pragma unroll 1
-      for (int j = 0; j < n + (kTiles == 1) && ok; ++j) {
-        if (j < n) {
+      bool room = x < steps && u - f < C::kAhead;
+      if (!kI8 && room && u >= C::kRing) {
+        uint64_t* place = empty + u % C::kRing;
+        const uint32_t phase = (u / C::kRing - 1) & 1;
+        if (f == u)
+          ok = __all_sync(~0u, bar_wait(place, phase, state));
+        else
+          room = __all_sync(~0u, mbar_test(place, phase));
+        if (!ok) break;
+      }
+      if (room) {
+        const int y = x / C::kUnits, k = x % C::kUnits;
+        const bool v = kTiles == 2 ? y & 1 : (y && !(y & 1)) || x + C::kUnits >= steps;
+        if (!v && k == 0) {
+          const int j = (y + 1) / 2, token = token_of(j);
           rows[1] = rows[0];
-          rows[0] = find(j);
-#pragma unroll
-          for (int k = 0; k < C::kUnits; ++k)
-            if (ok) next(false, k, rows[0], bad, it);
-        } else {
-          rows[1] = rows[0];
+          const bool bad = token >= 0 && (unsigned)page >= (unsigned)a.c.pages;
+          rows[0] = token < 0 || bad
+                        ? -1
+                        : ((int64_t)page * a.c.kv_heads + it.h) * p.by_page.d + (token - p.by_page(token) * p.by_page.d);
+          if (j + 1 < it.tiles) page = page_of(token_of(j + 1));
+          const unsigned any = __ballot_sync(~0u, bad);
+          if (lane == 0) bads[u & 15] = any;
         }
-        if (kTiles == 1 && j == 0) continue;
-#pragma unroll
-        for (int k = 0; k < C::kUnits; ++k)
-          if (ok) next(true, k, rows[kTiles == 1], false, it);
+        issue(v, k, kTiles == 1 && v && x + C::kUnits < steps ? rows[1] : rows[0]);
+        ++x;
+      } else if (f < u) {
+        copies_but(u - f - 1);
+        hand_over();
+      } else if (ending) {
+        break;
       }
-      if (!ok) break;
     }
-    if (ok) drain();
     copies_but<0>();  // whatever becomes of the MMAs, the copies land before the CTA ends
   } else if (warp >= kMma && warp < kMma + kTiles) {
     // ---- MMAs.  The warp stays converged and an elected lane issues each product
@@ -990,25 +1051,30 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     // this row's token of the tile, and those of the warp's first and last row
     const int my_tok = p.by_hg(row), tok_lo = p.by_hg(32 * quarter), tok_hi = p.by_hg(32 * quarter + 31);
     const int my_head = row - my_tok * p.hg;
-    const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     float2* sums = reinterpret_cast<float2*>(smem + C::kOffSums);
     int done = 0, fed = 0, outs[2] = {}, joins = 0;  // of the items before: tiles of this S, all tiles, outputs, sums
-    Item it;
-    while (read_item(it)) {
+    for (;; item_done()) {
+      // The item stays where it is and is read again for the output: the registers are
+      // the scores'.
+      const volatile Item& it = *item_there();
+      if (!ok || it.b < 0) break;
       const bool split = kTiles == 2 && it.split;
-      const int tiles = s ? it.n[1] : it.n[0], first = it.first + (split ? 0 : s * p.tpt);
+      const int tiles = s ? it.n[1] : it.n[0], t0 = it.t0;
+      auto first_of = [&] { return it.first + (split ? 0 : s * p.tpt); };
       // What the row of token t sees of the run's tokens.
       auto sight_of = [&](int t) {
-        const int end = max(0, it.nk - it.nq + min(first + t, it.nq - 1) + 1);  // (no more than the last query)
+        const int nq = it.nq, skip = it.skip;
+        const int end = max(0, it.nk - nq + min(first_of() + t, nq - 1) + 1);  // (no more than the last query)
         Sight x;
         x.sinks = a.sinks;
-        x.from = a.window ? max(0, end - a.window) - it.skip : 0;
-        x.end = end - it.skip;
+        x.from = a.window ? max(0, end - a.window) - skip : 0;
+        x.end = end - skip;
         return x;
       };
-      const Sight sight = sight_of(my_tok), lowest = sight_of(tok_lo), highest = sight_of(tok_hi);
-      const bool mine = row < p.hg * p.tpt && first + my_tok < it.nq;
-      const bool idle = first + tok_lo >= it.nq || 32 * quarter >= p.hg * p.tpt;  // no row of the warp is one
+      const Sight sight = sight_of(my_tok);
+      // of the warp's rows: the first end, the last one, the last beginning
+      const int lowest_end = sight_of(tok_lo).end, highest_end = sight_of(tok_hi).end, highest_from = sight_of(tok_hi).from;
+      const bool idle = first_of() + tok_lo >= it.nq || 32 * quarter >= p.hg * p.tpt;  // no row of the warp is one
       float m = kNegInf;  // what P refers to, in units of log2
       bool ready = false, odd = false;
       uint64_t sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
@@ -1026,15 +1092,14 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           ready = false;
           continue;
         }
-        const int v0 = (it.t0 + j) * kKeys;
-        const float* ks = nullptr;
-        const float* vs = nullptr;
+        const int v0 = (t0 + j) * kKeys;
+        uint32_t ks = 0, vs = 0;  // where the tile's scales are
         if constexpr (kI8) {
           const int sc = (fed + j) & (kScales - 1);
           ok = __all_sync(~0u, bar_wait(scales + sc, ((fed + j) / kScales) & 1, state));
           if (!ok) break;
-          ks = reinterpret_cast<const float*>(smem + C::kOffScale) + sc * 2 * kKeys;
-          vs = ks + kKeys;
+          ks = smem_addr(smem + C::kOffScale) + sc * 2 * kKeys * 4;
+          vs = ks + kKeys * 4;
           const uint4 om = *reinterpret_cast<const uint4*>(smem + C::kOffOdd + sc * 16);
           if (__builtin_expect(om.x | om.y | om.z | om.w, 0)) {
             const uint32_t o[4] = {om.x, om.y, om.z, om.w};
@@ -1046,8 +1111,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
         }
         fence_after();
-        const int left_hi = highest.end - v0;
-        if (__builtin_expect(lowest.end - v0 < kKeys || (highest.from > v0 && sight.sinks - v0 < kKeys), 0)) {
+        const int left_hi = highest_end - v0;
+        if (__builtin_expect(lowest_end - v0 < kKeys || (highest_from > v0 && sight.sinks - v0 < kKeys), 0)) {
           // Keys that a row does not see, in TMEM: a loop that fits the instruction cache.
 #pragma unroll 1
           for (int c = 0; c < (left_hi > 64 ? kKeys : 64); c += 32) {
@@ -1058,14 +1123,19 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
             tmem_ld32(at + c, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if constexpr (kI8) x[e] = __float_as_uint(__uint_as_float(x[e]) * ks[c + e]);
-              if (!(in >> e & 1)) x[e] = 0xff800000u;
+            for (int e = 0; e < 32; e += 4) {
+              float k[4];
+              if constexpr (kI8) shared4(ks + 4 * (c + e), k);
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                if constexpr (kI8) x[e + f] = __float_as_uint(__uint_as_float(x[e + f]) * k[f]);
+                if (!(in >> (e + f) & 1)) x[e + f] = 0xff800000u;
+              }
             }
             tmem_st32(at + c, x);
           }
           tmem_wait_st();
-          if constexpr (kI8) ks = reinterpret_cast<const float*>(smem + C::kOffOnes);
+          if constexpr (kI8) ks = smem_addr(smem + C::kOffOnes);
         }
         // The second 64 columns are read twice, for the maximum and again for their
         // exponentials: 128 values held beside P's do not fit the registers.
@@ -1078,11 +1148,11 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           if constexpr (kI8) {
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
-              const float4 k = *reinterpret_cast<const float4*>(ks + c0 + e);
-              float y0, y1;
-              unpair(mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair(k.x, k.y)), y0, y1);
+              float k[4], y0, y1;
+              shared4(ks + 4 * (c0 + e), k);
+              unpair(mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair(k[0], k[1])), y0, y1);
               x[e] = __float_as_uint(y0), x[e + 1] = __float_as_uint(y1);
-              unpair(mul2(pair(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), pair(k.z, k.w)), y0, y1);
+              unpair(mul2(pair(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), pair(k[2], k[3])), y0, y1);
               x[e + 2] = __float_as_uint(y0), x[e + 3] = __float_as_uint(y1);
             }
           }
@@ -1138,6 +1208,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         const uint64_t zz = pair(z, z), ss = pair(scale2, scale2);
         auto half_p = [&](int half) {  // of v
           uint32_t x[32];
+          float w[4];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float x0, x1;
@@ -1146,8 +1217,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
             x1 = exp2_fast(x1);
             sum2[e & 1] = add2(sum2[e & 1], pair(x0, x1));
             if constexpr (kI8) {
-              const float2 w = *reinterpret_cast<const float2*>(vs + 64 * half + 2 * e);
-              unpair(mul2(pair(x0, x1), pair(w.x, w.y)), x0, x1);
+              if (e % 2 == 0) shared4(vs + 4 * (64 * half + 2 * e), w);
+              unpair(mul2(pair(x0, x1), pair(w[2 * (e & 1)], w[2 * (e & 1) + 1])), x0, x1);
             }
             x[e] = bf16x2(x0, x1);
           }
@@ -1179,7 +1250,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       }
       if (!ok) break;
       done += tiles;
-      fed += it.tiles;
+      const int part_tiles = it.tiles, n0 = it.n[0], n1 = it.n[1];
+      fed += part_tiles;
 
       // ---- the output -------------------------------------------------------------------
       float l;
@@ -1188,7 +1260,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         unpair(add2(sum2[0], sum2[1]), lo, hi);
         l = lo + hi;
       }
-      const bool two = split && it.n[1] > 0;  // both O are one run's
+      const bool two = split && n1 > 0;  // both O are one run's
       if (two && s == 1) {
         if (joins > 0) ok = __all_sync(~0u, bar_wait(ml_free, (joins - 1) & 1, state));
         if (!ok) break;
@@ -1196,8 +1268,9 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
       }
-      if ((split && s == 1) || (!split && first >= it.nq)) {
-        outs[0] += it.n[0] > 0, outs[1] += it.n[1] > 0, joins += two;
+      const int t = first_of() + my_tok, nq = it.nq;
+      if ((split && s == 1) || (!split && t - my_tok >= nq)) {
+        outs[0] += n0 > 0, outs[1] += n1 > 0, joins += two;
         continue;
       }
       float w0 = 1.0f, w1 = 0.0f, l1 = 0.0f;
@@ -1215,10 +1288,11 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         l = l0 * w0 + l1 * w1;
         m = top;
       }
-      const int t = first + my_tok;
+      const bool mine = row < p.hg * p.tpt && t < nq;
+      const int slot = it.slot;
       const int64_t out_row = (int64_t)(it.q0 + t) * a.Hq + it.hq0 + my_head;
-      const bool parts = it.slot >= 0;
-      const int64_t part_row = ((int64_t)blockIdx.x * 2 + max(0, it.slot)) * p.part_rows + (split ? 0 : s * kRows) + row;
+      const bool parts = slot >= 0;
+      const int64_t part_row = ((int64_t)blockIdx.x * 2 + max(0, slot)) * p.part_rows + (split ? 0 : s * kRows) + row;
       if (mine) {
         if (parts)
           p.ml[part_row] = make_float2(m, l);
@@ -1231,53 +1305,16 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       }
       if (l0 == 0.0f) w0 = 0.0f;
       const int o_mine = split ? 0 : s;  // the O that this warp reads first
-      const bool has0 = (o_mine ? it.n[1] : it.n[0]) > 0;
+      const bool has0 = (o_mine ? n1 : n0) > 0;
       if (has0) ok = __all_sync(~0u, bar_wait(o_full + o_mine, outs[o_mine] & 1, state));
       if (two) ok = ok && __all_sync(~0u, bar_wait(o_full + 1, outs[1] & 1, state));
       if (!ok) break;
       fence_after();
-      uint64_t checked = pair(0.0f, 0.0f);
-      if (!idle) {
-        char* to = parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D);
-        const uint64_t ww0 = pair(w0, w0), ww1 = pair(w1, w1), zero2 = pair(0.0f, 0.0f);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16], o1[16];
-          if (has0) tmem_ld16(o_at + o_mine * D + c, o);
-          if (two) tmem_ld16(o_at + D + c, o1);
-          tmem_wait_ld();
-          if (w0 == 0.0f || !has0) {  // without a key O may be anything
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          }
-          if (w1 == 0.0f || !two) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o1[e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            uint64_t y = mul2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ww0);
-            if (two) y = fma2(pair(__uint_as_float(o1[e]), __uint_as_float(o1[e + 1])), ww1, y);
-            checked = fma2(y, zero2, checked);  // 0 as long as every value is finite
-            float y0, y1;
-            unpair(y, y0, y1);
-            if (odd) y0 = y1 = __int_as_float(0x7fc00000);
-            o[e] = __float_as_uint(y0), o[e + 1] = __float_as_uint(y1);
-          }
-          if (!mine) continue;
-          if (parts) {
-            store32(to, o, true);
-            store32(to + 32, o + 8, true);
-            to += 64;
-          } else {
-            uint32_t y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            store32(to, y, aligned32);
-            to += 32;
-          }
-        }
-      }
+      bool fine = true;
+      if (!idle)
+        fine = put_row<D>(o_at + o_mine * D, o_at + D, has0 ? w0 : 0.0f, two ? w1 : 0.0f,
+                          parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D),
+                          (two ? 1u : 0u) | (mine ? 2u : 0u) | (parts ? 4u : 0u) | (odd ? 8u : 0u));
       // the next item's products may come
       fence_before();
       __syncwarp();
@@ -1285,16 +1322,15 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (has0) mbar_arrive(o_free + o_mine);
         if (two) mbar_arrive(o_free + 1);
       }
-      outs[0] += it.n[0] > 0, outs[1] += it.n[1] > 0, joins += two;
+      outs[0] += n0 > 0, outs[1] += n1 > 0, joins += two;
       // rows whose sum is finite and whose output is not
-      float lo, hi;
-      unpair(checked, lo, hi);
-      const unsigned again = __ballot_sync(~0u, mine && !odd && !(lo + hi == 0.0f) && l == l);
+      const unsigned again = __ballot_sync(~0u, mine && !odd && !fine && l == l);
       if (__builtin_expect(again, 0)) {
         __syncwarp();
-        const int n = split ? it.tiles : s ? it.n[1] : it.n[0];
-        const Item copy = it;  // (its address is taken: `it` stays in registers)
-        repair<D, kI8>(p, copy, again, out_row, sight, it.t0 * kKeys, min(it.nv, (it.t0 + n) * kKeys),
+        const int n = split ? part_tiles : s ? n1 : n0;
+        Item copy;
+        copy.b = it.b, copy.h = it.h, copy.skip = it.skip;
+        repair<D, kI8>(p, copy, again, out_row, sight, t0 * kKeys, min((int)it.nv, (t0 + n) * kKeys),
                        parts ? p.part + part_row * D : nullptr, p.ml + part_row, state);
       }
     }
@@ -1402,7 +1438,7 @@ cudaError_t launch(const ChunkArgs& a, void* ws, cudaStream_t st) {
   const Plan plan = plan_of(a.B, a.Tq, a.Hq, a.c.kv_heads, D);
   const int64_t G = a.Hq / a.c.kv_heads;
   Args p{a, (int)G, plan.hg, plan.tpt, (int)(a.c.kv_heads * (G / plan.hg)), C::kTiles * plan.tpt, plan.part_rows,
-         Divider(G), Divider(plan.hg), Divider(C::kTiles * plan.tpt), nullptr, nullptr, nullptr};
+         Divider(G), Divider(plan.hg), Divider(C::kTiles * plan.tpt), Divider(a.c.page_tokens), nullptr, nullptr, nullptr};
   auto up = [](void* q) { return (reinterpret_cast<uintptr_t>(q) + 255) & ~(uintptr_t)255; };
   const size_t rows = (size_t)kCtas * 2 * plan.part_rows;
   p.part = reinterpret_cast<float*>(up(ws));
