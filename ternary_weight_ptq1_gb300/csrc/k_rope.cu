@@ -16,29 +16,38 @@
 // operations a clock and SM); pos times that, modulo 2^64, is the angle without
 // its whole turns, off by 2^-33 turns at most.
 //
-// A CTA has a few tokens: its threads make their cosines and sines once, in
-// shared memory, for all heads.  Then head_dim / 8 neighbouring threads hold a
-// row, each two pieces of four values that make four pairs, so neither the
-// rotation nor its loads and stores need an exchange; the rows of kRows heads
-// are loaded together.
+// head_dim / 8 neighbouring threads have a token and go through its heads, kRows
+// rows at a time, the next ones on their way; a thread holds two pieces of four values
+// that make four pairs of its own, so neither the rotation nor its loads and stores need
+// an exchange, and its cosines and sines are made once.  (A CTA with a table of four
+// tokens' angles in shared memory, whose threads took the rows in any order: 67 us for 38
+// on 8192 tokens of 40 + 8 heads of 128, 94 for 43 into a bf16 cache, 369 for 168 on 20,011
+// of 24 + 4 of 256 into int8 and out again.)  More CTAs an SM, which leave fewer registers,
+// lost: 41 us with five of 128 threads, 46 with six.
+//
+// Measured in CUDA graphs: those 8192 tokens, norms, three axes, bf16 in 38 us (5.2 TB/s,
+// 77% of the copy rate), 43 into a bf16 cache with the values (5.4 TB/s); 5003 tokens of 28
+// heads of 256, a quarter rotated, fp32 in 48 us (6.0 TB/s); 64 tokens of 48 heads in 3.4 us.
+#include <type_traits>
+
 #include "kv_row.cuh"
+#include "packed.cuh"
 
 namespace ptq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;      // rows a thread has in flight
-constexpr int kTokens = 4;    // most tokens of a CTA
-constexpr int kMaxPairs = 128;
+constexpr int kThreads = 128;
+// Rows a thread has in work, and as many on their way.  (8192 tokens of 48 heads of 128, bf16:
+// 38 us with four, 50 with two; 5003 of 28 of 256, fp32: 52 and 48.)
+template <Act T>
+constexpr int kRowsOf = T == Act::F32 ? 2 : 4;
 
 enum Dest { kTensor, kBf16, kI8 };  // where keys go (and values, unless kTensor)
 
 struct Args {
   RopeArgs a;
-  CacheGeometry g;       // kBf16, kI8
-  int heads;             // of a token: q, k and, into a cache, v
-  int tokens, per;       // of a CTA: tokens, heads
-  Divider by_per, by_half;
+  CacheGeometry g;  // kBf16, kI8
+  int heads, per;   // of a token (q, k and, into a cache, v), of a thread
 };
 
 // f / (2 pi) modulo 1, times 2^64: f is m 2^e with m a 24-bit integer, and m
@@ -55,175 +64,223 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   return b >> 31 ? 0 - t : t;
 }
 
+// Four values as they are in memory, and in fp32.
 template <Act T>
-__device__ __forceinline__ void load4(const void* p, int64_t e, float* x) {
-  if constexpr (T == Act::F32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e);
-    x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xffff0000u);
-    x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xffff0000u);
-  }
+using Raw4 = std::conditional_t<T == Act::F32, float4, uint2>;
+template <Act T>
+__device__ __forceinline__ Raw4<T> load4(const char* p) {
+  return *reinterpret_cast<const Raw4<T>*>(p);
+}
+__device__ __forceinline__ void value4(const float4& a, uint64_t* x) {
+  x[0] = pair(a.x, a.y), x[1] = pair(a.z, a.w);
+}
+__device__ __forceinline__ void value4(const uint2& a, uint64_t* x) {
+  x[0] = pair(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u));
+  x[1] = pair(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
 }
 template <Act T>
-__device__ __forceinline__ void store4(void* p, int64_t e, const float* x) {
+__device__ __forceinline__ void store4(char* p, const uint64_t* x) {
+  float v[4];
+  unpair(x[0], v[0], v[1]);
+  unpair(x[1], v[2], v[3]);
   if constexpr (T == Act::F32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + e) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + e) =
-        make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
 }
+__device__ __forceinline__ uint64_t swapped(uint64_t v) { return v >> 32 | v << 32; }
 
 template <Act T, int D, Dest kDest>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args p) {
-  constexpr int kLanes = D / kVec, kGroups = kThreads / kLanes;
-  __shared__ __align__(16) float2 turn[kTokens * kMaxPairs];  // (cos, sin)
+  constexpr int kLanes = D / kVec, kGroups = kThreads / kLanes, kSize = T == Act::F32 ? 4 : 2, kRows = kRowsOf<T>;
+  constexpr int kOut = kDest == kI8 ? 1 : 2;  // bytes of a cached value
   const RopeArgs& a = p.a;
-  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t t = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes;
+  const bool there = t < a.T;
+  const int first = blockIdx.y * p.per, last = min(first + p.per, p.heads);
   pdl_release();
   pdl_wait();
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
-  const int n_tok = (int)min((int64_t)p.tokens, a.T - t0), h0 = blockIdx.y * p.per;
-  const int rows = n_tok * p.per, half = a.rotary / 2;
+  const int half = a.rotary / 2;
   const bool rotates = 8 * lane < a.rotary;
   // this thread's pieces of a row
   const int e0 = rotates && !a.near ? 4 * lane : 8 * lane, e1 = rotates && !a.near ? half + 4 * lane : 8 * lane + 4;
 
-  struct Row {
-    int64_t t;
-    int in_cta, h;  // token of the CTA, head among q, k, v
-    bool there;
+  // The kinds of heads (0 q, 1 k, 2 v): each one's rows of this thread, one after the other.
+  Raw4<T> next[kRows][2];
+  auto from_of = [&](int kind) {
+    return static_cast<const char*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+           t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * kSize;
   };
-  auto row_at = [&](int r) {
-    Row w;
-    w.in_cta = p.by_per(r);
-    w.h = h0 + r - w.in_cta * p.per;
-    w.t = t0 + w.in_cta;
-    w.there = r < rows && w.h < p.heads;
-    return w;
-  };
-  float x[kRows][kVec];
-  auto load = [&](int r0) {
+  auto load = [&](const char* row, int n) {  // n rows
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const Row w = row_at(r0 + u * kGroups);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[u][i] = 0.0f;
-      if (!w.there) continue;
-      const int hk = w.h - a.Hq, hv = hk - a.Hkv;
-      const void* from = hk < 0 ? a.q : hv < 0 ? a.k : a.v;
-      const int64_t e = w.t * (hk < 0 ? a.q_stride : hv < 0 ? a.k_stride : a.v_stride) +
-                        (int64_t)(hk < 0 ? w.h : hv < 0 ? hk : hv) * D;
-      load4<T>(from, e + e0, x[u]);
-      load4<T>(from, e + e1, x[u] + 4);
-    }
+    for (int u = 0; u < kRows; ++u)
+      if (there && u < n) {
+        next[u][0] = load4<T>(row + (u * D + e0) * kSize);
+        next[u][1] = load4<T>(row + (u * D + e1) * kSize);
+      }
   };
-  load(group);
-  for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
-    const int tok = p.by_half(i), pair = i - tok * half;
-    const float f = __ldg(a.inv_freq + pair);
-    const int ax = a.axis ? __ldg(a.axis + pair) : 0;
-    float2 cs = make_float2(1.0f, 0.0f);  // a pair of no axis stays as it is
-    if ((unsigned)ax < (unsigned)a.axes) {
-      const int64_t pos = __ldg(a.pos + ax * a.pos_stride + t0 + tok);
-      const uint64_t at = (uint64_t)pos * turns_of(f) + (1ull << 31);
-      sincospif((float)(int32_t)(at >> 32) * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31 half turns
-      if (!(fabsf(f) < __int_as_float(0x7f800000))) cs.x = cs.y = __int_as_float(0x7fc00000);
+  // kind k has heads [begin(k), begin(k) + count(k)) of this thread's
+  auto begin = [&](int k) { return max(first - (k == 0 ? 0 : a.Hq + (k - 1) * a.Hkv), 0); };
+  auto end = [&](int k) { return min(last - (k == 0 ? 0 : a.Hq + (k - 1) * a.Hkv), k == 0 ? a.Hq : a.Hkv); };
+  int kind = 0;
+  while (kind < 3 && begin(kind) >= end(kind)) ++kind;
+  if (kind == 3) return;
+  load(from_of(kind) + (int64_t)begin(kind) * D * kSize, end(kind) - begin(kind));
+
+  // (cos, cos) and (-sin, sin) of pairs that lie side by side, else pairs of cosines and of sines
+  uint64_t c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = pair(1.0f, 1.0f), s[i] = 0;
+  if (rotates && first < a.Hq + a.Hkv) {
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = __ldg(a.inv_freq + 4 * lane + i);
+      const int ax = a.axis ? __ldg(a.axis + 4 * lane + i) : 0;
+      cs[i] = 1.0f, sn[i] = 0.0f;  // a pair of no axis stays as it is
+      if ((unsigned)ax < (unsigned)a.axes && there) {
+        const int64_t pos = __ldg(a.pos + ax * a.pos_stride + t);
+        const uint64_t at = (uint64_t)pos * turns_of(f) + (1ull << 31);
+        sincospif((float)(int32_t)(at >> 32) * 4.656612873077393e-10f, sn + i, cs + i);  // 2^-31 half turns
+        if (!(fabsf(f) < __int_as_float(0x7f800000))) cs[i] = sn[i] = __int_as_float(0x7fc00000);
+      }
     }
-    turn[i] = cs;
+    if (a.near) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = pair(cs[i], cs[i]), s[i] = pair(-sn[i], sn[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) c[i] = pair(cs[2 * i], cs[2 * i + 1]), s[i] = pair(sn[2 * i], sn[2 * i + 1]);
+    }
   }
-  __syncthreads();
 
 #pragma unroll 1
-  for (int r0 = group; r0 - group < rows; r0 += kRows * kGroups) {
-    if (r0 != group) load(r0);
+  for (; kind < 3; ++kind) {
+    const int h0 = begin(kind), h1 = end(kind);
+    if (h0 >= h1) continue;
+    const float* gain = kind == 0 ? a.q_gain : kind == 1 ? a.k_gain : nullptr;
+    uint64_t g[4] = {};
+    if (gain) {
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain + e0)),
+                   g1 = __ldg(reinterpret_cast<const float4*>(gain + e1));
+      value4(g0, g), value4(g1, g + 2);
+    }
+    // where rows go: a tensor, or this token's place in the cache
+    const bool cached = kDest != kTensor && kind > 0;
+    char* to;
+    int64_t step = (int64_t)D * kSize, row = 0;
+    bool stored = there;
+    if (cached) {
+      const int slot = there ? __ldg(a.slots + t) : -1;
+      stored = (unsigned)slot < (unsigned)p.g.pages_slots;
+      row = cache_row(stored ? slot : 0, 0, p.g);
+      to = static_cast<char*>(kind == 1 ? a.ck : a.cv) + row * (D * kOut);
+      step = (int64_t)p.g.page_tokens.d * (D * kOut);
+    } else {
+      to = static_cast<char*>(kind == 0 ? a.q_out : a.k_out) + t * (kind == 0 ? a.qo_stride : a.ko_stride) * kSize;
+    }
+    const char* from = from_of(kind);
+#pragma unroll 1
+    for (int h = h0; h < h1; h += kRows) {
+      uint64_t x[kRows][4];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const Row w = row_at(r0 + u * kGroups);
-      const int hk = w.h - a.Hq, hv = hk - a.Hkv;
-      const bool value = kDest != kTensor && hv >= 0;
-      const float* gain = value ? nullptr : hk < 0 ? a.q_gain : a.k_gain;
-      if (a.q_gain || a.k_gain) {
-        float ss = 0.0f;
+      for (int u = 0; u < kRows; ++u) {
+        x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0;
+        if (there && h + u < h1) value4(next[u][0], x[u]), value4(next[u][1], x[u] + 2);
+      }
+      // the next rows, of this kind or the one after
+      if (h + kRows < h1) {
+        load(from + (int64_t)(h + kRows) * D * kSize, h1 - h - kRows);
+      } else {
+        int k = kind + 1;
+        while (k < 3 && begin(k) >= end(k)) ++k;
+        if (k < 3) load(from_of(k) + (int64_t)begin(k) * D * kSize, end(k) - begin(k));
+      }
+      if (gain) {
+        float ss[kRows];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+        for (int u = 0; u < kRows; ++u) {
+          uint64_t q = mul2(x[u][0], x[u][0]);
 #pragma unroll
-        for (int i = kLanes / 2; i > 0; i >>= 1) ss += __shfl_xor_sync(~0u, ss, i);
-        if (__builtin_expect(__any_sync(~0u, !(ss < __int_as_float(0x7f800000))), 0)) {
-          // the squares of a row of finite values overflow: over a power of two
-          float m = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(x[u][i]));
-#pragma unroll
-          for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
-          const bool over = !(ss < __int_as_float(0x7f800000)) && gain && m < __int_as_float(0x7f800000);
-          float s2 = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            const float y = x[u][i] * 0x1p-96f;
-            s2 = fmaf(y, y, s2);
-            if (over) x[u][i] = y;
-          }
-#pragma unroll
-          for (int i = kLanes / 2; i > 0; i >>= 1) s2 += __shfl_xor_sync(~0u, s2, i);
-          if (over) ss = s2;  // (eps is far below a unit of it)
+          for (int i = 1; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
+          float lo, hi;
+          unpair(q, lo, hi);
+          ss[u] = lo + hi;
         }
-        if (gain) {
-          const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-          const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain + e0)),
-                       g1 = __ldg(reinterpret_cast<const float4*>(gain + e1));
-          const float g[kVec] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) x[u][i] = x[u][i] * inv * g[i];
+        for (int i = kLanes / 2; i > 0; i >>= 1)
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) ss[u] += __shfl_xor_sync(~0u, ss[u], i);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          if (__builtin_expect(__any_sync(~0u, !(ss[u] < __int_as_float(0x7f800000))), 0)) {
+            // the squares of a row of finite values overflow: over a power of two
+            float m = 0.0f, v[kVec], s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpair(x[u][i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+            for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
+            const bool over = !(ss[u] < __int_as_float(0x7f800000)) && m < __int_as_float(0x7f800000);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s2 = fmaf(v[i] * 0x1p-96f, v[i] * 0x1p-96f, s2);
+#pragma unroll
+            for (int i = kLanes / 2; i > 0; i >>= 1) s2 += __shfl_xor_sync(~0u, s2, i);
+            if (over) {
+              ss[u] = s2;  // (eps is far below a unit of it)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], pair(0x1p-96f, 0x1p-96f));
+            }
+          }
+          const float inv = rsqrtf(ss[u] * (1.0f / D) + a.eps);
+          const uint64_t ii = pair(inv, inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][i] = mul2(mul2(x[u][i], ii), g[i]);
         }
       }
-      if (rotates && !value && w.there) {
-        const float4* cs = reinterpret_cast<const float4*>(turn + w.in_cta * half + 4 * lane);
-        const float4 c01 = cs[0], c23 = cs[1];
-        const float c[4] = {c01.x, c01.z, c23.x, c23.z}, s[4] = {c01.y, c01.w, c23.y, c23.w};
-        auto turned = [&](float& ya, float& yb, int i) {
-          const float xa = ya, xb = yb;
-          ya = xa * c[i] - xb * s[i];
-          yb = xb * c[i] + xa * s[i];
-        };
+      if (rotates && kind < 2) {
         if (a.near) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) turned(x[u][2 * i], x[u][2 * i + 1], i);
+          for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = fma2(x[u][i], c[i], mul2(swapped(x[u][i]), s[i]));
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) turned(x[u][i], x[u][4 + i], i);
+          for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint64_t xa = x[u][i], xb = x[u][2 + i];
+              x[u][i] = fma2(xa, c[i], mul2(xb, s[i] ^ 0x8000000080000000ull));
+              x[u][2 + i] = fma2(xb, c[i], mul2(xa, s[i]));
+            }
         }
       }
-      if (kDest == kTensor || hk < 0) {
-        if (w.there && hk < 0) {
-          const int64_t e = w.t * a.qo_stride + (int64_t)w.h * D;
-          store4<T>(a.q_out, e + e0, x[u]);
-          store4<T>(a.q_out, e + e1, x[u] + 4);
-        } else if (w.there) {
-          const int64_t e = w.t * a.ko_stride + (int64_t)hk * D;
-          store4<T>(a.k_out, e + e0, x[u]);
-          store4<T>(a.k_out, e + e1, x[u] + 4);
-        }
-      }
-      if constexpr (kDest != kTensor) {
-        const int slot = w.there && hk >= 0 ? __ldg(a.slots + w.t) : -1;
-        const bool ok = (unsigned)slot < (unsigned)p.g.pages_slots;
-        const int64_t row = ok ? cache_row(slot, value ? hv : hk, p.g) : 0;
-        if constexpr (kDest == kBf16) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        char* at = to + (h + u) * step;
+        const bool ok = stored && h + u < h1;
+        if (!cached) {
           if (ok) {
-            void* to = value ? a.cv : a.ck;
-            store4<Act::BF16>(to, row * D + e0, x[u]);
-            store4<Act::BF16>(to, row * D + e1, x[u] + 4);
+            store4<T>(at + e0 * kSize, x[u]);
+            store4<T>(at + e1 * kSize, x[u] + 2);
           }
-        } else {
-          uint32_t code[2];
-          const float s = quantise<kLanes, true>(x[u], code);
+        } else if constexpr (kDest == kBf16) {
           if (ok) {
-            char* to = static_cast<char*>(value ? a.cv : a.ck) + row * D;
-            *reinterpret_cast<uint32_t*>(to + e0) = code[0];
-            *reinterpret_cast<uint32_t*>(to + e1) = code[1];
-            if (lane == 0) (value ? a.vs : a.ks)[row] = s;
+            store4<Act::BF16>(at + e0 * 2, x[u]);
+            store4<Act::BF16>(at + e1 * 2, x[u] + 2);
+          }
+        } else if constexpr (kDest == kI8) {
+          float v[kVec];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unpair(x[u][i], v[2 * i], v[2 * i + 1]);
+          uint32_t code[2];
+          const float sc = quantise<kLanes, true>(v, code);
+          if (ok) {
+            *reinterpret_cast<uint32_t*>(at + e0) = code[0];
+            *reinterpret_cast<uint32_t*>(at + e1) = code[1];
+            if (lane == 0) (kind == 2 ? a.vs : a.ks)[row + (int64_t)(h + u) * p.g.page_tokens.d] = sc;
           }
         }
       }
@@ -233,18 +290,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 template <Act T, int D, Dest kDest>
 cudaError_t launch(const RopeArgs& a, const ptq_kv_cache* c, cudaStream_t st) {
-  constexpr int kGroups = kThreads / (D / kVec);
+  constexpr int kGroups = kThreads / (D / kVec), kRows = kRowsOf<T>;
   const int64_t heads = a.Hq + a.Hkv * (kDest == kTensor ? 1 : 2);
-  // Few tokens: a row a thread group, over as many CTAs as that takes.  Many: a
-  // CTA has all heads of kTokens tokens, whose angles are made once.
-  const bool many = a.T >= 1024;
-  const int64_t per = many || heads <= kGroups ? heads : kGroups;
-  const int64_t tokens = many ? kTokens : 1;
-  const int64_t x = (a.T + tokens - 1) / tokens, y = (heads + per - 1) / per;
-  if (x > INT32_MAX || y > 65535 || per > INT32_MAX / kTokens) return cudaErrorInvalidValue;
+  // A thread goes through all heads of its token, or, where that leaves SMs without work,
+  // through as many as keep them busy, kRows at least.
+  const int64_t x = (a.T + kGroups - 1) / kGroups, most = (heads + kRows - 1) / kRows;
+  int64_t y = (4 * 152 + x - 1) / x;
+  y = y < most ? y : most;
+  const int64_t per = ((heads + y - 1) / y + kRows - 1) / kRows * kRows;
+  y = (heads + per - 1) / per;
+  if (x > INT32_MAX || y > 65535) return cudaErrorInvalidValue;
   const Args p{a, CacheGeometry{c ? (int)(c->pages * c->page_tokens) : 0, Divider(c ? c->page_tokens : 1),
                                 Divider(c ? c->kv_heads : 1)},
-               (int)heads, (int)tokens, (int)per, Divider(per), Divider(a.rotary ? a.rotary / 2 : 1)};
+               (int)heads, (int)per};
   return launch_pdl(rope_kernel<T, D, kDest>, dim3((unsigned)x, (unsigned)y), dim3(kThreads), 0, st, p);
 }
 
