@@ -72,14 +72,16 @@ struct Cfg {
   static constexpr int kStage = kI8 ? kUnit / 2 : 0;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
-  static constexpr int kThreads = 32 * (kSoftmax + 8);  // four to feed, four others
-  // Registers a thread.  Two Q tiles: 512 threads get 128 each at launch (65,536
+  static constexpr int kFeeds = kI8 ? 8 : 4;          // warps that feed
+  static constexpr int kThreads = 32 * (kSoftmax + kFeeds + 4);
+  // Registers a thread.  Two Q tiles, bf16: 512 threads get 128 each at launch (65,536
   // in all); 256 softmax threads take 168, 128 that feed keep 96 and 128 others
-  // 80 (65,536).  One: 384 get 168 (64,512); 128 take 232, 128 keep 128, 128 keep
-  // 104 (59,392).
-  static constexpr int kRegsSoftmax = kTiles == 2 ? 168 : 232;
-  static constexpr int kRegsFeed = kTiles == 2 ? 96 : 128;
-  static constexpr int kRegsOther = kTiles == 2 ? 80 : 104;
+  // 80 (65,536); int8: 640 get 96 (61,440), 256 take 152, 256 keep 56 and 128 keep 64
+  // (61,440).  One, bf16: 384 get 168 (64,512); 128 take 232, 128 keep 128, 128 keep
+  // 104 (59,392); int8: 512 get 128 (65,536), 128 take 232, 256 keep 80, 128 keep 104 (63,488).
+  static constexpr int kRegsSoftmax = kTiles == 1 ? 232 : kI8 ? 152 : 168;
+  static constexpr int kRegsFeed = kTiles == 1 ? (kI8 ? 80 : 128) : kI8 ? 56 : 96;
+  static constexpr int kRegsOther = kTiles == 1 ? 104 : kI8 ? 64 : 80;
   static constexpr int kOffRing = kTiles * kQ;
   static constexpr int kOffStage = kOffRing + kRing * kUnit;
   // int8: K and V scales of each tile, and a bit for each V scale that is not finite;
@@ -94,7 +96,7 @@ struct Cfg {
   static constexpr int kOffItem = (kOffBar + 8 * kBars + 15) / 16 * 16;
   static constexpr int kOffSums = kOffItem + kItems * 64;  // (maximum, sum) of the second half's rows
   static constexpr int kOffBad = kOffSums + (kTiles == 2 ? kRows * 8 : 0);
-  static constexpr int kOffMisc = kOffBad + 4 * 16 * 4;
+  static constexpr int kOffMisc = kOffBad + kFeeds * 16 * 4;
   static constexpr int kSmem = kOffMisc + 16;
 };
 static_assert(Cfg<128, false>::kSmem <= 227 * 1024 && Cfg<256, false>::kSmem <= 227 * 1024 &&
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
 
   const ChunkArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kFeed = C::kSoftmax, kMma = kFeed + 4, kPlan = kMma + kTiles, kWarps = C::kThreads / 32;
+  constexpr int kFeed = C::kSoftmax, kMma = kFeed + C::kFeeds, kPlan = kMma + kTiles, kWarps = C::kThreads / 32;
 
   pdl_release();
   pdl_wait();
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == kFeed && lane == 0) {
     for (int i = 0; i < C::kRing; ++i) {
-      mbar_init(full + i, 4);  // the four warps that feed
+      mbar_init(full + i, C::kFeeds);
       mbar_init(empty + i, kTiles);
     }
     for (int i = 0; i < 2; ++i) {
@@ -566,11 +568,11 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_free + i, 4 + kTiles + C::kSoftmax);  // every warp that reads items
+      mbar_init(item_free + i, C::kFeeds + kTiles + C::kSoftmax);  // every warp that reads items
     }
     mbar_init(ml_full, 4);
     mbar_init(ml_free, 4);
-    for (int i = 0; i < kScales; ++i) mbar_init(scales + i, 4);
+    for (int i = 0; i < kScales; ++i) mbar_init(scales + i, C::kFeeds);
     mbar_init(all_done, kTiles);
     *state = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -711,14 +713,15 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       if (qn[t] > 0) static_cast<void>(mbar_wait(q_full + t, (qn[t] - 1) & 1, nullptr));
   } else if (warp >= kFeed && warp < kMma) {
     // ---- K and V tiles through the ring in the order of their use: K_0 V_0 K_1 V_1 ..., or
-    // with one Q tile K_0 K_1 V_0 K_2 V_1 ...  A warp has 32 keys of each tile (lane l
-    // key 64 (l / 16) + 16 w + l % 16: 16 of each half), of a V unit of 64 keys 16 ------
+    // with one Q tile K_0 K_1 V_0 K_2 V_1 ...  A warp has kMine keys of each tile, as many of
+    // each half (a lane finds the page of one), of a V unit of 64 keys those ---------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFeed));
     constexpr int kRowBytes = D * (kI8 ? 1 : 2);       // of a cached row
     constexpr int kSrcCols = C::kCols * (kI8 ? 1 : 2);  // bytes of a row in a K unit
     const int w = warp - kFeed;
-    const int key = 64 * (lane >> 4) + 16 * w + (lane & 15);
-    const uint32_t stage = smem_addr(smem + C::kOffStage) + w * (C::kStage / 4);
+    constexpr int kMine = kKeys / C::kFeeds, kHalf = kMine / 2;
+    const int key = 64 * (lane / kHalf & 1) + kHalf * w + lane % kHalf;
+    const uint32_t stage = smem_addr(smem + C::kOffStage) + w * (C::kStage / C::kFeeds);
     uint32_t* bads = reinterpret_cast<uint32_t*>(smem + C::kOffBad) + 16 * w;
     int u = 0, f = 0;     // units issued, units handed over
     uint32_t kinds = 0;   // of the last 16 units: 1 V, 2 its second unit
@@ -739,8 +742,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         // of 128 bytes, then 1, 3, 5, 7, the rows beside them the others (by the swizzle).
         auto go = [&](auto quads_c, auto rows_c) {
           constexpr int kQuads = decltype(quads_c)::value, kUnitRows = decltype(rows_c)::value;
-          constexpr int kIts = C::kStage / 4 / 512, kBatch = 4;
-          const uint32_t at = to + (16 * w + (lane >> 2)) * 128, p0 = ((2 * (lane & 3)) ^ (lane >> 2)) << 4;
+          constexpr int kIts = C::kStage / C::kFeeds / 512, kBatch = kIts < 4 ? kIts : 4;
+          const uint32_t at = to + (kHalf * w + (lane >> 2)) * 128, p0 = ((2 * (lane & 3)) ^ (lane >> 2)) << 4;
 #pragma unroll
           for (int i0 = 0; i0 < kIts; i0 += kBatch) {
             uint32_t x[kBatch][4];
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
               const int g = (i0 + i) / kQuads, block = (i0 + i) % kQuads;  // rows 8 g .. of the warp
-              const uint32_t d = at + block * kUnitRows * 128 + (kUnitRows == kKeys ? 64 * (g >> 1) + 8 * (g & 1) : 8 * g) * 128;
+              const uint32_t d = at + block * kUnitRows * 128 + (64 * (8 * g / kHalf) + 8 * g % kHalf) * 128;
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[2 * e] = codes<0x4140>(x[i][e]), y[2 * e + 1] = codes<0x4342>(x[i][e]);
@@ -773,12 +776,15 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (!v && !second) {  // this lane's scales
           const int slot = tiles_out & (kScales - 1);
           float* sc = reinterpret_cast<float*>(smem + C::kOffScale) + slot * 2 * kKeys + key;
-          if (bads[at16] >> lane & 1) sc[0] = __int_as_float(0x7fc00000);
-          const bool odd = !(fabsf(sc[kKeys]) < -kNegInf);
-          if (odd) sc[kKeys] = 0.0f;
+          bool odd = false;
+          if (lane < kMine) {
+            if (bads[at16] >> lane & 1) sc[0] = __int_as_float(0x7fc00000);
+            odd = !(fabsf(sc[kKeys]) < -kNegInf);
+            if (odd) sc[kKeys] = 0.0f;
+          }
           const unsigned odds = __ballot_sync(~0u, odd);
-          uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kOffOdd + slot * 16);
-          if ((lane & 15) == 0) mask[4 * (lane >> 4) + w] = (uint16_t)(odds >> lane);
+          uint8_t* mask = smem + C::kOffOdd + slot * 16;  // (eight keys a byte)
+          if (lane == 0) mask[w] = (uint8_t)odds, mask[8 + w] = (uint8_t)(odds >> 8);
           __syncwarp();
           if (lane == 0) mbar_arrive(scales + slot);
         }
@@ -802,11 +808,13 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (!v && k == 0) {
           const int slot = tiles_in & (kScales - 1);
           const uint32_t sc = smem_addr(smem + C::kOffScale) + slot * (2 * kKeys * 4) + 4 * key;
-          copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
-          copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
+          if (lane < kMine) {
+            copy4(sc, a.c.k_scale + (row < 0 ? 0 : row), row >= 0);
+            copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
+          }
         }
         auto go = [&](auto quads_c, int row0) {
-          constexpr int kQuads = decltype(quads_c)::value, kIts = C::kStage / 4 / 512;
+          constexpr int kQuads = decltype(quads_c)::value, kIts = C::kStage / C::kFeeds / 512;
 #pragma unroll
           for (int g = 0; g < kIts / kQuads; ++g) {
             const int64_t src = __shfl_sync(~0u, row, row0 + 8 * g + (lane >> 2));
@@ -816,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
         };
         if (D == 256 && v)
-          go(std::integral_constant<int, D / 64>(), 16 * k);
+          go(std::integral_constant<int, D / 64>(), kHalf * k);
         else
           go(std::integral_constant<int, C::kCols / 64>(), 0);
       } else {
@@ -824,20 +832,20 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         // Four rows and 64 columns of each at a time.
         auto go = [&](auto octs_c, auto rows_c, int row0) {
           constexpr int kOcts = decltype(octs_c)::value, kUnitRows = decltype(rows_c)::value;
-          constexpr int kIts = C::kUnit / 4 / 512;
-          const uint32_t at = to + (16 * w + (lane >> 3)) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4;
+          constexpr int kIts = C::kUnit / C::kFeeds / 512;
+          const uint32_t at = to + (kHalf * w + (lane >> 3)) * 128, p0 = ((lane & 7) ^ (lane >> 3)) << 4;
 #pragma unroll
           for (int g = 0; g < kIts / kOcts; ++g) {
             const int64_t src = __shfl_sync(~0u, row, row0 + 4 * g + (lane >> 3));
             const char* from = base + (src < 0 ? 0 : src) * kRowBytes + (lane & 7) * 16;
-            const uint32_t d = at + (kUnitRows == kKeys ? 64 * (g >> 2) + 4 * (g & 3) : 4 * g) * 128 + (p0 ^ (64 * (g & 1)));
+            const uint32_t d = at + (64 * (4 * g / kHalf) + 4 * g % kHalf) * 128 + (p0 ^ (64 * (g & 1)));
 #pragma unroll
             for (int o = 0; o < kOcts; ++o) copy16(d + o * kUnitRows * 128, from + 128 * o, src >= 0);
           }
         };
         using std::integral_constant;
         if (D == 256 && v)
-          go(integral_constant<int, D / 64>(), integral_constant<int, C::kVKeys>(), 16 * k);
+          go(integral_constant<int, D / 64>(), integral_constant<int, C::kVKeys>(), kHalf * k);
         else
           go(integral_constant<int, C::kCols / 64>(), integral_constant<int, kKeys>(), 0);
       }
