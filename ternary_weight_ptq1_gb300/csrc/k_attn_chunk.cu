@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     uint32_t kinds = 0;   // of the last 16 units: 1 V, 2 its second unit
     int tiles_in = 0, tiles_out = 0;  // K tiles issued, handed over
     int64_t rows[2] = {};  // this lane's row of the cache in tiles j and j - 1 (those whose V is to come)
-    int page = 0;          // and its page of tile j + 1; -1: no token
+    int page = 0;          // and its page of tile j + 1
     // Unit f has landed (its group has been waited for): to the tensor core.
     auto hand_over = [&] {
       const int at16 = f & 15, st = f % C::kRing;
@@ -861,9 +861,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       const int v = (it.t0 + j) * kKeys + key;
       return v < it.nv ? v + (v >= a.sinks ? it.skip : 0) : -1;
     };
-    auto page_of = [&](int token) {
-      return token < 0 ? 0 : __ldg(a.table + it.b * a.table_width + p.by_page(token));
-    };
+    // (always a load into the one register, which nothing touches until the tile is issued)
+    auto page_of = [&](int token) { return __ldg(a.table + it.b * a.table_width + p.by_page(max(token, 0))); };
     while (ok) {
       if (x == steps && !ending && (f == u || __all_sync(~0u, item_ready()))) {
         ending = !read_item(it);
@@ -891,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           rows[0] = token < 0 || bad
                         ? -1
                         : ((int64_t)page * a.c.kv_heads + it.h) * p.by_page.d + (token - p.by_page(token) * p.by_page.d);
-          if (j + 1 < it.tiles) page = page_of(token_of(j + 1));
+          page = page_of(token_of(min(j + 1, it.tiles - 1)));
           const unsigned any = __ballot_sync(~0u, bad);
           if (lane == 0) bads[u & 15] = any;
         }
