@@ -1151,10 +1151,10 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           tmem_ld32(at + c0, to);
           tmem_ld32(at + c0 + 32, to + 32);
         };
-        auto scaled = [&](uint32_t* x, int c0) {  // scores of int8 codes
+        auto scaled = [&](uint32_t* x, int c0, auto n) {  // n scores of int8 codes
           if constexpr (kI8) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < decltype(n)::value; e += 4) {
               float k[4], y0, y1;
               shared4(ks + 4 * (c0 + e), k);
               unpair(mul2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair(k[0], k[1])), y0, y1);
@@ -1165,22 +1165,36 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
         };
         float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-        auto take_max = [&](const uint32_t* x) {
+        using std::integral_constant;
+        constexpr integral_constant<int, 64> k64;
+        constexpr integral_constant<int, 32> k32;
+        auto take_max = [&](const uint32_t* x, auto n) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 2)
+          for (int c = 0; c < decltype(n)::value; c += 2)
             top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
         };
-        {
+        if constexpr (kI8) {  // (with their scales 128 values do not fit)
+          read_s(v, 0);
+          tmem_wait_ld();
+          scaled(v, 0, k64);
+          take_max(v, k64);
+          if (left_hi > 64) {
+#pragma unroll
+            for (int c = 64; c < kKeys; c += 32) {
+              uint32_t x[32];
+              tmem_ld32(at + c, x);
+              tmem_wait_ld();
+              scaled(x, c, k32);
+              take_max(x, k32);
+            }
+          }
+        } else {
           uint32_t second[64];
           read_s(v, 0);
           read_s(second, 64);
           tmem_wait_ld();
-          scaled(v, 0);
-          take_max(v);
-          if (left_hi > 64) {
-            scaled(second, 64);
-            take_max(second);
-          }
+          take_max(v, k64);
+          if (left_hi > 64) take_max(second, k64);
         }
         const float t2 = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale2;
         if (i == 0) {
@@ -1247,7 +1261,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (left_hi > 64) {
           read_s(v, 64);
           tmem_wait_ld();
-          scaled(v, 64);
+          scaled(v, 64, k64);
           half_p(1);
         } else {
           const uint32_t none[32] = {};
