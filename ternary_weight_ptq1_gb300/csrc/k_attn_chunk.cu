@@ -68,7 +68,7 @@ struct Cfg {
   static constexpr int kUnit = kKeys * kCols * 2;    // bytes
   static constexpr int kRing = kI8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
   // Units on their way at most (int8: the places that they land in).
-  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 3) : kRing - 1;
+  static constexpr int kAhead = kI8 ? (D == 64 ? 6 : 2) : D == 128 ? 2 : 3;
   static constexpr int kStage = kI8 ? kUnit / 2 : 0;
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSoftmax = 4 * kTiles;        // softmax warps
@@ -863,24 +863,9 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     };
     // (always a load into the one register, which nothing touches until the tile is issued)
     auto page_of = [&](int token) { return __ldg(a.table + it.b * a.table_width + p.by_page(max(token, 0))); };
-    while (ok) {
-      if (x == steps && !ending && (f == u || __all_sync(~0u, item_ready()))) {
-        ending = !read_item(it);
-        x = 0, steps = ending ? 0 : 2 * C::kUnits * it.tiles;
-        if (steps) page = page_of(token_of(0));
-        continue;
-      }
-      bool room = x < steps && u - f < C::kAhead;
-      if (!kI8 && room && u >= C::kRing) {
-        uint64_t* place = empty + u % C::kRing;
-        const uint32_t phase = (u / C::kRing - 1) & 1;
-        if (f == u)
-          ok = __all_sync(~0u, bar_wait(place, phase, state));
-        else
-          room = __all_sync(~0u, mbar_test(place, phase));
-        if (!ok) break;
-      }
-      if (room) {
+    for (;;) {
+      const bool more = x < steps;
+      if (more) {
         const int y = x / C::kUnits, k = x % C::kUnits;
         const bool v = kTiles == 2 ? y & 1 : (y && !(y & 1)) || x + C::kUnits >= steps;
         if (!v && k == 0) {
@@ -894,13 +879,27 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           const unsigned any = __ballot_sync(~0u, bad);
           if (lane == 0) bads[u & 15] = any;
         }
+        if (!kI8 && u >= C::kRing) {
+          ok = __all_sync(~0u, bar_wait(empty + u % C::kRing, (u / C::kRing - 1) & 1, state));
+          if (!ok) break;
+        }
         issue(v, k, kTiles == 1 && v && x + C::kUnits < steps ? rows[1] : rows[0]);
         ++x;
-      } else if (f < u) {
-        copies_but(u - f - 1);
-        hand_over();
-      } else if (ending) {
+      } else if (!ending && (f == u || __all_sync(~0u, item_ready()))) {
+        ending = !read_item(it);
+        x = 0, steps = ending ? 0 : 2 * C::kUnits * it.tiles;
+        if (steps) page = page_of(token_of(0));
+        continue;
+      } else if (f == u) {
         break;
+      }
+      if (u - f == C::kAhead || !more) {
+        if (more)
+          copies_but<C::kAhead - 1>();
+        else
+          copies_but(u - f - 1);
+        hand_over();
+        if (!ok) break;
       }
     }
     copies_but<0>();  // whatever becomes of the MMAs, the copies land before the CTA ends
