@@ -942,18 +942,19 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         mma_commit(empty + st);
         if (kTiles == 2 && (split || j >= theirs) && !(v && owns_last && j == tiles - 1)) mma_commit(empty + st);
       };
-      // S of tile j into its slot
-      auto scores = [&](int j) {
+      // S of tile j into its slot; `there`: K has landed
+      const uint32_t q_desc = tile_desc(qs + q_at * C::kQ, 16);
+      auto scores = [&](int j, unsigned x, bool there) {
         const int slot = slot_of(j);
         if (j == 0) wait(q_full + q_at, qn[q_at] - 1);
 #pragma unroll
-        for (int k = 0; k < C::kUnits; ++k) {  // by columns
-          const unsigned x = k_unit(j) + k;
-          landed(x);
+        for (int k = 0; k < C::kUnits; ++k, ++x) {  // by columns
+          const int st = place(x);
+          if (!there) landed(x);
           fence_after();
           if (ok && elected()) {
-            const uint32_t qd = tile_desc(qs + q_at * C::kQ + k * (C::kCols / 64) * kRows * 128, 16);
-            const uint32_t kd = tile_desc(ring + place(x) * C::kUnit, 16);
+            const uint32_t qd = q_desc + k * (C::kCols / 64) * (kRows * 128 / 16);
+            const uint32_t kd = tile_desc(ring + st * C::kUnit, 16);
 #pragma unroll
             for (int c = 0; c < C::kCols / 64; ++c)  // descriptors count 16 bytes
 #pragma unroll
@@ -964,7 +965,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
                 else
                   mma_ss<true>(tmem + slot * kKeys, qd + o, kd + o, idesc<kKeys, false>());
               }
-            release(j, place(x), false);
+            release(j, st, false);
             if (k == C::kUnits - 1) {
               mma_commit(s_full + slot);
               if (j == tiles - 1) {
@@ -981,21 +982,24 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         if (ok && lane == 0) mbar_arrive(q_free);
         __syncwarp();
       }
-      if (!kAfter) scores(0);
+      if (!kAfter) scores(0, k_unit(0), false);
 #pragma unroll 1
       for (int j = kAfter ? -1 : 0; j < most && ok; ++j) {
         const bool mine = j >= 0 && j < tiles, more = j + 1 < tiles;
-        if (!kAfter && more) scores(j + 1);
+        const unsigned k_at = k_unit(j + 1);
+        if (!kAfter && more) scores(j + 1, k_at, false);
         // O += P V, over the first and second 64 keys
         const int slot = slot_of(j), use = use_of(j);
         const unsigned v = v_unit(j);
+        const int v_st[2] = {place(v), place(v + C::kUnits - 1)};
         if (mine) {
 #pragma unroll
           for (int k = 0; k < C::kUnits; ++k) landed(v + k);
           if (j == 0 && outs > 0) wait(o_free + s, outs - 1);
         }
         // (not where S have each their own tiles: K may wait for V's release)
-        if (kAfter && !split && j >= 0 && more) landed(k_unit(j + 1));
+        const bool there = kAfter && !split && j >= 0 && more;
+        if (there) landed(k_at);
 #pragma unroll
         for (int half = 0; half < 2 && j >= 0; ++half) {
           if (mine) wait(p_full + 2 * slot + half, use);
@@ -1009,7 +1013,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           if (!mine) break;
           fence_after();
           if (ok && elected()) {
-            const int st = place(v + (C::kUnits == 2 ? half : 0));
+            const int st = v_st[half];
             const uint32_t pa = tmem + slot * kKeys + 32 * half;
             const uint32_t d = tmem + 2 * kKeys + s * D;
             const uint32_t vd = tile_desc(ring + st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
@@ -1029,7 +1033,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (kAfter && more) scores(j + 1);
+        if (kAfter && more) scores(j + 1, k_at, there);
         if (kAfter && !split && j >= 0 && ok && lane == 0) mbar_arrive(turn + 1 - s);
       }
       if (kTiles == 2 && !owns_last) {
