@@ -908,8 +908,12 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     // in straight-line code; with two Q tiles each has an issuing warp of its own, and
     // one waits for barriers while the other's MMAs run ----------------------------------
     const int s = warp - kMma;
-    auto wait = [&](uint64_t* bar, int phase) {
-      ok = ok && __all_sync(~0u, bar_wait(bar, phase & 1, state));
+    // The lanes agree on how the waits went once a tile, when its products are issued (a vote at
+    // each wait took 530 us for 514 at 8192 tokens); until then all of them go the same way, and
+    // one that ran out of time issues nothing.
+    auto wait = [&](uint64_t* bar, int phase) { ok = ok && bar_wait(bar, phase & 1, state); };
+    auto agree = [&] {
+      ok = __all_sync(~0u, ok);
     };
     // of the items before: units in the ring, tiles of this S, rounds of turns, outputs of
     // this S, Q tiles loaded
@@ -952,7 +956,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           const int st = place(x);
           if (!there) landed(x);
           fence_after();
-          if (ok && elected()) {
+          if (elected() && ok) {
             const uint32_t qd = q_desc + k * (C::kCols / 64) * (kRows * 128 / 16);
             const uint32_t kd = tile_desc(ring + st * C::kUnit, 16);
 #pragma unroll
@@ -979,6 +983,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       };
       if (split && tiles == 0) {  // (it releases the Q tile too, as above)
         wait(q_full, qn[0] - 1);
+        agree();
         if (ok && lane == 0) mbar_arrive(q_free);
         __syncwarp();
       }
@@ -992,6 +997,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         const int slot = slot_of(j), use = use_of(j);
         const unsigned v = v_unit(j);
         const int v_st[2] = {place(v), place(v + C::kUnits - 1)};
+        const uint32_t v_desc[2] = {tile_desc(ring + v_st[0] * C::kUnit, C::kVKeys * 128),
+                                    tile_desc(ring + v_st[1] * C::kUnit + (C::kUnits == 2 ? 0 : 8192), C::kVKeys * 128)};
         if (mine) {
 #pragma unroll
           for (int k = 0; k < C::kUnits; ++k) landed(v + k);
@@ -1012,12 +1019,11 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
           if (!mine) break;
           fence_after();
-          if (ok && elected()) {
+          if (elected() && ok) {
             const int st = v_st[half];
             const uint32_t pa = tmem + slot * kKeys + 32 * half;
             const uint32_t d = tmem + 2 * kKeys + s * D;
-            const uint32_t vd = tile_desc(ring + st * C::kUnit + (C::kUnits == 2 ? 0 : 8192 * half),
-                                          C::kVKeys * 128);
+            const uint32_t vd = v_desc[half];
             if (half > 0 || j > 0)
               mma_ts<true>(d, pa, vd, idesc<D, true>());
             else
@@ -1035,10 +1041,12 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         }
         if (kAfter && more) scores(j + 1, k_at, there);
         if (kAfter && !split && j >= 0 && ok && lane == 0) mbar_arrive(turn + 1 - s);
+        agree();
       }
       if (kTiles == 2 && !owns_last) {
         const unsigned last = units + 2 * it.tiles - 1;
         landed(last);
+        agree();
         if (ok && lane == 0) mbar_arrive(empty + place(last));
         __syncwarp();
       }
