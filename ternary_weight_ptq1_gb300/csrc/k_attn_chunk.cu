@@ -53,7 +53,8 @@ namespace ptq {
 namespace {
 
 constexpr int kCtas = (int)kSms;
-constexpr int kLead = 256;   // cost of a run's start, in keys
+constexpr int kLead = 512;   // cost of a run's start, in keys
+constexpr int kLeast = 256;  // the shortest stretch of a CTA
 constexpr int kScales = 8;   // tiles whose scales are in shared memory
 constexpr int kItems = 4;    // items on their way from the warp that plans to the others
 
@@ -182,6 +183,8 @@ __device__ __forceinline__ int tokens_of(const Args& p, const Seq& s, int r, int
   *skip = p.a.window ? max(0, max(0, from - p.a.window) - p.a.sinks) : 0;
   return end - *skip;
 }
+
+__device__ __forceinline__ int tiles_of(int tokens) { return (int)(((unsigned)tokens + kKeys - 1) / kKeys); }
 
 // The first tile of a run (of n, which begins at unit `start`) that is not before unit u.
 __device__ __forceinline__ int tile_at(int64_t u, int64_t start, int n) {
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       total += scan[w];
     }
     per = (total + gridDim.x - 1) / gridDim.x;
-    per = (per + kKeys - 1) / kKeys * kKeys;
+    per = max((int64_t)kLeast, (per + kKeys - 1) / kKeys * kKeys);
     u0 = blockIdx.x * per;
     u1 = min(u0 + per, total);
     if (u0 >= total) return;
@@ -645,12 +648,12 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           }
         }
         it.nv = tokens_of(p, s, r, &it.skip);
-        const int n = (it.nv + kKeys - 1) / kKeys;
+        const int n = tiles_of(it.nv);
         it.t0 = tile_at(u0, start, n);
         const int t1 = tile_at(u1, start, n);
         const int64_t begin = start;
         const int this_run = r++;
-        start += kLead + it.nv;
+        start += (int64_t)kLead + it.nv;
         if (it.t0 >= t1 && !(n == 0 && begin >= u0)) continue;
         it.b = seq;
         it.q0 = s.q0, it.nq = s.nq, it.nk = s.nk;
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           it.n[0] = (it.tiles + 1) / 2, it.n[1] = it.tiles / 2;
         } else {
           const int v = it.nk - it.nq + it.first + p.tpt - it.skip;  // what the first tile's last query sees
-          const int n0 = v > 0 ? (v + kKeys - 1) / kKeys : 0;
+          const int n0 = tiles_of(max(v, 0));
           it.n[0] = max(0, min(n0 - it.t0, it.tiles)), it.n[1] = it.tiles;
         }
         if (it.slot >= 0 && it.t0 == 0 && lane == 0) {
@@ -720,6 +723,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     constexpr int kSrcCols = C::kCols * (kI8 ? 1 : 2);  // bytes of a row in a K unit
     const int w = warp - kFeed;
     constexpr int kMine = kKeys / C::kFeeds, kHalf = kMine / 2;
+    constexpr int kUnitSh = C::kCols == 128;  // a unit is 64 << kUnitSh columns (V of 256 twice that)
     const int key = 64 * (lane / kHalf & 1) + kHalf * w + lane % kHalf;
     const uint32_t stage = smem_addr(smem + C::kOffStage) + w * (C::kStage / C::kFeeds);
     uint32_t* bads = reinterpret_cast<uint32_t*>(smem + C::kOffBad) + 16 * w;
@@ -740,8 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         const uint32_t from = stage + (f % C::kAhead) * C::kStage;
         // Eight rows and 64 codes of each at a time: four lanes a row write pieces 0, 2, 4, 6
         // of 128 bytes, then 1, 3, 5, 7, the rows beside them the others (by the swizzle).
-        auto go = [&](auto quads_c, auto rows_c) {
-          constexpr int kQuads = decltype(quads_c)::value, kUnitRows = decltype(rows_c)::value;
+        auto go = [&](int sh) {  // 64 << sh columns
           constexpr int kIts = C::kStage / C::kFeeds / 512, kBatch = kIts < 4 ? kIts : 4;
           const uint32_t at = to + (kHalf * w + (lane >> 2)) * 128, p0 = ((2 * (lane & 3)) ^ (lane >> 2)) << 4;
 #pragma unroll
@@ -754,8 +757,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
                            : "r"(from + ((i0 + i) * 32 + lane) * 16));
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-              const int g = (i0 + i) / kQuads, block = (i0 + i) % kQuads;  // rows 8 g .. of the warp
-              const uint32_t d = at + block * kUnitRows * 128 + (64 * (8 * g / kHalf) + 8 * g % kHalf) * 128;
+              const int g = (i0 + i) >> sh, block = (i0 + i) & ((1 << sh) - 1);  // rows 8 g .. of the warp
+              const uint32_t d = at + block * (C::kUnit >> sh) + (64 * (8 * g / kHalf) + 8 * g % kHalf) * 128;
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[2 * e] = codes<0x4140>(x[i][e]), y[2 * e + 1] = codes<0x4342>(x[i][e]);
@@ -768,11 +771,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
             }
           }
         };
-        using std::integral_constant;
-        if (D == 256 && v)
-          go(integral_constant<int, D / 64>(), integral_constant<int, C::kVKeys>());
-        else
-          go(integral_constant<int, C::kCols / 64>(), integral_constant<int, kKeys>());
+        go(kUnitSh + (D == 256 && v));
         if (!v && !second) {  // this lane's scales
           const int slot = tiles_out & (kScales - 1);
           float* sc = reinterpret_cast<float*>(smem + C::kOffScale) + slot * 2 * kKeys + key;
@@ -813,20 +812,14 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
             copy4(sc + 4 * kKeys, a.c.v_scale + (row < 0 ? 0 : row), row >= 0);
           }
         }
-        auto go = [&](auto quads_c, int row0) {
-          constexpr int kQuads = decltype(quads_c)::value, kIts = C::kStage / C::kFeeds / 512;
+        constexpr int kIts = C::kStage / C::kFeeds / 512;
+        const int sh = kUnitSh + (D == 256 && v), row0 = D == 256 && v ? kHalf * k : 0;
 #pragma unroll
-          for (int g = 0; g < kIts / kQuads; ++g) {
-            const int64_t src = __shfl_sync(~0u, row, row0 + 8 * g + (lane >> 2));
-            const char* from = base + (src < 0 ? 0 : src) * kRowBytes + (lane & 3) * 16;
-#pragma unroll
-            for (int q = 0; q < kQuads; ++q) copy16(to + ((g * kQuads + q) * 32 + lane) * 16, from + 64 * q, src >= 0);
-          }
-        };
-        if (D == 256 && v)
-          go(std::integral_constant<int, D / 64>(), kHalf * k);
-        else
-          go(std::integral_constant<int, C::kCols / 64>(), 0);
+        for (int i = 0; i < kIts; ++i) {
+          const int64_t src = __shfl_sync(~0u, row, row0 + 8 * (i >> sh) + (lane >> 2));
+          copy16(to + (i * 32 + lane) * 16,
+                 base + (src < 0 ? 0 : src) * kRowBytes + (lane & 3) * 16 + 64 * (i & ((1 << sh) - 1)), src >= 0);
+        }
       } else {
         const uint32_t to = ring + u % C::kRing * C::kUnit;
         // Four rows and 64 columns of each at a time.
@@ -858,8 +851,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     int x = 0, steps = 0;   // units of the item issued, all of them
     bool ending = false;
     auto token_of = [&](int j) {  // this lane's token of tile j; -1: none
-      const int v = (it.t0 + j) * kKeys + key;
-      return v < it.nv ? v + (v >= a.sinks ? it.skip : 0) : -1;
+      const unsigned v = (unsigned)(it.t0 + j) * kKeys + key;
+      return v < (unsigned)it.nv ? (int)v + (v >= (unsigned)a.sinks ? it.skip : 0) : -1;
     };
     // (always a load into the one register, which nothing touches until the tile is issued)
     auto page_of = [&](int token) { return __ldg(a.table + it.b * a.table_width + p.by_page(max(token, 0))); };
@@ -1383,7 +1376,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
 
 // Joins the parts of the run that begins in CTA blockIdx.x and goes on in the CTAs
 // after it, in their order: a warp a row.
-constexpr int kJoinCtas = 8;
+constexpr int kJoinCtas = 16;
 template <int D>
 __global__ void __launch_bounds__(256) attn_chunk_join_kernel(Args p) {
   constexpr int N = D / 32;
