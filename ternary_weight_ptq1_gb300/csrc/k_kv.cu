@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads)
       if (ok) store8<Act::BF16>(to, row * D + e, x[n]);
     } else {
       uint32_t w[2];
-      const float s = quantise<kLanes, T == Act::F32>(x[n], w);  // (bf16 rows stay within 127 as they are)
+      const float s = quantise<kLanes, T == Act::F32, false>(x[n], w);  // (bf16 rows stay within 127 as they are)
       if (ok) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(to) + row * D + e) = make_uint2(w[0], w[1]);
         if (e == 0) (n ? vs : ks)[row] = s;

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < 4; ++i) unpair(x[u][i], v[2 * i], v[2 * i + 1]);
           uint32_t code[2];
-          const float sc = quantise<kLanes, true>(v, code);
+          const float sc = quantise<kLanes, true, true>(v, code);
           if (ok) {
             *reinterpret_cast<uint32_t*>(at + e0) = code[0];
             *reinterpret_cast<uint32_t*>(at + e1) = code[1];

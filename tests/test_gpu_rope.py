@@ -252,6 +252,31 @@ def test_slots_outside_skip_and_nothing_else_is_written(P, kv):
     assert P.kv_append(cache, c.rope(P), k, v, slots, c.positions()) is None
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_codes_are_kv_writes_where_rounding_is_close(P, act):
+    """Halves, zeros, rows of few bits and of the smallest values: the same codes and scales, bit for bit."""
+    import torch
+
+    rng = np.random.default_rng(44)
+    T, Hkv, D = 400, 3, 64
+    v = rng.standard_normal((T, Hkv, D)).astype(np.float32)
+    v[:100] = (rng.integers(-254, 255, (100, Hkv, D)) / 2).astype(np.float32)        # halves of a scale of 1
+    v[:100, :, 0] = 127.0
+    v[100:150] = (rng.integers(-300, 300, (50, Hkv, D)) * 2.0 ** -149).astype(np.float32)
+    v[150:160] = 0.0
+    v[160:200] *= 2.0 ** rng.integers(-120, 120, (40, 1, 1)).astype(np.float32)
+    v[200:300] = rng.integers(-127, 128, (100, Hkv, D)) * np.float32(0.1)              # near whole codes
+    vd = _dev(v, act)
+    k = torch.randn(T, Hkv, D, device="cuda").to(_torch(act))
+    slots = torch.randperm(T + 8, device="cuda")[:T].to(torch.int32)
+    one, two = (P.KVCache.empty(T + 8, Hkv, 1, D, torch.int8) for _ in range(2))
+    rope = P.Rope(torch.zeros(0, device="cuda"))                                       # neither norm nor rotation
+    P.kv_append(one, rope, k, vd, slots, torch.zeros(T, dtype=torch.int32, device="cuda"))
+    P.kv_write(two, k, vd, slots)
+    for a, b in zip(_rows(one, slots), _rows(two, slots)):
+        assert torch.equal(a, b)
+
+
 def test_non_finite_rows_have_nan_scales(P):
     import torch
 
