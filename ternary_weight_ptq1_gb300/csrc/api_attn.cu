@@ -200,6 +200,10 @@ ptq_status attn_decode(const void* q, int64_t q_stride, const ptq_kv_cache* cach
   return e == cudaSuccess ? PTQ_OK : cuda_fail(e, who);
 }
 
+// Tokens that a query of a chunk may see: a CTA goes through as many in one piece of work, and the
+// waits for the next one end after 6 s (2^27 over int8 at head_dim 256 take 4).
+constexpr int64_t kMostSeen = (int64_t)1 << 27;
+
 bool chunk_shape_ok(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D) {
   return prefill_shape_ok(B, Tq, 0, Hq, Hkv, D);
 }
@@ -405,6 +409,10 @@ PTQ_API ptq_status ptq_attn_chunk(const void* q, int64_t q_stride, const ptq_kv_
                 (long long)q_stride);
   if (dtype != PTQ_BF16)
     return fail(PTQ_ERR_UNSUPPORTED, "%s: no kernel for dtype=f32 (chunks are bf16)", who);
+  if (t > kMostSeen && (window == 0 || window + sinks > kMostSeen))
+    return fail(PTQ_ERR_UNSUPPORTED,
+                "%s: a table row and a window of over 2^27 tokens (%lld, %lld + %lld)", who, (long long)t,
+                (long long)window, (long long)sinks);
   if (B == 0 || Tq == 0) return PTQ_OK;
   if (!q || !lens || !cu_q || !out || (!table && table_width > 0))
     return fail(PTQ_ERR_NULL, "%s: NULL pointer", who);

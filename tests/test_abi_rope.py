@@ -129,6 +129,10 @@ def test_chunk_alone(P):
     if need:
         assert _chunk(P, ws=None) == 6 and _chunk(P, wsb=need - 1) == 6 and _chunk(P, ws=ODD) == 3
     assert _chunk(P, dt=0) == 5 and b"f32" in P.load().ptq_last_error()
+    big = dict(pages=2 ** 20, page_tokens=256, kv_heads=1, head_dim=64)
+    most = dict(cache=big, qs=256, Hq=4)
+    assert _chunk(P, width=2 ** 19 + 1, **most) == 5 and _chunk(P, width=2 ** 19 + 1, window=2 ** 27, sinks=1, **most) == 5
+    assert _chunk(P, width=2 ** 19 + 1, window=2 ** 27, ws=None, **most) == 6       # (as far as the workspace)
     assert _chunk(P, Tq=-1) == 2 and _chunk(P, Tq=2 ** 31) == 2 and _chunk(P, B=2 ** 26) == 2
     assert _chunk(P, Tq=0, q=None, out=None, ws=None, wsb=0) == 0
     for bad in ((-1, 10, 4, 2, 128), (2, -1, 4, 2, 128), (2, 10, 5, 2, 128), (2, 10, 4, 2, 100), (2 ** 26, 10, 4, 2, 128)):
