@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import numpy as np
 
@@ -668,11 +669,12 @@ class Rope:
         self._int32 = torch.int32
         self._on = on
         self.inv_freq, self.axis, self.q_gain, self.k_gain = inv_freq, axis, q_gain, k_gain
-        self._front = (_dev(inv_freq, torch.float32, "inv_freq", on),
-                       None if axis is None else _dev(axis, torch.int8, "axis", on))
-        self._back = (2 * inv_freq.numel(), int(bool(interleaved)),
-                      None if q_gain is None else _dev(q_gain, torch.float32, "q_gain", on),
-                      None if k_gain is None else _dev(k_gain, torch.float32, "k_gain", on), eps)
+        self._fields = (_dev(inv_freq, torch.float32, "inv_freq", on),
+                        None if axis is None else _dev(axis, torch.int8, "axis", on), None, 0, 0, 2 * inv_freq.numel(),
+                        int(bool(interleaved)), None if q_gain is None else _dev(q_gain, torch.float32, "q_gain", on),
+                        None if k_gain is None else _dev(k_gain, torch.float32, "k_gain", on), eps)
+        self._gains = [(n, g.shape[0]) for n, g in (("q_gain", q_gain), ("k_gain", k_gain)) if g is not None]
+        self._own = threading.local()       # a struct for each thread that calls
 
     def __setattr__(self, name, value):
         if name in self.__dict__:
@@ -680,16 +682,25 @@ class Rope:
         self.__dict__[name] = value
 
     def _at(self, pos, T, D, on):
-        """The struct for T tokens of head width D at `pos`, on device `on`."""
+        """The address of the struct for T tokens of head width D at `pos`, on
+        device `on`: this thread's, until its next call."""
         if self._on != on:
             raise ValueError(f"the tensors of the Rope are on another device: cuda:{self._on}, not cuda:{on}")
-        for g, name in ((self.q_gain, "q_gain"), (self.k_gain, "k_gain")):
-            if g is not None and g.shape[0] != D:
-                raise ValueError(f"{name} must be {D} values, got {g.shape[0]}")
+        for name, n in self._gains:
+            if n != D:
+                raise ValueError(f"{name} must be {D} values, got {n}")
         s = pos.shape
         if len(s) not in (1, 2) or s[-1] != T:
             raise ValueError(f"pos must be axes x tokens ({T}), got {tuple(s)}")
-        return _RopeStruct(*self._front, _dev(pos, self._int32, "pos", on), T, 1 if len(s) == 1 else s[0], *self._back)
+        own = self._own.__dict__
+        if not own:
+            own["struct"] = struct = _RopeStruct(*self._fields)
+            own["at"] = ctypes.addressof(struct)
+        struct = own["struct"]
+        struct.pos = _dev(pos, self._int32, "pos", on)
+        struct.pos_stride = T
+        struct.axes = 1 if len(s) == 1 else s[0]
+        return own["at"]
 
 
 def qk_rope(rope, q, k, pos, q_out=None, k_out=None, stream=None):
@@ -711,7 +722,7 @@ def qk_rope(rope, q, k, pos, q_out=None, k_out=None, stream=None):
         k_out = _new(k, k.shape, dtype, stream)
     qo, qos = _heads(q_out, "q_out", dtype, on, q.shape)
     ko, kos = _heads(k_out, "k_out", dtype, on, k.shape)
-    _check(load().ptq_qk_rope(ctypes.addressof(at), qp, kp, qs, ks, qo, ko, qos, kos, T, Hq, k.shape[1], D, dt,
+    _check(load().ptq_qk_rope(at, qp, kp, qs, ks, qo, ko, qos, kos, T, Hq, k.shape[1], D, dt,
                               _stream(stream, on)), "ptq_qk_rope")
     return q_out, k_out
 
@@ -740,7 +751,7 @@ def kv_append(cache, rope, k, v, slots, pos, q=None, q_out=None, stream=None):
         qo, qos = _heads(q_out, "q_out", dtype, on, q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(load().ptq_kv_append(cache._ref, ctypes.addressof(at), qp, kp, vp, qs, ks, vs,
+    _check(load().ptq_kv_append(cache._ref, at, qp, kp, vp, qs, ks, vs,
                                 _dev(slots, cache._int32, "slots", on), qo, qos, T, Hq, dt, _stream(stream, on)),
            "ptq_kv_append")
     return q_out

@@ -1436,7 +1436,7 @@ __global__ void __launch_bounds__(256) attn_chunk_join_kernel(Args p) {
   const ChunkArgs& a = p.a;
   const Note note = p.note[blockIdx.x];
   const int lane = threadIdx.x & 31, parts = note.last - (int)blockIdx.x + 1;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < note.tokens * p.hg; r += 8 * kJoinCtas) {
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < note.tokens * p.hg; r += 8 * gridDim.y) {
     const int t = p.by_hg(r), head = r - t * p.hg;
     const int tile = t / p.tpt, in_part = tile * kRows + (t - tile * p.tpt) * p.hg + head;
     auto row_of = [&](int i) {
@@ -1530,7 +1530,8 @@ cudaError_t launch(const ChunkArgs& a, void* ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(kCtas), dim3(C::kThreads), C::kSmem, st, mq, p, status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_chunk_join_kernel<D>, dim3(kCtas, kJoinCtas), dim3(256), 0, st, p);
+  const int y = (plan.part_rows + 7) / 8;
+  return launch_pdl(attn_chunk_join_kernel<D>, dim3(kCtas, y < kJoinCtas ? y : kJoinCtas), dim3(256), 0, st, p);
 }
 
 template <bool kI8>

@@ -127,3 +127,30 @@ def test_shapes_that_do_not_fit(world):  # noqa: F811
     with pytest.raises(ValueError, match="head_dim"):
         P.attn_chunk(new((4, 4, 128), bf16), cache, t["table"], t["lens"], t["cu_q"])
     assert not world.calls
+
+
+def test_a_rope_in_two_threads(world):  # noqa: F811
+    """Each thread has a struct of its own: positions of one call are not another's."""
+    import threading
+
+    P, _, r, t = _things(world)
+    rope = P.Rope(**r)
+    import torch
+
+    other = world.new((4,), torch.int32)
+    got, both = {}, threading.Barrier(2)
+
+    def call(name, pos):
+        at = rope._at(pos, 4, 64, 0)
+        both.wait()
+        s = P._RopeStruct.from_address(at)
+        got[name] = at, s.pos, s.axes
+        both.wait()
+
+    threads = [threading.Thread(target=call, args=a) for a in (("a", t["pos"]), ("b", other))]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert got["a"][0] != got["b"][0]
+    assert got["a"][1:] == (t["pos"].data_ptr(), 2) and got["b"][1:] == (other.data_ptr(), 1)
