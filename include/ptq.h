@@ -456,7 +456,7 @@ typedef struct ptq_kv_cache {
  *          apart (so they may be columns of a fused projection's output);
  *          16-byte aligned, strides a multiple of 16 bytes
  *   slots  T int32 slots (device); a slot outside the cache skips its token.
- *          Two tokens with one slot leave either token's values there.
+ *          Two tokens with one slot may leave some values (and scales) of each there.
  * cache: a HOST struct, read during the call only.  T = 0 is a no-op.
  * Errors: PTQ_ERR_NULL, PTQ_ERR_SHAPE, PTQ_ERR_ALIGN, PTQ_ERR_VALUE (dtype or
  * type), PTQ_ERR_UNSUPPORTED (head_dim), PTQ_ERR_CUDA. */
@@ -560,7 +560,7 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_attn_prefill(
  *             Its angles are right to 2^-31 of a turn at any position.
  *   axis      rotary_dim / 2 int8: which axis of the positions pair i goes by
  *             (text, or time, height and width of images and video); NULL: all
- *             by axis 0.  A pair whose axis is not in [0, axes) is not turned.
+ *             by axis 0.  A pair whose axis is not in [0, axes) has the angle 0.
  *   pos       axes x T int32, an axis pos_stride elements after the one before
  *   rotary_dim  the head's first values that are turned: a multiple of 8, 0 to
  *             head_dim (0: none; inv_freq and pos may then be NULL)
@@ -606,7 +606,7 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_qk_rope(const ptq_rope* rope, const void* q
  * from fp32 to the cache's type, with no rounding to dtype between.
  *   q, k, v, slots and q_out as for ptq_qk_rope and ptq_kv_write: a slot
  *   outside the cache skips its token's key and value (not its query), and two
- *   tokens with one slot leave either's values there.
+ *   tokens with one slot may leave some values (and scales) of each there.
  * Errors as ptq_qk_rope and ptq_kv_write. */
 PTQ_API PTQ_NODISCARD ptq_status ptq_kv_append(const ptq_kv_cache* cache, const ptq_rope* rope,
                                                const void* q, const void* k, const void* v,

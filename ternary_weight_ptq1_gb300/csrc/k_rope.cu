@@ -214,27 +214,31 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           for (int u = 0; u < kRows; ++u) ss[u] += __shfl_xor_sync(~0u, ss[u], i);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          if (__builtin_expect(__any_sync(~0u, !(ss[u] < __int_as_float(0x7f800000))), 0)) {
-            // the squares of a row of finite values overflow: over a power of two
+          const float mean = ss[u] * (1.0f / D) + a.eps;
+          float inv = rsqrtf(mean);
+          // squares that vanish count below 2^-124; sums may be over the range
+          const bool small = mean < 0x1p-124f, rare = small || !(mean < __int_as_float(0x7f800000));
+          if (__builtin_expect(__any_sync(~0u, rare), 0)) {
+            // again over a power of two
+            const float by = small ? 0x1p96f : 0x1p-70f;
             float m = 0.0f, v[kVec], s2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) unpair(x[u][i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(v[i]));
+            for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(v[i])), s2 = fmaf(v[i] * by, v[i] * by, s2);
 #pragma unroll
-            for (int i = kLanes / 2; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
-            const bool over = !(ss[u] < __int_as_float(0x7f800000)) && m < __int_as_float(0x7f800000);
+            for (int i = kLanes / 2; i > 0; i >>= 1) {
+              m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
+              s2 += __shfl_xor_sync(~0u, s2, i);
+            }
+            if (rare && m < __int_as_float(0x7f800000)) {
+              // x by (1 / root) by the power or the other way round: no product loses bits
+              const float of = rsqrtf(s2 * (1.0f / D) + a.eps * by * by);
+              inv = small ? of : by;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) s2 = fmaf(v[i] * 0x1p-96f, v[i] * 0x1p-96f, s2);
-#pragma unroll
-            for (int i = kLanes / 2; i > 0; i >>= 1) s2 += __shfl_xor_sync(~0u, s2, i);
-            if (over) {
-              ss[u] = s2;  // (eps is far below a unit of it)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], pair(0x1p-96f, 0x1p-96f));
+              for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], small ? pair(by, by) : pair(of, of));
             }
           }
-          const float inv = rsqrtf(ss[u] * (1.0f / D) + a.eps);
           const uint64_t ii = pair(inv, inv);
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[u][i] = mul2(mul2(x[u][i], ii), g[i]);

@@ -182,6 +182,27 @@ def test_rows_of_zeros_large_and_infinite_values(P):
     assert np.isfinite(y[1:3]).all() and np.isfinite(_host(ko)).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -120, 1.5 * 2.0 ** 127])
+def test_any_eps_and_any_size_of_values(P, D, eps):
+    """Squares that vanish beside an eps that is as small, and sums over fp32's range.
+    Results under its normal values round, five times at most (by the power, the gain, two
+    products, a sum; gains are under 2), to multiples of 2^-149: up to 8 of them more."""
+    sizes = (2.0 ** -148, 1e-40, 2.0 ** -75, 2.0 ** -70, 1e-10, 1e18, 3e38)
+    c = Case(len(sizes), 3, 1, D, D, "f32")
+    for t, size in enumerate(sizes):
+        x = c.x[t].astype(np.float64)
+        c.x[t] = x * (size / np.abs(x).max(-1, keepdims=True))
+    c.x[1, 0], c.x[6, 1, 7] = 0.0, 1e-25
+    assert np.abs(c.gq).max() < 2
+    q, k, _ = c.parts()
+    rope = P.Rope(_dev(c.inv), q_gain=_dev(c.gq), k_gain=_dev(c.gk), eps=eps)
+    for y, x, g in zip(P.qk_rope(rope, q, k, c.positions()), (c.x[:, :3], c.x[:, 3:4]), (c.gq, c.gk), strict=True):
+        ref, size = R.turned(x, g, eps, c.pos, c.inv, None, False)
+        err, b = np.abs(_host(y) - ref), R.bound(ref, size, False) + 8 * 2.0 ** -149
+        assert (err <= b).all(), (np.argwhere(err > b)[:4], err[err > b][:4], b[err > b][:4])
+
+
 def test_a_side_without_heads(P):
     c = Case(5, 4, 2, 128, 128, "f32")
     q, k, _ = c.parts()
