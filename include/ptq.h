@@ -648,7 +648,7 @@ PTQ_API size_t ptq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t q_h
  *           of those the last `window` (p - window < j) and the first `sinks`
  *           (j < sinks).  With lens[b] < nq the first queries see none.
  *   out     Tq x q_heads x head_dim bf16, contiguous; lse: Tq x q_heads fp32, or
- *           NULL.  Rows of no sequence are not written.
+ *           NULL.  Rows of no sequence are not written.  Neither may overlap q.
  * A query that sees a token of a page outside the cache is NaN (nothing is read
  * for it); entries that no query of the sequence sees are not used.  A key or
  * value that a query does not see has no effect on it, NaN and infinities
