@@ -21,7 +21,7 @@
 // that make four pairs of its own, so neither the rotation nor its loads and stores need
 // an exchange, and its cosines and sines are made once.  (A CTA with a table of four
 // tokens' angles in shared memory, whose threads took the rows in any order: 67 us for 38
-// on 8192 tokens of 40 + 8 heads of 128, 94 for 43 into a bf16 cache, 369 for 168 on 20,011
+// on 8192 tokens of 40 + 8 heads of 128, 94 for 43 into a bf16 cache, 369 for 154 on 20,011
 // of 24 + 4 of 256 into int8 and out again.)  More CTAs an SM, which leave fewer registers,
 // lost: 41 us with five of 128 threads, 46 with six.
 //
@@ -89,6 +89,12 @@ __device__ __forceinline__ void store4(char* p, const uint64_t* x) {
     *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
 }
 __device__ __forceinline__ uint64_t swapped(uint64_t v) { return v >> 32 | v << 32; }
+
+// A mean of squares in which some that vanished may count, or over the range (or NaN).
+constexpr float kLeast = 0x1p-124f;
+__device__ __forceinline__ bool is_rare(float mean) {
+  return __float_as_uint(mean) - __float_as_uint(kLeast) >= 0x7f800000u - __float_as_uint(kLeast);
+}
 
 template <Act T, int D, Dest kDest>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args p) {
@@ -212,14 +218,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         for (int i = kLanes / 2; i > 0; i >>= 1)
 #pragma unroll
           for (int u = 0; u < kRows; ++u) ss[u] += __shfl_xor_sync(~0u, ss[u], i);
+        float inv[kRows];
+        bool any = false;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          const float mean = ss[u] * (1.0f / D) + a.eps;
-          float inv = rsqrtf(mean);
-          // squares that vanish count below 2^-124; sums may be over the range
-          const bool small = mean < 0x1p-124f, rare = small || !(mean < __int_as_float(0x7f800000));
-          if (__builtin_expect(__any_sync(~0u, rare), 0)) {
+          ss[u] = ss[u] * (1.0f / D) + a.eps;
+          inv[u] = rsqrtf(ss[u]);
+          any |= is_rare(ss[u]);
+        }
+        if (__builtin_expect(__any_sync(~0u, any), 0)) {
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
             // again over a power of two
+            const bool small = ss[u] < kLeast;
             const float by = small ? 0x1p96f : 0x1p-70f;
             float m = 0.0f, v[kVec], s2 = 0.0f;
 #pragma unroll
@@ -231,15 +242,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
               m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
               s2 += __shfl_xor_sync(~0u, s2, i);
             }
-            if (rare && m < __int_as_float(0x7f800000)) {
+            if (is_rare(ss[u]) && m < __int_as_float(0x7f800000)) {
               // x by (1 / root) by the power or the other way round: no product loses bits
               const float of = rsqrtf(s2 * (1.0f / D) + a.eps * by * by);
-              inv = small ? of : by;
+              inv[u] = small ? of : by;
 #pragma unroll
               for (int i = 0; i < 4; ++i) x[u][i] = mul2(x[u][i], small ? pair(by, by) : pair(of, of));
             }
           }
-          const uint64_t ii = pair(inv, inv);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const uint64_t ii = pair(inv[u], inv[u]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[u][i] = mul2(mul2(x[u][i], ii), g[i]);
         }
