@@ -454,9 +454,10 @@ __device__ __forceinline__ uint32_t low_bits(int n) {  // n below 0: none, above
   return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
 }
 
-// A row's output, w0 O0 + w1 O1 (a weight of 0: that O may be anything), from TMEM, as bf16 or
-// (a part) fp32; whether it is finite.  how: 1 both O, 2 the row is one, 4 a part, 8 NaN.
-// (Called: inlined its registers are kept from the scores', which then spill.)
+// A row's output, w0 O0 + w1 O1, from TMEM, as bf16 or (a part) fp32; whether it is finite.
+// how: 1 both O, 2 the row is one, 4 a part, 8 NaN, 16 O0 has a key's product (else it may be
+// anything), 32 O1 has one.  (A weight says neither: it is 0 also where an O's scores are far
+// below the other's, and 0 times a value that is not finite is NaN.)  (Called: inlined its registers are kept from the scores', which then spill.)
 template <int D>
 __device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w1, char* to, unsigned how) {
   uint64_t checked = pair(0.0f, 0.0f);
@@ -468,11 +469,11 @@ __device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w
     tmem_ld16(o0 + c, o);
     if (__any_sync(~0u, how & 1)) tmem_ld16(o1 + c, x);  // (of the whole warp)
     tmem_wait_ld();
-    if (w0 == 0.0f) {
+    if (!(how & 16)) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[e] = 0u;
     }
-    if (w1 == 0.0f) {
+    if (!(how & 32)) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = 0u;
     }
@@ -1379,7 +1380,6 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
         w0 *= inv, w1 *= inv;
       }
-      if (l0 == 0.0f) w0 = 0.0f;
       const int o_mine = split ? 0 : s;  // the O that this warp reads first
       const bool has0 = (o_mine ? n1 : n0) > 0;
       if (has0) ok = __all_sync(~0u, bar_wait(o_full + o_mine, outs[o_mine] & 1, state));
@@ -1388,9 +1388,10 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       fence_after();
       bool fine = true;
       if (!idle)
-        fine = put_row<D>(o_at + o_mine * D, o_at + D, has0 ? w0 : 0.0f, two ? w1 : 0.0f,
+        fine = put_row<D>(o_at + o_mine * D, o_at + D, w0, w1,
                           parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D),
-                          (two ? 1u : 0u) | (mine ? 2u : 0u) | (parts ? 4u : 0u) | (odd ? 8u : 0u));
+                          (two ? 1u : 0u) | (mine ? 2u : 0u) | (parts ? 4u : 0u) | (odd ? 8u : 0u) |
+                              (has0 && l0 != 0.0f ? 16u : 0u) | (two && l1 != 0.0f ? 32u : 0u));
       // the next item's products may come
       fence_before();
       __syncwarp();
