@@ -56,7 +56,7 @@
 // A key that a row does not see has P = 0, and 0 times a non-finite value is NaN.
 // Over int8 a row is not finite by its scale: such scales enter as 0, and rows that
 // see one are made NaN.  Over bf16 rows whose sum is finite and whose output is not
-// are looked at, and computed again where no value that they see explains it.
+// are looked at, and computed again where no value that they see explains a dimension of it.
 //
 // Every wait is bounded, to some 6 s in which no warp computes rows again; one that
 // runs out raises the device status word and the CTA drains what it has in flight and
@@ -331,20 +331,32 @@ __device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t r
 
 // The rows `again` of a warp (a lane a row) whose sum is finite and whose output is not.  A
 // value that a row sees and that is not finite leaves its column so, rightly.  The row is
-// computed again where a column has none of those, but one among the hidden tokens of its
-// tiles [v0, v1) (0 times it is NaN), and where no value explains it (P may be 2^8 times a
-// probability, and the sums of large values overflow).  8192 tokens, 8 x 5 heads of 128, 0.56 ms: with
-// the first token's value infinite, which all rows see, 1.3 (21 when each row was looked at alone),
-// with the middle one's 26 (426), with the last one's 37 (184).
+// computed again where a column of its output is not finite and has none of those: a hidden
+// one (0 times it is NaN) did it, or the sum of large values overflowed (P may be 2^8 times a
+// probability).  The tokens of [v0, v1) that all of the rows see are looked at together, until
+// they explain every column.  8192 tokens, 8 x 5 heads of 128, 0.56 ms: with the first token's value
+// infinite, which all rows see, 0.75 (21 when each row was looked at alone), with the middle one's 26
+// (426), with the last one's 37 (184).
 template <int D>
-__device__ __noinline__ unsigned spoilt(const Args& p, const Item& it, unsigned again, Sight sight, int v0, int v1) {
+__device__ __noinline__ unsigned spoilt(const Args& p, const Item& it, unsigned again, int64_t row, const float* part,
+                                        Sight sight, int v0, int v1) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x & 31;
   const bool mine = again >> lane & 1;
-  // tokens that all of the rows see, [sinks, from) left out, and the others of the tiles
-  const int end = min(v1, __reduce_min_sync(~0u, mine ? sight.end : v1)),
-            from = __reduce_max_sync(~0u, mine ? sight.from : 0), sinks = sight.sinks;
-  const int gap0 = max(v0, min(sinks, end)), gap1 = min(from, end);
+  // this lane's columns (a bit each) of row `who` as it was written that are not finite
+  auto bad_of = [&](int who) {
+    const int64_t r = __shfl_sync(~0u, row, who);
+    const volatile float* from =
+        reinterpret_cast<const float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(part), who));
+    const volatile uint16_t* out = p.a.out + r * D + lane * N;
+    unsigned bad = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float y = from ? from[lane * N + i] : __uint_as_float((uint32_t)out[i] << 16);
+      if (!(fabsf(y) < -kNegInf)) bad |= 1u << i;
+    }
+    return bad;
+  };
   auto look = [&](int v, unsigned& found) {  // this lane's columns of token v
     const int64_t at = cached_row(p.a, it, v);
     float y[N];
@@ -355,35 +367,35 @@ __device__ __noinline__ unsigned spoilt(const Args& p, const Item& it, unsigned 
         if (!(fabsf(y[i]) < -kNegInf)) found |= 1u << i;
     }
   };
-  unsigned odd = 0, known = 0;
-#pragma unroll 4
-  for (int v = gap0; v < gap1; ++v) look(v, odd);
-#pragma unroll 4
-  for (int v = max(v0, end); v < v1; ++v) look(v, odd);
+  unsigned all = 0, known = 0;
+#pragma unroll 1
+  for (unsigned rest = again; rest; rest &= rest - 1) all |= bad_of(__ffs(rest) - 1);
+  // tokens that all of the rows see, [sinks, from) left out
+  const int end = min(v1, __reduce_min_sync(~0u, mine ? sight.end : v1)),
+            from = __reduce_max_sync(~0u, mine ? sight.from : 0), sinks = sight.sinks;
+  const int gap0 = max(v0, min(sinks, end)), gap1 = min(from, end);
 #pragma unroll 1
   for (int v = v0; v < end; v += 8) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (v + e < end && !(v + e >= gap0 && v + e < gap1)) look(v + e, known);
-    if (__any_sync(~0u, known) && !__any_sync(~0u, odd & ~known)) break;
+    if (!__any_sync(~0u, all & ~known)) return 0u;
   }
-  if (!__any_sync(~0u, odd & ~known)) return __any_sync(~0u, known) ? 0u : again;  // the same for all rows
   unsigned todo = 0;
 #pragma unroll 1
   for (; again; again &= again - 1) {
     const int who = __ffs(again) - 1;
+    const unsigned bad = bad_of(who) & ~known;
+    if (!__any_sync(~0u, bad)) continue;
     const Sight s{__shfl_sync(~0u, sight.end, who), __shfl_sync(~0u, sight.from, who), sinks};
-    unsigned hid = 0, seen = known;
-    auto both = [&](int v) {
-      unsigned found = 0;
-      look(v, found);
-      if (s.sees(v)) seen |= found; else hid |= found;
-    };
+    unsigned seen = 0;  // by this row among the others
 #pragma unroll 4
-    for (int v = gap0; v < gap1; ++v) both(v);
+    for (int v = gap0; v < gap1; ++v)
+      if (s.sees(v)) look(v, seen);
 #pragma unroll 4
-    for (int v = max(v0, end); v < v1; ++v) both(v);
-    if (__any_sync(~0u, hid & ~seen) || !__any_sync(~0u, seen)) todo |= 1u << who;
+    for (int v = max(v0, end); v < v1; ++v)
+      if (s.sees(v)) look(v, seen);
+    if (__any_sync(~0u, bad & ~seen)) todo |= 1u << who;
   }
   return todo;
 }
@@ -392,7 +404,7 @@ template <int D, bool kI8>
 __device__ __noinline__ void repair(const Args& p, const Item& it, unsigned again, int64_t row, Sight sight, int v0,
                                     int v1, float* part, float2* ml, volatile int* state) {
   const Busy busy(state);
-  if constexpr (!kI8) again = spoilt<D>(p, it, again, sight, v0, v1);
+  if constexpr (!kI8) again = spoilt<D>(p, it, again, row, part, sight, v0, v1);
 #pragma unroll 1
   for (; again; again &= again - 1) {
     const int who = __ffs(again) - 1;
