@@ -47,8 +47,9 @@
 // together.  The lengths are on the device: every CTA adds them up (in closed form
 // for a sequence) and one of its warps walks its stretch.  A run that is cut
 // leaves its sums, relative to their maxima, in the workspace, and a second kernel
-// joins them in order.  (A start of 128 keys: 64 sequences over int8 231 us, of 256 204,
-// of 512 202, of 1024 217; three chunks 613, 597, 590, 601.)
+// joins them in order; a CTA joins those of its own part every 2^15 keys.  (A start of 128
+// keys: 64 sequences over int8 231 us, of 256 204, of 512 202, of 1024 217; three chunks 613, 597,
+// 590, 601.)
 //
 // What runs between two products is kept short: an issuing warp that works out its places
 // after its waits, or votes on each wait, takes 610 us for 518 at 8192 tokens.
@@ -77,6 +78,12 @@ constexpr int kLead = 512;   // cost of a run's start, in keys
 constexpr int kLeast = 256;  // the shortest stretch of a CTA
 constexpr int kScales = 8;   // tiles whose scales are in shared memory
 constexpr int kItems = 4;    // items on their way from the warp that plans to the others
+// A sum of n terms made one after the other is off by up to n / 2 units of 2^-23 where it truncates
+// (as the tensor core does, 16 keys a term: 2^20 keys of one score were off by 1.5%), n / 2 half ones
+// where it rounds.  So O and the row's four sums go over kPiece tiles of keys, 2^15, off by
+// 2^-13 and 2^-12 at most, and are then joined.  (A row's sums joined every 16 tiles beside: 8192 tokens
+// of 4 x 6 of 256 715 us for 703.)
+constexpr int kPiece = 256;
 
 template <int D, bool kI8>
 struct Cfg {
@@ -151,7 +158,7 @@ struct Args {
 };
 
 // A CTA's next piece of work: the Q tiles of one run and head block, over tiles
-// of the keys that the run sees.  b < 0: no more.
+// of the keys that the run sees, kPiece at most (the next piece goes on from its sums).  b < 0: no more.
 struct Item {
   int b, q0, nq, first;  // the sequence, its first query's row, its queries, the run's first
   int h, hq0;            // kv head, first query head
@@ -160,8 +167,11 @@ struct Item {
   int t0, tiles;         // this part's tiles
   int n[2];              // tiles of each Q tile, or (split) of each half
   int split;             // one Q tile, its key tiles dealt out to both S
-  int slot;              // part of the workspace; -1: the whole run
+  int slot;              // part of the workspace and kWhole, kOnto; -1: the whole run at once
+  int r0;                // the run's first tile in this CTA
 };
+// The item ends its run, all of which is this CTA's; the part has the sums of tiles [r0, t0).
+constexpr int kWhole = 2, kOnto = 4;
 static_assert(sizeof(Item) <= 64, "its place in shared memory");
 
 // ---- the order of the work -----------------------------------------------------------
@@ -256,7 +266,9 @@ __device__ __forceinline__ int64_t cached_row(const ChunkArgs& a, const Item& it
 // One query row by a warp over the run's tokens [v0, v1): 32 keys at a time, a
 // lane's own key for the scores and its own columns for the output.  Where the
 // weights' sum is large the sums of values near the largest overflow although
-// their mean does not: then again with weights 2^-40 times as large.
+// their mean does not: then again with weights 2^-40 times as large.  Sums go over kRowKeys
+// keys and are then joined.
+constexpr int kRowKeys = 4096;
 template <int D, bool kI8>
 __device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t row, Sight sight, int v0, int v1,
                                         float* part, float2* ml) {
@@ -265,15 +277,17 @@ __device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t r
   const int lane = threadIdx.x & 31;
   const int64_t t = row / a.Hq;
   const uint16_t* q = a.q + t * a.q_stride + (row - t * a.Hq) * D;
-  RowState<D> s;
-  float l, small = 1.0f;
+  const int stop = min(v1, sight.end);
+  RowState<D> all;
+  float small = 1.0f;
 #pragma unroll 1
   for (;;) {
-    s = RowState<D>();
+    all = RowState<D>();
+    RowState<D> s;
 #pragma unroll 1
-    for (int v = v0; v < min(v1, sight.end); v += 32) {
+    for (int v = v0; v < stop; v += 32) {
       const int mine = v + lane;
-      const bool in = mine < v1 && sight.sees(mine);
+      const bool in = mine < stop && sight.sees(mine);
       const int64_t at = in ? cached_row(a, it, mine) : -1;
       float x = in ? __int_as_float(0x7fc00000) : kNegInf, vs = 1.0f;
       if (at >= 0) {
@@ -307,25 +321,29 @@ __device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t r
           }
         }
       }
-    }
-    l = s.l;
+      if ((v - v0) % kRowKeys == kRowKeys - 32 || stop - v <= 32) {
+        float l = s.l;
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+        for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+        all.join(s.m, l, s.o);
+        s = RowState<D>();
+      }
+    }
     bool fine = true;
 #pragma unroll
-    for (int i = 0; i < N; ++i) fine = fine && fabsf(s.o[i]) < -kNegInf;
-    if (small != 1.0f || !(l == l) || __all_sync(~0u, fine)) break;
+    for (int i = 0; i < N; ++i) fine = fine && fabsf(all.o[i]) < -kNegInf;
+    if (small != 1.0f || !(all.l == all.l) || __all_sync(~0u, fine)) break;
     small = 0x1p-40f;
   }
   if (part) {
-    if (lane == 0) *ml = make_float2(small == 1.0f ? s.m : s.m + 40.0f, l * small);
+    if (lane == 0) *ml = make_float2(small == 1.0f ? all.m : all.m + 40.0f, all.l * small);
 #pragma unroll
-    for (int i = 0; i < N; ++i) part[lane * N + i] = s.o[i];
+    for (int i = 0; i < N; ++i) part[lane * N + i] = all.o[i];
   } else {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * small);
+    const float inv = all.l == 0.0f ? 0.0f : 1.0f / (all.l * small);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      a.out[row * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(s.o[i] * inv));
+      a.out[row * D + lane * N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(all.o[i] * inv));
   }
 }
 
@@ -470,8 +488,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) {  // n below 0: none, above
 // how: 1 both O, 2 the row is one, 4 a part, 8 NaN, 16 O0 has a key's product (else it may be
 // anything), 32 O1 has one.  (A weight says neither: it is 0 also where an O's scores are far
 // below the other's, and 0 times a value that is not finite is NaN.)  (Called: inlined its registers are kept from the scores', which then spill.)
-template <int D>
-__device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w1, char* to, unsigned how) {
+template <int D, bool kOnto>
+__device__ __forceinline__ bool put_columns(uint32_t o0, uint32_t o1, float w0, float w1, char* to, unsigned how,
+                                            const float* before, float wb) {
   uint64_t checked = pair(0.0f, 0.0f);
   const uint64_t ww0 = pair(w0, w0), ww1 = pair(w1, w1), zero2 = pair(0.0f, 0.0f);
   __syncwarp();
@@ -493,6 +512,9 @@ __device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w
     for (int e = 0; e < 16; e += 2) {
       uint64_t y = mul2(pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ww0);
       y = fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), ww1, y);
+      if constexpr (kOnto) {
+        if (how & 2) y = fma2(pair(before[c + e], before[c + e + 1]), pair(wb, wb), y);
+      }
       checked = fma2(y, zero2, checked);  // 0 as long as every value is finite
       float y0, y1;
       unpair(y, y0, y1);
@@ -518,6 +540,38 @@ __device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w
   float lo, hi;
   unpair(checked, lo, hi);
   return lo + hi == 0.0f;
+}
+template <int D>
+__device__ __noinline__ bool put_row(uint32_t o0, uint32_t o1, float w0, float w1, char* to, unsigned how) {
+  return put_columns<D, false>(o0, o1, w0, w1, to, how, nullptr, 0.0f);
+}
+
+// The output of a piece whose run has pieces before it in this CTA: w0 O0 + w1 O1, of maximum m and
+// sum l, joined with the part's sums; back into the part, or the row's output.  Bits: 1 all is finite,
+// 2 the row is NaN by a value's scale, 4 its sum is no NaN.
+template <int D, bool kI8>
+__device__ __noinline__ unsigned put_row_onto(const Args& p, uint32_t o0, uint32_t o1, float w0, float w1, float m, float l,
+                                              unsigned how, int64_t part_row, int64_t out_row) {
+  float* part = p.part + part_row * D;
+  float wb = 0.0f;
+  if (how & 2) {
+    const float2 before = p.ml[part_row];
+    const float top = fmaxf(m, before.x), f = weight(m, l, top);
+    wb = weight(before.x, before.y, top);
+    w0 *= f, w1 *= f;
+    l = l * f + before.y * wb;
+    if (kI8 && !(part[0] == part[0])) how |= 8;  // (over int8 a row that sees such a scale is NaN)
+    if (how & 4) {
+      p.ml[part_row] = make_float2(top, l);
+    } else {
+      const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+      w0 *= inv, w1 *= inv, wb *= inv;
+      if (p.a.lse) p.a.lse[out_row] = l == 0.0f ? kNegInf : (top + __log2f(l)) * kLn2;
+    }
+  }
+  char* to = how & 4 ? reinterpret_cast<char*>(part) : reinterpret_cast<char*>(p.a.out + out_row * D);
+  const bool fine = put_columns<D, true>(o0, o1, w0, w1, to, how, part, wb);
+  return (fine ? 1u : 0u) | (how & 8 ? 2u : 0u) | (l == l ? 4u : 0u);
 }
 
 template <int D, bool kI8>
@@ -691,42 +745,62 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       r = lo;
       start += cost_of(p, s, r);
     }
+    Item it;
+    it.b = -1;
+    int t1 = 0;    // the end of the run's tiles in this CTA
+    int part = 0;  // where its sums go if they are not the whole run's
     while (ok) {
-      Item it;
-      it.b = -1;
-      while (start < u1) {
-        if (r * (int64_t)p.run >= s.nq) {  // the next head block, or sequence with queries
-          r = 0;
-          if (++hb == p.heads) {
-            hb = 0;
-            for (++seq;; seq += 32) {
-              const bool some = seq + lane < a.B && seq_of(a, seq + lane).nq > 0;
-              const unsigned which = __ballot_sync(~0u, some);
-              if (which) {
-                seq += __ffs(which) - 1;
-                break;
+      if (it.b >= 0 && it.t0 + it.tiles < t1) {
+        it.t0 += it.tiles;  // the run's next piece
+      } else {
+        it.b = -1;
+        while (start < u1) {
+          if (r * (int64_t)p.run >= s.nq) {  // the next head block, or sequence with queries
+            r = 0;
+            if (++hb == p.heads) {
+              hb = 0;
+              for (++seq;; seq += 32) {
+                const bool some = seq + lane < a.B && seq_of(a, seq + lane).nq > 0;
+                const unsigned which = __ballot_sync(~0u, some);
+                if (which) {
+                  seq += __ffs(which) - 1;
+                  break;
+                }
+                if (seq + 32 >= a.B) break;  // (start is u1 before that)
               }
-              if (seq + 32 >= a.B) break;  // (start is u1 before that)
+              s = seq_of(a, min(seq, (int)a.B - 1));
             }
-            s = seq_of(a, min(seq, (int)a.B - 1));
           }
+          it.nv = tokens_of(p, s, r, &it.skip);
+          const int n = tiles_of(it.nv);
+          it.t0 = it.r0 = tile_at(u0, start, n);
+          t1 = tile_at(u1, start, n);
+          const int64_t begin = start;
+          const int this_run = r++;
+          start += (int64_t)kLead + it.nv;
+          if (it.t0 >= t1 && !(n == 0 && begin >= u0)) continue;
+          it.b = seq;
+          it.q0 = s.q0, it.nq = s.nq, it.nk = s.nk;
+          it.first = this_run * p.run;
+          it.hq0 = hb * p.hg;
+          it.h = p.by_G(it.hq0);
+          it.split = kTiles == 2 && it.first + p.tpt >= it.nq;
+          part = begin < u0 ? 0 : 1;
+          if (it.t0 == 0 && t1 < n && lane == 0) {
+            Note note;
+            note.row = (int64_t)(it.q0 + it.first) * a.Hq + it.hq0;
+            note.tokens = min(p.run, it.nq - it.first);
+            note.slot = part;
+            note.last = (int)((begin + kLead + (int64_t)(n - 1) * kKeys) / per);
+            p.note[blockIdx.x] = note;
+          }
+          break;
         }
-        it.nv = tokens_of(p, s, r, &it.skip);
-        const int n = tiles_of(it.nv);
-        it.t0 = tile_at(u0, start, n);
-        const int t1 = tile_at(u1, start, n);
-        const int64_t begin = start;
-        const int this_run = r++;
-        start += (int64_t)kLead + it.nv;
-        if (it.t0 >= t1 && !(n == 0 && begin >= u0)) continue;
-        it.b = seq;
-        it.q0 = s.q0, it.nq = s.nq, it.nk = s.nk;
-        it.first = this_run * p.run;
-        it.hq0 = hb * p.hg;
-        it.h = p.by_G(it.hq0);
-        it.tiles = t1 - it.t0;
-        it.split = kTiles == 2 && it.first + p.tpt >= it.nq;
-        it.slot = it.tiles == n ? -1 : begin < u0 ? 0 : 1;
+      }
+      if (it.b >= 0) {
+        it.tiles = min(t1 - it.t0, kPiece);
+        const bool whole = it.r0 == 0 && t1 == tiles_of(it.nv), ends = it.t0 + it.tiles == t1, onto = it.t0 != it.r0;
+        it.slot = whole && ends && !onto ? -1 : part | (whole && ends ? kWhole : 0) | (onto ? kOnto : 0);
         if (kTiles == 1) {
           it.n[0] = it.tiles, it.n[1] = 0;
         } else if (it.split) {
@@ -736,15 +810,6 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           const int n0 = tiles_of(max(v, 0));
           it.n[0] = max(0, min(n0 - it.t0, it.tiles)), it.n[1] = it.tiles;
         }
-        if (it.slot >= 0 && it.t0 == 0 && lane == 0) {
-          Note note;
-          note.row = (int64_t)(it.q0 + it.first) * a.Hq + it.hq0;
-          note.tokens = min(p.run, it.nq - it.first);
-          note.slot = it.slot;
-          note.last = (int)((begin + kLead + (int64_t)(n - 1) * kKeys) / per);
-          p.note[blockIdx.x] = note;
-        }
-        break;
       }
       if (seen >= kItems)
         ok = __all_sync(~0u, bar_wait(item_free + seen % kItems, (seen / kItems - 1) & 1, state));
@@ -1380,17 +1445,19 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       const bool mine = row < p.hg * p.tpt && t < nq;
       const int slot = it.slot;
       const int64_t out_row = (int64_t)(it.q0 + t) * a.Hq + it.hq0 + my_head;
-      const bool parts = slot >= 0;
-      const int64_t part_row = ((int64_t)blockIdx.x * 2 + max(0, slot)) * p.part_rows + (split ? 0 : s * kRows) + row;
-      if (mine) {
-        if (parts)
-          p.ml[part_row] = make_float2(m, l);
-        else if (a.lse)
-          a.lse[out_row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * kLn2;
-      }
-      if (!parts) {
-        const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-        w0 *= inv, w1 *= inv;
+      const bool parts = slot >= 0 && !(slot & kWhole), onto = slot >= 0 && slot & kOnto;
+      const int64_t part_row = ((int64_t)blockIdx.x * 2 + (slot & 1)) * p.part_rows + (split ? 0 : s * kRows) + row;
+      if (!__builtin_expect(onto, 0)) {
+        if (mine) {
+          if (parts)
+            p.ml[part_row] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[out_row] = l == 0.0f ? kNegInf : (m + __log2f(l)) * kLn2;
+        }
+        if (!parts) {
+          const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+          w0 *= inv, w1 *= inv;
+        }
       }
       const int o_mine = split ? 0 : s;  // the O that this warp reads first
       const bool has0 = (o_mine ? n1 : n0) > 0;
@@ -1398,12 +1465,19 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       if (two) ok = ok && __all_sync(~0u, bar_wait(o_full + 1, outs[1] & 1, state));
       if (!ok) break;
       fence_after();
-      bool fine = true;
-      if (!idle)
-        fine = put_row<D>(o_at + o_mine * D, o_at + D, w0, w1,
-                          parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D),
-                          (two ? 1u : 0u) | (mine ? 2u : 0u) | (parts ? 4u : 0u) | (odd ? 8u : 0u) |
-                              (has0 && l0 != 0.0f ? 16u : 0u) | (two && l1 != 0.0f ? 32u : 0u));
+      bool fine = true, sound = l == l;  // the output is finite; its sum is no NaN
+      if (!idle) {
+        const unsigned how = (two ? 1u : 0u) | (mine ? 2u : 0u) | (parts ? 4u : 0u) | (odd ? 8u : 0u) |
+                             (has0 && l0 != 0.0f ? 16u : 0u) | (two && l1 != 0.0f ? 32u : 0u);
+        if (__builtin_expect(onto, 0)) {
+          const unsigned is = put_row_onto<D, kI8>(p, o_at + o_mine * D, o_at + D, w0, w1, m, l, how, part_row, out_row);
+          fine = is & 1, odd = is & 2, sound = is & 4;
+        } else {
+          fine = put_row<D>(o_at + o_mine * D, o_at + D, w0, w1,
+                            parts ? reinterpret_cast<char*>(p.part + part_row * D) : reinterpret_cast<char*>(a.out + out_row * D),
+                            how);
+        }
+      }
       // the next item's products may come
       fence_before();
       __syncwarp();
@@ -1413,13 +1487,13 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
       }
       outs[0] += n0 > 0, outs[1] += n1 > 0, joins += two;
       // rows whose sum is finite and whose output is not
-      const unsigned again = __ballot_sync(~0u, mine && !odd && !fine && l == l);
+      const unsigned again = __ballot_sync(~0u, mine && !odd && !fine && sound);
       if (__builtin_expect(again, 0)) {
         __syncwarp();
         const int n = split ? part_tiles : s ? n1 : n0;
         Item copy;
         copy.b = it.b, copy.h = it.h, copy.skip = it.skip;
-        repair<D, kI8>(p, copy, again, out_row, sight, t0 * kKeys, min((int)it.nv, (t0 + n) * kKeys),
+        repair<D, kI8>(p, copy, again, out_row, sight, it.r0 * kKeys, min((int)it.nv, (t0 + n) * kKeys),
                        parts ? p.part + part_row * D : nullptr, p.ml + part_row, state);
       }
     }
