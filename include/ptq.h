@@ -654,12 +654,13 @@ PTQ_API size_t ptq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t q_h
  * value that a query does not see has no effect on it, NaN and infinities
  * included; a seen value that is not finite leaves its dimension of the output
  * not finite.  dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED
- * (ptq_attn_decode serves it).  Over int8 the codes enter the products as they
- * are and the scales stay fp32; probabilities (times their value's scale) enter
- * the second product as bf16, and their sum is taken in fp32.  Results are bitwise
- * reproducible.  B = 0 or Tq = 0 is a no-op; Tq is under 2^30, B under 2^26; more
- * than 2^27 tokens that could be seen (a table row's, or a window's and the first
- * ones') are refused with PTQ_ERR_UNSUPPORTED.
+ * (ptq_attn_decode serves it).  Over int8 the codes enter the products exactly
+ * (2^-16 of them: no query is too large) and the scales stay fp32;
+ * probabilities (times their value's scale) enter the second product as bf16,
+ * and their sum is taken in fp32.  Results are bitwise reproducible.  B = 0 or
+ * Tq = 0 is a no-op; Tq is under 2^30, B under 2^26; more than 2^27 tokens that
+ * could be seen (a table row's, or a window's and the first ones') are refused
+ * with PTQ_ERR_UNSUPPORTED.
  * workspace as for ptq_attn_decode (NULL when ptq_attn_chunk_workspace_bytes is
  * 0).  Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for window and sinks. */
 PTQ_API PTQ_NODISCARD ptq_status ptq_attn_chunk(

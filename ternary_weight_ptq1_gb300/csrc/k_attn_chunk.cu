@@ -28,7 +28,7 @@
 // tiles, and rows that are not there are zeros.  (8192 tokens take 606 us with these
 // copies left out and 610 with them: the tensor memory accelerator, which wants
 // whole pieces of pages, would not be faster.)  Over int8 eight warps each copy codes
-// to a place of their own and spread them to bf16 for the products, which is exact
+// to a place of their own and spread them to bf16 for the products (times 2^-16), which is exact
 // (four take 286 us for 266 on the 64 sequences); a score is then multiplied by its
 // key's scale and a probability by its value's, in fp32, before P is rounded to bf16.
 //
@@ -77,6 +77,7 @@ constexpr int kCtas = (int)kSms;
 constexpr int kLead = 512;   // cost of a run's start, in keys
 constexpr int kLeast = 256;  // the shortest stretch of a CTA
 constexpr int kScales = 8;   // tiles whose scales are in shared memory
+constexpr float kCodeUp = 0x1p16f, kCodeDown = 0x1p-16f;  // codes enter the products as 2^-16 of themselves
 constexpr int kItems = 4;    // items on their way from the warp that plans to the others
 // A sum of n terms made one after the other is off by up to n / 2 units of 2^-23 where it truncates
 // (as the tensor core does, 16 keys a term: 2^20 keys of one score were off by 1.5%), n / 2 half ones
@@ -152,6 +153,9 @@ struct Args {
   int run;         // queries of an item: the Q tiles' tokens
   int part_rows;   // rows of a part
   Divider by_G, by_hg, by_run, by_page;
+  // A score in units of log2 is S times scale2 (over int8 also its key's scale, times key_up: 2^16 is in
+  // the one or, for a softmax_scale that leaves no room for it, in the other).
+  float scale2, key_up;
   float* part;     // [CTA][2][part_rows][D] output sums
   float2* ml;      // [CTA][2][part_rows], the maximum and sum they refer to
   Note* note;      // [CTA]
@@ -298,10 +302,10 @@ __device__ __noinline__ void attend_row(const Args& p, const Item& it, int64_t r
           row8<kI8>(a.c.k, at * D + d, k);
           row8<false>(q, d, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x = fmaf(k[i], y[i], x);
+          for (int i = 0; i < 8; ++i) x = fmaf(k[i], kI8 ? y[i] * kCodeDown : y[i], x);
         }
-        if constexpr (kI8) x *= __ldg(a.c.k_scale + at), vs = __ldg(a.c.v_scale + at);
-        x *= a.scale * kLog2e;
+        if constexpr (kI8) x *= __ldg(a.c.k_scale + at) * p.key_up, vs = __ldg(a.c.v_scale + at);
+        x *= p.scale2;
       }
       const float w = s.weigh(x) * (small * vs);
       const unsigned there = __ballot_sync(~0u, at >= 0);
@@ -459,12 +463,13 @@ __device__ __forceinline__ void copies_but(int n) {
   }
 }
 
-// Two of the four int8 codes of x as bf16: under the exponent of 128 a byte's low
-// seven bits are 128 + them and its top bit is 128 or 256, and their difference is the
-// code.
+// Two of the four int8 codes of x as bf16, times 2^-16: under the exponent of 2^-9 a byte's low
+// seven bits are 2^-9 + them and its top bit is 2^-9 or 2^-8, and their difference is the code.
+// q times such codes, added up over 256 columns, stays under 2^127 for any bf16 q (times whole codes it
+// passed 2^128 from q of 2^113 on), and is exact down to the smallest q, 2^-133: fp32 holds 2^-149.
 template <uint32_t kSel>
 __device__ __forceinline__ uint32_t codes(uint32_t x) {
-  const uint32_t w = __byte_perm(x, 0x43434343u, kSel), a = w & 0xff7fff7fu, b = w & 0xff80ff80u;
+  const uint32_t w = __byte_perm(x, 0x3b3b3b3bu, kSel), a = w & 0xff7fff7fu, b = w & 0xff80ff80u;
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -909,6 +914,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           float* sc = reinterpret_cast<float*>(smem + C::kOffScale) + slot * 2 * kKeys + key;
           bool odd = false;
           if (lane < kMine) {
+            if (p.key_up != 1.0f) sc[0] *= p.key_up;
             if (bads[at16] >> lane & 1) sc[0] = __int_as_float(0x7fc00000);
             odd = !(fabsf(sc[kKeys]) < -kNegInf);
             if (odd) sc[kKeys] = 0.0f;
@@ -1186,7 +1192,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
     const int s = kTiles == 1 ? 0 : warp >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int row = 32 * quarter + lane;
-    const float scale2 = a.scale * kLog2e;
+    const float scale2 = kI8 ? p.scale2 : a.scale * kLog2e;  // (read alone over bf16: at head_dim 256 719 us for 707)
     const uint32_t o_at = tmem + lanes + 2 * kKeys;
     // this row's token of the tile, and those of the warp's first and last row
     const int my_tok = p.by_hg(row), tok_lo = p.by_hg(32 * quarter), tok_hi = p.by_hg(32 * quarter + 31);
@@ -1427,7 +1433,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         outs[0] += n0 > 0, outs[1] += n1 > 0, joins += two;
         continue;
       }
-      float w0 = 1.0f, w1 = 0.0f, l1 = 0.0f;
+      float w0 = kI8 ? kCodeUp : 1.0f, w1 = 0.0f, l1 = 0.0f;
       const float l0 = l;
       if (two) {
         ok = __all_sync(~0u, bar_wait(ml_full, joins & 1, state));
@@ -1441,6 +1447,7 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
         w0 = weight(m, l0, top), w1 = weight(other.x, l1, top);
         l = l0 * w0 + l1 * w1;
         m = top;
+        if constexpr (kI8) w0 *= kCodeUp, w1 *= kCodeUp;
       }
       const bool mine = row < p.hg * p.tpt && t < nq;
       const int slot = it.slot;
@@ -1601,7 +1608,8 @@ cudaError_t launch(const ChunkArgs& a, void* ws, cudaStream_t st) {
   const Plan plan = plan_of(a.B, a.Tq, a.Hq, a.c.kv_heads, D);
   const int64_t G = a.Hq / a.c.kv_heads;
   Args p{a, (int)G, plan.hg, plan.tpt, (int)(a.c.kv_heads * (G / plan.hg)), C::kTiles * plan.tpt, plan.part_rows,
-         Divider(G), Divider(plan.hg), Divider(C::kTiles * plan.tpt), Divider(a.c.page_tokens), nullptr, nullptr, nullptr};
+         Divider(G), Divider(plan.hg), Divider(C::kTiles * plan.tpt), Divider(a.c.page_tokens), a.scale * kLog2e, 1.0f, nullptr, nullptr, nullptr};
+  if (kI8) (a.scale < 0x1p100f ? p.scale2 : p.key_up) *= kCodeUp;
   auto up = [](void* q) { return (reinterpret_cast<uintptr_t>(q) + 255) & ~(uintptr_t)255; };
   const size_t rows = (size_t)kCtas * 2 * plan.part_rows;
   p.part = reinterpret_cast<float*>(up(ws));
