@@ -925,14 +925,14 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(scales + slot);
         }
-      } else if (!v && !second && bads[at16]) {  // a key of no page: its scores are NaN
+      } else if (!v && !second && ok && bads[at16]) {  // a key of no page: its scores are NaN
         if (bads[at16] >> lane & 1)
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + key * 128 + ((key & 7) << 4)), "h"((short)0x7fc0) : "memory");
       }
       if (!v && !second) ++tiles_out;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + st);
+      if (lane == 0 && (kI8 || ok)) mbar_arrive(full + st);
       ++f;
     };
     // Of the unit's rows, idx / chunks is the row of this warp and idx % chunks the piece.
@@ -971,7 +971,8 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
             const char* from = base + (src < 0 ? 0 : src) * kRowBytes + (lane & 7) * 16;
             const uint32_t d = at + (64 * (4 * g / kHalf) + 4 * g % kHalf) * 128 + (p0 ^ (64 * (g & 1)));
 #pragma unroll
-            for (int o = 0; o < kOcts; ++o) copy16(d + o * kUnitRows * 128, from + 128 * o, src >= 0);
+            for (int o = 0; o < kOcts; ++o)
+              if (ok) copy16(d + o * kUnitRows * 128, from + 128 * o, src >= 0);
           }
         };
         using std::integral_constant;
@@ -1010,10 +1011,17 @@ __global__ void __launch_bounds__(Cfg<D, kI8>::kThreads, 1)
           const unsigned any = __ballot_sync(~0u, bad);
           if (lane == 0) bads[u & 15] = any;
         }
-        if (!kI8 && u >= C::kRing) ok = bar_wait(empty + u % C::kRing, (u / C::kRing - 1) & 1, state);
+        // (a lane whose wait ran out, now or for a unit before, copies nothing: hand_over says so for all)
+        if (!kI8 && u >= C::kRing) ok = ok && bar_wait(empty + u % C::kRing, (u / C::kRing - 1) & 1, state);
         issue(v, k, kTiles == 1 && v && x + C::kUnits < steps ? rows[1] : rows[0]);
         ++x;
       } else if (!ending && (f == u || __all_sync(~0u, item_ready()))) {
+        if constexpr (!kI8) {  // (units issued and not yet handed over may have run out of time)
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+        }
+        // A read that runs out of time issues nothing any more: either the work was at its end, or
+        // the products' own waits run out.  (To leave at once takes 830 us for 817 over int8.)
         ending = !read_item(it);
         x = 0, steps = ending ? 0 : 2 * C::kUnits * it.tiles;
         if (steps) page = page_of(token_of(0));
