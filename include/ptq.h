@@ -557,7 +557,8 @@ PTQ_API PTQ_NODISCARD ptq_status ptq_attn_prefill(
 /* How queries and keys are normed and rotated; a HOST struct, read during the
  * call only, whose pointers are device memory.
  *   inv_freq  rotary_dim / 2 fp32: pair i turns by pos * inv_freq[i] radians.
- *             Its angles are right to 2^-31 of a turn at any position.
+ *             Its angles are right to 2^-27 of a turn at any position, for
+ *             frequencies up to 2^32.
  *   axis      rotary_dim / 2 int8: which axis of the positions pair i goes by
  *             (text, or time, height and width of images and video); NULL: all
  *             by axis 0.  A pair whose axis is not in [0, axes) has the angle 0.

@@ -14,7 +14,8 @@
 // by 2^-24 of the angle: 0.03 at 2^19.  A frequency is made a 64-bit fraction
 // of a turn, inv_freq / (2 pi) modulo 1, by integer products (fp64 runs at two
 // operations a clock and SM); pos times that, modulo 2^64, is the angle without
-// its whole turns, off by 2^-33 turns at most.
+// its whole turns, off by 2^-33 turns at most (by as much again for a frequency of 2^32,
+// as 1 / (2 pi) has 96 bits).  With the integer's 2^-33 and fp32's 2^-28: under 2^-27.
 //
 // head_dim / 8 neighbouring threads have a token and go through its heads, kRows
 // rows at a time, the next ones on their way; a thread holds two pieces of four values
@@ -62,6 +63,17 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   const uint64_t t = shift >= 128 ? 0 : shift >= 0 ? (uint64_t)(p >> shift)
                                     : shift > -64 ? (uint64_t)p << -shift : 0;
   return b >> 31 ? 0 - t : t;
+}
+
+// Cosine and sine of at 2^-32 turns.  The nearest quarter comes off before the angle is rounded to
+// fp32, to 2^-28 of a turn then (a half turn's 31 bits rounded to 24 were off by 2^-26).
+__device__ __forceinline__ void turn(uint32_t at, float* c, float* s) {
+  const uint32_t quarters = (at + (1u << 29)) >> 30;
+  float x, y;
+  sincospif((float)(int32_t)(at - (quarters << 30)) * 0x1p-31f, &y, &x);
+  const float a = quarters & 1 ? y : x, b = quarters & 1 ? x : y;
+  *c = (quarters + 1) & 2 ? -a : a;
+  *s = quarters & 2 ? -b : b;
 }
 
 // Four values as they are in memory, and in fp32.
@@ -147,8 +159,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       cs[i] = 1.0f, sn[i] = 0.0f;  // a pair of no axis stays as it is
       if ((unsigned)ax < (unsigned)a.axes && there) {
         const int64_t pos = __ldg(a.pos + ax * a.pos_stride + t);
-        const uint64_t at = (uint64_t)pos * turns_of(f) + (1ull << 31);
-        sincospif((float)(int32_t)(at >> 32) * 4.656612873077393e-10f, sn + i, cs + i);  // 2^-31 half turns
+        turn((uint32_t)(((uint64_t)pos * turns_of(f) + (1ull << 31)) >> 32), cs + i, sn + i);
         if (!(fabsf(f) < __int_as_float(0x7f800000))) cs[i] = sn[i] = __int_as_float(0x7fc00000);
       }
     }
