@@ -828,7 +828,7 @@ def attn_decode(q, cache, table, lens, scale=None, out=None, lse=None, workspace
         q, out, lse, workspace, lambda: attn_decode_workspace_bytes(B, Hq, cache.kv_heads, D, dt), stream, on)
     tp, np_ = _dev(table, int32, "table", on), _dev(lens, int32, "lens", on)
     scale = D ** -0.5 if scale is None else scale
-    if window == 0:
+    if window == 0 and 0 <= sinks < 1 << 31:
         _check(load().ptq_attn_decode(qp, qs, cache._ref, tp, ts[1], np_, op, lp, B, Hq, scale, dt, wp, wb,
                                       _stream(stream, on)), "ptq_attn_decode")
     else:
