@@ -12,8 +12,9 @@ Every matrix is a rotated PTQ1_0 matrix (random here) applied by
 rotate_matmul, the feed-forward block is ffn, and between the projections the
 keys and values go through a paged int8 cache:
 
-  prompt   bf16: kv_append norms and turns queries and keys and stores the chunk,
-           attn_chunk reads the pages; the chunks of all requests are packed.
+  prompt   bf16: kv_append norms and turns queries and keys and stores the chunk; kv_read
+           returns the cached tokens, the chunk's among them, and attn_prefill sees them;
+           under a window attn_chunk reads the pages.  The chunks of all requests are packed.
   decode   fp32: kv_append stores the new token, attn_decode reads the pages.
 
 With --window W a token sees the last W tokens and the first 4.  At the end the
@@ -82,19 +83,29 @@ class Requests:
         self.lens = [0] * batch
         self.rope, self.window = layer.rope, dict(window=window, sinks=SINKS)
 
+    def places(self, starts, counts):
+        """Slots and positions of counts[b] tokens of each request from starts[b] on."""
+        b = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts)).cuda()
+        j = torch.cat([torch.arange(n, n + c) for n, c in zip(starts, counts)]).cuda()
+        return (self.table[b, j // PAGE] * PAGE + j % PAGE).to(torch.int32), j.to(torch.int32)
+
     def append(self, counts, q, k, v):
         """The next counts[b] tokens of each request into the cache; their queries, normed and turned."""
-        b = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts)).cuda()
-        j = torch.cat([torch.arange(n, n + c) for n, c in zip(self.lens, counts)]).cuda()
-        slots = (self.table[b, j // PAGE] * PAGE + j % PAGE).to(torch.int32)
+        slots, pos = self.places(self.lens, counts)
         self.lens = [n + c for n, c in zip(self.lens, counts)]
-        return P.kv_append(self.cache, self.rope, k, v, slots, j.to(torch.int32), q=q)
+        return P.kv_append(self.cache, self.rope, k, v, slots, pos, q=q)
 
     def prompt(self, counts):
         """attend() for the next counts[b] tokens of each request."""
         def attend(q, k, v):
             q = self.append(counts, q, k, v)
-            return P.attn_chunk(q, self.cache, self.table, int32(self.lens), offsets(counts), **self.window)
+            if self.window["window"]:
+                return P.attn_chunk(q, self.cache, self.table, int32(self.lens), offsets(counts), **self.window)
+            # Over int8 the rows read back are the faster way for chunks of prompts (8 x 5 heads of 128: 96 tokens
+            # after 96 in 11 us for attn_chunk's 22, 2048 after 2048 in 118 for 184); a few tokens each after
+            # thousands are attn_chunk's (32 x 16 after 2000 in 78 for 137).
+            k, v = P.kv_read(self.cache, self.places([0] * len(counts), self.lens)[0], dtype=q.dtype)
+            return P.attn_prefill(q, k, v, offsets(counts), offsets(self.lens))
         return attend
 
     def decode(self, q, k, v):
