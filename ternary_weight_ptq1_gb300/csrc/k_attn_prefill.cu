@@ -47,7 +47,7 @@
 // The values past a long sequence's end are cleared in shared memory; rows that a
 // value hidden from them has spoilt are computed again over the keys they see (8192
 // tokens, 8 x 5 heads of 128, 0.46 ms: with the last token's value infinite 18 ms,
-// with the first one's, which every row sees, 0.64).
+// with the first one's, which every row sees, 0.9).
 //
 // All roles' code together is larger than the instruction cache: what runs once
 // an item is kept short, in loops where that costs nothing (a fifth of the
@@ -230,9 +230,9 @@ __device__ __forceinline__ void attend_rows(const Args& p, int split, unsigned t
 // The rows `again` of a warp (a lane a row: query t, head hq, which sees `sees` of
 // the part's `end` keys from key0 on) whose output is not finite though their sum
 // is.  A value that a row sees and that is not finite leaves its column so, rightly.
-// The row is computed again where a column has none of those, but one among the
-// hidden keys of the tiles (0 times it is NaN), and where no value explains it
-// (P may be 2^8 times a probability, and the sums of large values overflow).
+// The row is computed again where a column of its output is not finite and has none of
+// those: a hidden key did it (0 times its value is NaN), or the sum of large values
+// overflowed (P may be 2^8 times a probability).
 template <int D>
 __device__ __noinline__ void repair(const Args& p, int split, unsigned again, int t, int hq, int sees, int h,
                                     int key0, int end, volatile int* state) {
@@ -240,50 +240,47 @@ __device__ __noinline__ void repair(const Args& p, int split, unsigned again, in
   const Busy busy(state);
   const PrefillArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  const bool mine = again >> lane & 1;
-  const int least = __reduce_min_sync(~0u, mine ? sees : end), most = __reduce_max_sync(~0u, mine ? sees : 0);
+  const int most = __reduce_max_sync(~0u, again >> lane & 1 ? sees : 0);
   const uint16_t* value = a.v + (int64_t)key0 * a.v_stride + (int64_t)h * D + lane * N;
-  // of this lane's columns: the last hidden key and the first seen one that are not finite
-  int last[N], first[N];
+  // this lane's columns (a bit each) of row `who` as it was written that are not finite
+  auto bad_of = [&](int who) {
+    const int64_t at = ((int64_t)__shfl_sync(~0u, t, who) * a.Hq + __shfl_sync(~0u, hq, who)) * D + lane * N;
+    const volatile float* part = p.part + (int64_t)split * a.Tq * a.Hq * D + at;
+    const volatile uint16_t* out = a.out + at;
+    unsigned bad = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) last[i] = -1, first[i] = end;
-#pragma unroll 4
-  for (int j = least; j < end; ++j) {
-    float v[N];
-    load_bf16(value + (int64_t)j * a.v_stride, v);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!(fabsf(v[i]) < -kNegInf)) last[i] = j;
-  }
+    for (int i = 0; i < N; ++i) {
+      const float y = p.splits > 1 ? part[i] : __uint_as_float((uint32_t)out[i] << 16);
+      if (!(fabsf(y) < -kNegInf)) bad |= 1u << i;
+    }
+    return bad;
+  };
+  unsigned all = 0, found = 0;
 #pragma unroll 1
-  for (int j0 = 0; j0 < most; j0 += 16) {
+  for (unsigned rest = again; rest; rest &= rest - 1) all |= bad_of(__ffs(rest) - 1);
+  int first[N];  // of this lane's columns: the first key that is not finite
+#pragma unroll
+  for (int i = 0; i < N; ++i) first[i] = end;
+#pragma unroll 1
+  for (int j0 = 0; j0 < most && __any_sync(~0u, all & ~found); j0 += 16) {
 #pragma unroll 4
     for (int j = j0; j < min(j0 + 16, most); ++j) {
       float v[N];
       load_bf16(value + (int64_t)j * a.v_stride, v);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (!(fabsf(v[i]) < -kNegInf)) first[i] = min(first[i], j);
+        if (!(fabsf(v[i]) < -kNegInf)) first[i] = min(first[i], j), found |= 1u << i;
     }
-    bool some = false, open = false;  // found one; a column that a hidden key spoils has none yet
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      some |= first[i] < end;
-      open |= first[i] == end && last[i] >= 0;
-    }
-    if (__any_sync(~0u, some) && !__any_sync(~0u, open)) break;
   }
   unsigned todo = 0;
 #pragma unroll 1
   for (; again; again &= again - 1) {
     const int who = __ffs(again) - 1, n = __shfl_sync(~0u, sees, who);
-    bool known = false, spoiled = false;
+    unsigned bad = bad_of(who);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      known |= first[i] < n;
-      spoiled |= first[i] >= n && last[i] >= n;
-    }
-    if (__any_sync(~0u, spoiled) || !__any_sync(~0u, known)) todo |= 1u << who;
+    for (int i = 0; i < N; ++i)
+      if (first[i] < n) bad &= ~(1u << i);
+    if (__any_sync(~0u, bad)) todo |= 1u << who;
   }
   attend_rows<D>(p, split, todo, t, hq, h, key0, key0 + sees);
 }
