@@ -541,7 +541,9 @@ PTQ_API size_t ptq_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t T
  * dtype: PTQ_BF16; PTQ_F32 is refused with PTQ_ERR_UNSUPPORTED (the fp32
  * route serves decode).  Probabilities enter the second product as bf16, the
  * type of the values: a relative 2^-9 of each, their sum is taken in fp32.
- * Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; Tq and Tk are
+ * The products' sums are fp32 and truncated, 16 keys a term: of 2^17 keys of like
+ * scores in one sequence they are off by up to 2^-10, of 2^20 by 2^-7
+ * (ptq_attn_chunk joins them every 2^15 keys).  Results are bitwise reproducible.  B = 0 or Tq = 0 is a no-op; Tq and Tk are
  * under 2^30, B under 2^26.  workspace as for ptq_attn_decode (NULL when ptq_attn_prefill_workspace_bytes is 0).
  * Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for unknown flags. */
 #define PTQ_ATTN_CAUSAL 1u
@@ -661,7 +663,8 @@ PTQ_API size_t ptq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t q_h
  * and their sum is taken in fp32.  Results are bitwise reproducible.  B = 0 or
  * Tq = 0 is a no-op; Tq is under 2^30, B under 2^26; more than 2^27 tokens that
  * could be seen (a table row's, or a window's and the first ones') are refused
- * with PTQ_ERR_UNSUPPORTED.
+ * with PTQ_ERR_UNSUPPORTED.  For chunks of prompts without a window over an int8
+ * cache ptq_kv_read and ptq_attn_prefill are faster, given room for the copy.
  * workspace as for ptq_attn_decode (NULL when ptq_attn_chunk_workspace_bytes is
  * 0).  Errors: as ptq_attn_decode, plus PTQ_ERR_VALUE for window and sinks. */
 PTQ_API PTQ_NODISCARD ptq_status ptq_attn_chunk(

@@ -848,7 +848,8 @@ def attn_chunk(q, cache, table, lens, cu_q, window=0, sinks=0, scale=None, out=N
     sequences one after the other; cu_q: their int32 offsets (one more than there
     are sequences); table and lens as for attn_decode.  A query sees its
     token and those before it; with `window` the last `window` of these and the
-    first `sinks`.  scale, out, lse and workspace as for attn_decode."""
+    first `sinks`.  scale, out, lse and workspace as for attn_decode.  (Chunks of
+    prompts without a window over an int8 cache are faster with kv_read and attn_prefill.)"""
     dt = _act_dtype(q)
     on = cache._on
     qp, qs = _heads(q, "q", q.dtype, on)

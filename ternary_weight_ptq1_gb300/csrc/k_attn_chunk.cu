@@ -15,26 +15,30 @@
 // Measured in CUDA graphs, causal: chunks of 1300 to 2048 tokens of three prompts over
 // up to 14,000 before them, 8 x 5 heads of 128, bf16 in 582 us (1340 TFLOP/s; with
 // nothing waited for between calls 624, under the power limit); 8192 tokens over
-// themselves in 518 (1330), through int8 in 810 (850), 4 x 6 of 256 in 705 (1170) and
-// 1226 (670), 4 x 7 of 64 in 330 (730) and 526 (460); 64 sequences' 1 to 5 new tokens over
+// themselves in 520 (1320), through int8 in 817 (840), 4 x 6 of 256 in 704 (1170) and
+// 1229 (670), 4 x 7 of 64 in 332 (725) and 530 (455); 64 sequences' 1 to 5 new tokens over
 // up to 8192, 8 x 8 of 128, over bf16 in 167 us (5.7 TB/s, 84% of the copy rate), over
-// int8 in 204 (2.4); 12 chunks of up to 900 under a window of 1024 + 4, 4 x 6 of 256,
-// int8 in 188; 4 tokens over 781 in 14.4.
+// int8 in 205 (2.4); 12 chunks of up to 900 under a window of 1024 + 4, 4 x 6 of 256,
+// int8 in 188; 4 tokens over 781 in 14.4.  Reading the rows back and the kernel of whole
+// prompts take 463 us for the first of those 8192, over int8 or bf16, 542 and 262 for the others.
 //
 // Keys.  The tokens that some query of a Q tile sees are counted through: the
 // first `sinks`, then those of the window, so first tokens share a tile of 128
 // keys with others and hidden ones cost nothing.  Four warps copy a tile's rows out of
 // the pages (cp.async, a lane finds the page of a row): any page size packs full
-// tiles, and rows that are not there are zeros.  (8192 tokens take 606 us with these
-// copies left out and 610 with them: the tensor memory accelerator, which wants
-// whole pieces of pages, would not be faster.)  Over int8 eight warps each copy codes
-// to a place of their own and spread them to bf16 for the products (times 2^-16), which is exact
-// (four take 286 us for 266 on the 64 sequences); a score is then multiplied by its
-// key's scale and a probability by its value's, in fp32, before P is rounded to bf16.
+// tiles, and rows that are not there are zeros.  (With zeros for every row, nothing read
+// from the pages, 8192 tokens take 510 us for 527, 4 x 7 of 64 326 for 332: what the
+// tensor memory accelerator, which wants whole pieces of pages, could save is within
+// that.)  Over int8 eight warps each copy codes to a place of their own and spread them
+// to bf16 for the products (times 2^-16), which is exact (four take 286 us for 266 on the
+// 64 sequences); a score is then multiplied by its key's scale and a probability by its
+// value's, in fp32, before P is rounded to bf16.
 //
 // Tile.  128 rows of Q are tpt tokens of hg query heads that share a kv head.  S, P
 // and O live in TMEM as in the kernel of whole prompts: P goes back over S as bf16
-// and is the A operand of the second product; the maximum that it refers to moves
+// and is the A operand of the second product (both operands have one type, and two
+// terms of P would add half to its work: 2^-9 of each weight, which takes an output's
+// error from its own rounding's 1.7e-3 to 2.3e-3); the maximum that it refers to moves
 // when a row's grows by more than 2^8.  A CTA works on two S at a time (head_dim up
 // to 128): of two Q tiles, neighbours in the sequence, that share each K and V
 // tile; or, where a sequence's queries fill one, of the one tile over every other
@@ -47,9 +51,9 @@
 // together.  The lengths are on the device: every CTA adds them up (in closed form
 // for a sequence) and one of its warps walks its stretch.  A run that is cut
 // leaves its sums, relative to their maxima, in the workspace, and a second kernel
-// joins them in order; a CTA joins those of its own part every 2^15 keys.  (A start of 128
-// keys: 64 sequences over int8 231 us, of 256 204, of 512 202, of 1024 217; three chunks 613, 597,
-// 590, 601.)
+// joins them in order; a CTA joins those of its own part every 2^15 keys.  (A start of
+// 128 keys: 64 sequences over int8 231 us, of 256 204, of 512 202, of 1024 217; three
+// chunks 613, 597, 590, 601.)
 //
 // What runs between two products is kept short: an issuing warp that works out its places
 // after its waits, or votes on each wait, takes 610 us for 518 at 8192 tokens.
@@ -57,7 +61,8 @@
 // A key that a row does not see has P = 0, and 0 times a non-finite value is NaN.
 // Over int8 a row is not finite by its scale: such scales enter as 0, and rows that
 // see one are made NaN.  Over bf16 rows whose sum is finite and whose output is not
-// are looked at, and computed again where no value that they see explains a dimension of it.
+// are looked at, and computed again where no value that they see explains a dimension
+// of it.
 //
 // Every wait is bounded, to some 6 s in which no warp computes rows again; one that
 // runs out raises the device status word and the CTA drains what it has in flight and

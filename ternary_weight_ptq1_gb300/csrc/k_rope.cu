@@ -26,8 +26,8 @@
 // of 24 + 4 of 256 into int8 and out again.)  More CTAs an SM, which leave fewer registers,
 // lost: 41 us with five of 128 threads, 46 with six.
 //
-// Measured in CUDA graphs: those 8192 tokens, norms, three axes, bf16 in 38 us (5.2 TB/s,
-// 77% of the copy rate), 43 into a bf16 cache with the values (5.4 TB/s); 5003 tokens of 28
+// Measured in CUDA graphs: those 8192 tokens, norms, three axes, bf16 in 39 us (5.2 TB/s,
+// 77% of the copy rate), 44 into a bf16 cache with the values (5.3 TB/s); 5003 tokens of 28
 // heads of 256, a quarter rotated, fp32 in 48 us (6.0 TB/s); 64 tokens of 48 heads in 3.4 us.
 #include <type_traits>
 
